@@ -300,6 +300,62 @@ int taco_decompress_reordered(taco_codec c, const void* in, int64_t rows, int64_
 int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, const void* w_bf16, int64_t N, void* out,
                          int32_t out_dtype, hipStream_t stream);
 
+/* ---- layers around the compressed all-reduce ------------------------------
+ * The rest of a tensor-parallel feed-forward sub-layer, forward and backward:
+ * the layer norm that reads a decoded sum (float32 or bf16, as taco_decompress
+ * and taco_decompress_reduce leave it), the projections whose partial sums
+ * taco_compress takes, and their gradients (the input gradient of a
+ * column-parallel projection is again such a partial sum).
+ *
+ * Matrices are row-major with a row stride of their own, so a slice of columns
+ * of a wider tensor can be given. `data` NULL: the array is absent, where a
+ * function says that it may be. Arrays need the alignment of their elements
+ * (not 16 bytes); rows that start on 16 bytes and hold a multiple of 8
+ * elements are read fastest. Vectors (weight, bias) have one row: their stride
+ * is not looked at.
+ * Errors, for every function here: TACO_ERR_FORMAT for an element type or an
+ * activation that it does not take; TACO_ERR_SHAPE for a stride below the
+ * number of columns or a size beyond what the function says;
+ * TACO_ERR_INVALID_ARG for sizes below zero, tensors above 2^35 elements, a
+ * missing array or an output that overlaps an input or another output;
+ * TACO_ERR_ALIGN; TACO_ERR_WORKSPACE for a workspace that is missing, smaller
+ * than the function's *_workspace_bytes or not 16-byte aligned. Workspaces are
+ * scratch: nothing is kept in them between calls, they need no clearing, and
+ * calls that may run at the same time need one each. Results do not depend on
+ * timing: the same call gives the same bits. Inputs may hold infinities and
+ * NaN; they follow the formulas and stay in the rows (or, for sums over rows,
+ * the columns) that they enter. The launch cap does not apply. */
+#define TACO_F32 0
+#define TACO_BF16 1
+
+typedef struct taco_array {
+  void* data;       /* device memory; inputs are never written */
+  int64_t stride;   /* elements from one row to the next, at least the columns */
+  int32_t dtype;    /* TACO_F32 or TACO_BF16 */
+  int32_t reserved; /* must be 0 */
+} taco_array;
+
+/* y = (x - mean) * rstd * weight + bias for each row of x [rows, cols], with
+ * mean = sum(x) / cols and rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps) in
+ * float32, y rounded once. cols at most TACO_NORM_MAX_COLS.
+ *   weight, bias   [cols], each may be absent (1 and 0)
+ *   mean, rstd     float32 [rows] for the backward pass, nullable */
+#define TACO_NORM_MAX_COLS 32768
+int taco_layer_norm(taco_array x, int64_t rows, int64_t cols, taco_array weight, taco_array bias, float eps,
+                    taco_array y, float* mean, float* rstd, hipStream_t stream);
+
+/* Gradients of taco_layer_norm from dy [rows, cols] and what the forward pass
+ * kept, with xhat = (x - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - sum(g) / cols - xhat * sum(g * xhat) / cols)
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * in float32, each rounded once. dx, dweight and dbias may each be absent (not
+ * all); the workspace is needed for dweight or dbias. rows == 0 clears dweight
+ * and dbias. */
+int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t cols, taco_array weight,
+                             const float* mean, const float* rstd, taco_array dx, taco_array dweight,
+                             taco_array dbias, void* workspace, size_t ws_bytes, hipStream_t stream);
+size_t taco_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
 /* Cap on the workgroups of every later launch made by the calling host
  * thread (0 = no cap, the default): lets the codec share the GPU with a
  * concurrent kernel, e.g. the GEMM that produces the next activation on

@@ -34,13 +34,18 @@ TACO_SCALE_DELAYED = -1.0
 TACO_MAX_SHARDS = 16
 TACO_WORKSPACE_BYTES = 32768
 
+TACO_F32 = 0
+TACO_BF16 = 1
+TACO_NORM_MAX_COLS = 32768
+
 # Entry points declared in include/taco.h (checked by the ABI tests).
 EXPORTS = (
     "taco_layout", "taco_compressed_bytes", "taco_workspace_bytes", "taco_compress",
     "taco_compress_debug", "taco_decompress_reduce", "taco_ring_hop", "taco_requantize", "taco_decompress",
     "taco_e4m3_encode", "taco_e5m2_encode", "taco_status_string", "taco_compress_noalloc",
     "taco_set_launch_limit", "taco_chunk_order", "taco_compress_reordered", "taco_decompress_reordered",
-    "taco_decompress_gemm",
+    "taco_decompress_gemm", "taco_layer_norm", "taco_layer_norm_backward",
+    "taco_layer_norm_backward_workspace_bytes",
 )
 
 
@@ -59,6 +64,11 @@ class taco_layout_t(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class taco_array(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def codec(fmt, block, hadamard=0):
@@ -81,7 +91,7 @@ def _load():
         _build.build()
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-    C = taco_codec
+    C, A = taco_codec, taco_array
     sig = {
         "taco_layout": (ctypes.c_int, [C, I64, I64, ctypes.POINTER(taco_layout_t)]),
         "taco_compressed_bytes": (I64, [C, I64, I64]),
@@ -101,6 +111,9 @@ def _load():
         "taco_compress_reordered": (ctypes.c_int, [C, P, I64, I64, F32, P, P, SZ, P, P]),
         "taco_decompress_reordered": (ctypes.c_int, [C, P, I64, I64, P, I32, P, P]),
         "taco_decompress_gemm": (ctypes.c_int, [C, P, I64, I64, P, I64, P, I32, P]),
+        "taco_layer_norm": (ctypes.c_int, [A, I64, I64, A, A, F32, A, P, P, P]),
+        "taco_layer_norm_backward": (ctypes.c_int, [A, A, I64, I64, A, P, P, A, A, A, P, SZ, P]),
+        "taco_layer_norm_backward_workspace_bytes": (SZ, [I64, I64]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -262,6 +275,82 @@ def taco_e4m3_encode(x, codes, n, stream=None):
 
 def taco_e5m2_encode(x, codes, n, stream=None):
     return _check(_lib.taco_e5m2_encode(_ptr(x), _ptr(codes), n, _stream(stream)), "taco_e5m2_encode")
+
+
+# ---------------------------------------------------------------- layers --
+# These take torch tensors: matrices [rows, cols] with unit column stride and
+# any row stride, vectors [n]; sizes, strides and element types come from them.
+
+_ABSENT = taco_array(None, 0, TACO_F32, 0)
+_DTYPES = {}   # torch dtype -> TACO_F32 / TACO_BF16, filled with torch's import
+
+
+def _dtype(t, what):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: TACO_F32, torch.bfloat16: TACO_BF16})
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what}: {t.dtype} is neither float32 nor bfloat16")
+    return dt
+
+
+def _matrix(t, rows, cols, what):
+    if t is None:
+        return _ABSENT
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
+    return taco_array(t.data_ptr(), stride, _dtype(t, what), 0)
+
+
+def _vector(t, n, what):
+    if t is None:
+        return _ABSENT
+    if t.shape != (n,):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n,)}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what}: must be contiguous")
+    return taco_array(t.data_ptr(), n, _dtype(t, what), 0)
+
+
+def _floats(t, n, what):
+    if t is None:
+        return None
+    if _vector(t, n, what).dtype != TACO_F32:
+        raise TypeError(f"{what}: must be float32")
+    return t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def taco_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * weight + bias by row of x [rows, cols]; weight and
+    bias [cols] or None; mean and rstd (float32 [rows]) are kept where given."""
+    rows, cols = x.shape
+    return _check(_lib.taco_layer_norm(_matrix(x, rows, cols, "x"), rows, cols, _vector(weight, cols, "weight"),
+                                       _vector(bias, cols, "bias"), eps, _matrix(y, rows, cols, "y"),
+                                       _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _stream(stream)),
+                  "taco_layer_norm")
+
+
+def taco_layer_norm_backward_workspace_bytes(rows, cols):
+    return _lib.taco_layer_norm_backward_workspace_bytes(rows, cols)
+
+
+def taco_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None,
+                             stream=None):
+    """Gradients of taco_layer_norm, each where its tensor is given."""
+    rows, cols = x.shape
+    return _check(_lib.taco_layer_norm_backward(
+        _matrix(dy, rows, cols, "dy"), _matrix(x, rows, cols, "x"), rows, cols, _vector(weight, cols, "weight"),
+        _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _matrix(dx, rows, cols, "dx"),
+        _vector(dweight, cols, "dweight"), _vector(dbias, cols, "dbias"), _ptr(workspace), _bytes(workspace),
+        _stream(stream)), "taco_layer_norm_backward")
 
 
 # ------------------------------------------------- buffer plumbing (torch) --

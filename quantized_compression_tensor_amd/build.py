@@ -17,10 +17,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
+LAYERS = os.path.join("..", "csrc_layers")   # the layers' sources, beside the codecs' (names relative to CSRC)
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtaco.so")
 
-SOURCES = ["taco_abi.hip", "fp8_hadamard.hip", "codecs.hip", "reorder.hip", "dequant_gemm.hip"]
+SOURCES = ["taco_abi.hip", "fp8_hadamard.hip", "codecs.hip", "reorder.hip", "dequant_gemm.hip",
+           *(os.path.join(LAYERS, f) for f in ("layers_abi.hip", "norm.hip"))]
 ARCH = "gfx950"
 
 # -ffp-contract=off: no fused multiply-adds except the explicit fmaf calls,
@@ -61,7 +63,7 @@ def build(verbose=False, extra_flags=(), out=None):
     os.makedirs(LIBDIR, exist_ok=True)
     with tempfile.TemporaryDirectory(dir=LIBDIR) as tmp:
         def compile_one(src):
-            obj = os.path.join(tmp, src.replace(".hip", ".o"))
+            obj = os.path.join(tmp, os.path.basename(src).replace(".hip", ".o"))
             _run([cc, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
             return obj
         with ThreadPoolExecutor(len(SOURCES)) as ex:

@@ -1,0 +1,95 @@
+"""The layers' entry points refuse bad arguments before anything is enqueued
+(none of these calls touches a GPU; the addresses are never read)."""
+
+import ctypes
+
+import pytest
+
+import quantized_compression_tensor_amd as T
+
+F, B = T.TACO_F32, T.TACO_BF16
+INVALID, SHAPE, FORMAT, ALIGN, WORKSPACE = (T.TACO_ERR_INVALID_ARG, T.TACO_ERR_SHAPE, T.TACO_ERR_FORMAT,
+                                            T.TACO_ERR_ALIGN, T.TACO_ERR_WORKSPACE)
+NONE = T.taco_array(None, 0, 0, 0)
+
+
+def at(i):
+    """Address number i: 1 GiB apart, so nothing overlaps by accident."""
+    return (i + 1) << 30
+
+
+def arr(i, stride, dtype=B, off=0, reserved=0):
+    return T.taco_array(at(i) + off, stride, dtype, reserved)
+
+
+def norm(rows=4, cols=64, x=None, w=None, b=None, eps=1e-5, y=None, mean=None, rstd=None):
+    return T.lib().taco_layer_norm(arr(0, 64) if x is None else x, rows, cols, NONE if w is None else w,
+                                   NONE if b is None else b, eps, arr(1, 64) if y is None else y, mean, rstd, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (T.TACO_OK, dict(rows=0)),
+    (T.TACO_OK, dict(rows=0, x=NONE, y=NONE)),
+    (INVALID, dict(rows=-1)), (INVALID, dict(cols=0)), (SHAPE, dict(cols=T.TACO_NORM_MAX_COLS + 1)),
+    (INVALID, dict(rows=1 << 40)), (INVALID, dict(rows=1 << 31, cols=1)),
+    (INVALID, dict(eps=-1.0)), (INVALID, dict(eps=float("nan"))), (INVALID, dict(eps=float("inf"))),
+    (INVALID, dict(x=NONE)), (INVALID, dict(y=NONE)),
+    (SHAPE, dict(x=arr(0, 63))), (SHAPE, dict(y=arr(1, 8))), (INVALID, dict(x=arr(0, 1 << 60))),
+    (FORMAT, dict(x=arr(0, 64, 2))), (FORMAT, dict(w=arr(2, 64, -1))), (INVALID, dict(y=arr(1, 64, reserved=1))),
+    (ALIGN, dict(x=arr(0, 64, B, 1))), (ALIGN, dict(y=arr(1, 64, F, 2))), (ALIGN, dict(mean=at(3) + 2)),
+    (INVALID, dict(y=arr(0, 64))), (INVALID, dict(y=arr(0, 64, B, 4 * 64 * 2 - 2))),
+    (INVALID, dict(b=arr(1, 64, F, 64))), (INVALID, dict(mean=at(1) + 16)), (INVALID, dict(mean=at(3), rstd=at(3) + 12)),
+])
+def test_layer_norm_refusals(want, kw):
+    assert norm(**kw) == want
+
+
+def norm_back(rows=4, cols=64, dy=None, x=None, w=None, mean=at(2), rstd=at(3), dx=None, dw=None, db=None,
+              ws=at(7), ws_bytes=1 << 20):
+    return T.lib().taco_layer_norm_backward(
+        arr(0, 64) if dy is None else dy, arr(1, 64) if x is None else x, rows, cols, NONE if w is None else w,
+        mean, rstd, arr(4, 64) if dx is None else dx, arr(5, 64, F) if dw is None else dw,
+        arr(6, 64, F) if db is None else db, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (T.TACO_OK, dict(rows=0, dw=NONE, db=NONE)),
+    (INVALID, dict(rows=-1)), (INVALID, dict(cols=0)), (SHAPE, dict(cols=T.TACO_NORM_MAX_COLS + 1)),
+    (INVALID, dict(dy=NONE)), (INVALID, dict(x=NONE)), (INVALID, dict(mean=None)), (INVALID, dict(rstd=None)),
+    (INVALID, dict(dx=NONE, dw=NONE, db=NONE)),
+    (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=2 * 64 * 4 - 1)), (WORKSPACE, dict(ws=at(7) + 8)),
+    (SHAPE, dict(dx=arr(4, 63))), (FORMAT, dict(dw=arr(5, 64, 7))), (ALIGN, dict(db=arr(6, 64, F, 1))),
+    (INVALID, dict(dx=arr(0, 64))), (INVALID, dict(dw=arr(6, 64, F))), (INVALID, dict(dw=arr(7, 64, F))),
+    (INVALID, dict(dx=arr(7, 64))),
+])
+def test_layer_norm_backward_refusals(want, kw):
+    assert norm_back(**kw) == want
+
+
+def test_norm_workspace():
+    size = T.taco_layer_norm_backward_workspace_bytes
+    assert size(0, 64) == 0 and size(-1, 64) == 0 and size(4, 0) == 0 and size(4, T.TACO_NORM_MAX_COLS + 1) == 0
+    assert size(1, 64) == 2 * 64 * 4                 # one workgroup takes 16 rows of 64
+    assert size(4, 1000) == 4 * 2 * 1000 * 4
+    assert size(1 << 20, 5120) == 512 * 2 * 5120 * 4  # and never more than 512 workgroups
+
+
+def test_binding_refuses_other_tensors():
+    import torch
+    x = torch.zeros(4, 8)
+    v = torch.zeros(8)
+    with pytest.raises(TypeError):
+        T.taco_layer_norm(x.double(), None, None, 1e-5, x)
+    with pytest.raises(TypeError):
+        T.taco_layer_norm(x, None, None, 1e-5, x, mean=torch.zeros(4, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        T.taco_layer_norm(x, torch.zeros(7), None, 1e-5, x)
+    with pytest.raises(ValueError):
+        T.taco_layer_norm(x, None, v[::2].expand(4), 1e-5, x)
+    with pytest.raises(ValueError):
+        T.taco_layer_norm(x, None, None, 1e-5, torch.zeros(8, 4).t())
+    with pytest.raises(ValueError):
+        T.taco_layer_norm(x, None, None, 1e-5, torch.zeros(4, 9))
+    with pytest.raises(T.TacoError):
+        T.taco_layer_norm(x, None, None, 1e-5, x)     # the output is the input
+    assert ctypes.sizeof(T.taco_array) == 24
