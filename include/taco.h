@@ -340,7 +340,7 @@ typedef struct taco_array {
  * float32, y rounded once. cols at most TACO_NORM_MAX_COLS.
  *   weight, bias   [cols], each may be absent (1 and 0)
  *   mean, rstd     float32 [rows] for the backward pass, nullable */
-#define TACO_NORM_MAX_COLS 32768
+#define TACO_NORM_MAX_COLS 16384
 int taco_layer_norm(taco_array x, int64_t rows, int64_t cols, taco_array weight, taco_array bias, float eps,
                     taco_array y, float* mean, float* rstd, hipStream_t stream);
 
@@ -355,6 +355,62 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
                              const float* mean, const float* rstd, taco_array dx, taco_array dweight,
                              taco_array dbias, void* workspace, size_t ws_bytes, hipStream_t stream);
 size_t taco_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Activations of the projections: none, t Phi(t) with the normal distribution's
+ * Phi (the error function's form), t / (1 + exp(-t)), max(t, 0). */
+#define TACO_ACT_NONE 0
+#define TACO_ACT_GELU 1
+#define TACO_ACT_SILU 2
+#define TACO_ACT_RELU 3
+
+/* A linear layer with its epilogue, in one pass over the output:
+ *   z = x W^T + bias,  out = act(z) + residual
+ * x bf16 [M, K], w bf16 [N, K] (a linear layer's weight); products summed in
+ * float32 on the matrix cores, the epilogue in float32, each output rounded
+ * once. N, K at most TACO_LINEAR_MAX_DIM, M below 2^31 and strides of x and w
+ * at most TACO_LINEAR_MAX_STRIDE.
+ *   bias      [N], may be absent
+ *   residual  [M, N], may be absent
+ *   preact    [M, N] receives z for the backward pass, may be absent
+ * M may be 0 (nothing enqueued). */
+#define TACO_LINEAR_MAX_DIM (1 << 20)
+#define TACO_LINEAR_MAX_STRIDE (1 << 21)
+int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_array residual, taco_array out,
+                taco_array preact, int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                hipStream_t stream);
+size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Gradients of taco_linear from dout [M, N] (bf16) and the forward pass's
+ * preact [M, N] (needed unless act is NONE):
+ *   dz = dout * act'(preact),  dx = dz W [M, K],  dw = dz^T x [N, K],
+ *   dbias = sum over rows of dz
+ * (the residual's gradient is dout itself). Where there is an activation, dz
+ * is rounded to bf16 once, as an operand of the matrix cores; dbias sums it
+ * unrounded. dx, dw and dbias may each be absent (not all). M == 0 clears dw
+ * and dbias. */
+int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
+                         taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
+                         size_t ws_bytes, hipStream_t stream);
+size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* The gated projections of a feed-forward layer, with activation and product,
+ * in one kernel: w bf16 [2 F, K] holds the gate's rows and then the other
+ * projection's,
+ *   z = x W^T [M, 2 F],  out = act(z[:, :F]) * z[:, F:]  [M, F]
+ * with the limits and types of taco_linear (2 F in place of N).
+ *   preact    [M, 2 F] receives z for the backward pass, may be absent */
+int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, taco_array preact, int64_t M,
+                      int64_t F, int64_t K, void* workspace, size_t ws_bytes, hipStream_t stream);
+size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
+
+/* Gradients of taco_gated_linear from dout [M, F] (bf16) and its preact:
+ *   dz = [dout * z[:, F:] * act'(z[:, :F]), dout * act(z[:, :F])], rounded to
+ *   bf16 once,  dx = dz W [M, K],  dw = dz^T x [2 F, K]
+ * dx and dw may each be absent (not both). M == 0 clears dw. */
+int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
+                               taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,
+                               size_t ws_bytes, hipStream_t stream);
+size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /* Cap on the workgroups of every later launch made by the calling host
  * thread (0 = no cap, the default): lets the codec share the GPU with a

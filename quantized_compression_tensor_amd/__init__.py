@@ -36,7 +36,13 @@ TACO_WORKSPACE_BYTES = 32768
 
 TACO_F32 = 0
 TACO_BF16 = 1
-TACO_NORM_MAX_COLS = 32768
+TACO_NORM_MAX_COLS = 16384
+TACO_ACT_NONE = 0
+TACO_ACT_GELU = 1
+TACO_ACT_SILU = 2
+TACO_ACT_RELU = 3
+TACO_LINEAR_MAX_DIM = 1 << 20
+TACO_LINEAR_MAX_STRIDE = 1 << 21
 
 # Entry points declared in include/taco.h (checked by the ABI tests).
 EXPORTS = (
@@ -45,7 +51,9 @@ EXPORTS = (
     "taco_e4m3_encode", "taco_e5m2_encode", "taco_status_string", "taco_compress_noalloc",
     "taco_set_launch_limit", "taco_chunk_order", "taco_compress_reordered", "taco_decompress_reordered",
     "taco_decompress_gemm", "taco_layer_norm", "taco_layer_norm_backward",
-    "taco_layer_norm_backward_workspace_bytes",
+    "taco_layer_norm_backward_workspace_bytes", "taco_linear", "taco_linear_workspace_bytes", "taco_linear_backward",
+    "taco_linear_backward_workspace_bytes", "taco_gated_linear", "taco_gated_linear_workspace_bytes",
+    "taco_gated_linear_backward", "taco_gated_linear_backward_workspace_bytes",
 )
 
 
@@ -114,6 +122,12 @@ def _load():
         "taco_layer_norm": (ctypes.c_int, [A, I64, I64, A, A, F32, A, P, P, P]),
         "taco_layer_norm_backward": (ctypes.c_int, [A, A, I64, I64, A, P, P, A, A, A, P, SZ, P]),
         "taco_layer_norm_backward_workspace_bytes": (SZ, [I64, I64]),
+        "taco_linear": (ctypes.c_int, [A, A, A, I32, A, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_linear_backward": (ctypes.c_int, [A, A, A, I32, A, A, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_gated_linear": (ctypes.c_int, [A, A, I32, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_gated_linear_backward": (ctypes.c_int, [A, A, A, I32, A, A, A, I64, I64, I64, P, SZ, P]),
+        **{f"taco_{n}_workspace_bytes": (SZ, [I64, I64, I64])
+           for n in ("linear", "linear_backward", "gated_linear", "gated_linear_backward")},
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -351,6 +365,63 @@ def taco_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, d
         _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _matrix(dx, rows, cols, "dx"),
         _vector(dweight, cols, "dweight"), _vector(dbias, cols, "dbias"), _ptr(workspace), _bytes(workspace),
         _stream(stream)), "taco_layer_norm_backward")
+
+
+def taco_linear_workspace_bytes(M, N, K):
+    return _lib.taco_linear_workspace_bytes(M, N, K)
+
+
+def taco_linear(x, w, out, bias=None, act=TACO_ACT_NONE, residual=None, preact=None, workspace=None, stream=None):
+    """out = act(x w^T + bias) + residual; x bf16 [M, K], w bf16 [N, K]; preact,
+    where given, receives x w^T + bias."""
+    (M, K), N = x.shape, w.shape[0]
+    return _check(_lib.taco_linear(
+        _matrix(x, M, K, "x"), _matrix(w, N, K, "w"), _vector(bias, N, "bias"), act,
+        _matrix(residual, M, N, "residual"), _matrix(out, M, N, "out"), _matrix(preact, M, N, "preact"), M, N, K,
+        _ptr(workspace), _bytes(workspace), _stream(stream)), "taco_linear")
+
+
+def taco_linear_backward_workspace_bytes(M, N, K):
+    return _lib.taco_linear_backward_workspace_bytes(M, N, K)
+
+
+def taco_linear_backward(dout, x, w, act=TACO_ACT_NONE, preact=None, dx=None, dw=None, dbias=None, workspace=None,
+                         stream=None):
+    """Gradients of taco_linear, each where its tensor is given."""
+    (M, K), N = x.shape, w.shape[0]
+    return _check(_lib.taco_linear_backward(
+        _matrix(dout, M, N, "dout"), _matrix(x, M, K, "x"), _matrix(w, N, K, "w"), act,
+        _matrix(preact, M, N, "preact"), _matrix(dx, M, K, "dx"), _matrix(dw, N, K, "dw"),
+        _vector(dbias, N, "dbias"), M, N, K, _ptr(workspace), _bytes(workspace), _stream(stream)),
+        "taco_linear_backward")
+
+
+def taco_gated_linear_workspace_bytes(M, F, K):
+    return _lib.taco_gated_linear_workspace_bytes(M, F, K)
+
+
+def taco_gated_linear(x, w, out, act=TACO_ACT_SILU, preact=None, workspace=None, stream=None):
+    """out = act(z[:, :F]) * z[:, F:] with z = x w^T; w bf16 [2 F, K], the gate's
+    rows first; preact, where given, receives z."""
+    (M, K), F = x.shape, w.shape[0] // 2
+    return _check(_lib.taco_gated_linear(
+        _matrix(x, M, K, "x"), _matrix(w, 2 * F, K, "w"), act, _matrix(out, M, F, "out"),
+        _matrix(preact, M, 2 * F, "preact"), M, F, K, _ptr(workspace), _bytes(workspace), _stream(stream)),
+        "taco_gated_linear")
+
+
+def taco_gated_linear_backward_workspace_bytes(M, F, K):
+    return _lib.taco_gated_linear_backward_workspace_bytes(M, F, K)
+
+
+def taco_gated_linear_backward(dout, x, w, act=TACO_ACT_SILU, preact=None, dx=None, dw=None, workspace=None,
+                               stream=None):
+    """Gradients of taco_gated_linear, each where its tensor is given."""
+    (M, K), F = x.shape, w.shape[0] // 2
+    return _check(_lib.taco_gated_linear_backward(
+        _matrix(dout, M, F, "dout"), _matrix(x, M, K, "x"), _matrix(w, 2 * F, K, "w"), act,
+        _matrix(preact, M, 2 * F, "preact"), _matrix(dx, M, K, "dx"), _matrix(dw, 2 * F, K, "dw"), M, F, K,
+        _ptr(workspace), _bytes(workspace), _stream(stream)), "taco_gated_linear_backward")
 
 
 # ------------------------------------------------- buffer plumbing (torch) --

@@ -22,7 +22,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtaco.so")
 
 SOURCES = ["taco_abi.hip", "fp8_hadamard.hip", "codecs.hip", "reorder.hip", "dequant_gemm.hip",
-           *(os.path.join(LAYERS, f) for f in ("layers_abi.hip", "norm.hip"))]
+           *(os.path.join(LAYERS, f) for f in ("layers_abi.hip", "norm.hip", "linear.hip"))]
 ARCH = "gfx950"
 
 # -ffp-contract=off: no fused multiply-adds except the explicit fmaf calls,

@@ -84,6 +84,80 @@ int check_norm_sizes(int64_t rows, int64_t cols) {
   return TACO_OK;
 }
 
+// Sizes of a projection with `n` output columns and `wide` weight rows.
+int check_linear_sizes(int64_t m, int64_t n, int64_t wide, int64_t k) {
+  if (m < 0 || n <= 0 || k <= 0) return TACO_ERR_INVALID_ARG;
+  if (n > TACO_LINEAR_MAX_DIM || wide > TACO_LINEAR_MAX_DIM || k > TACO_LINEAR_MAX_DIM) return TACO_ERR_SHAPE;
+  if (m > (int64_t(1) << 30) || wide * k > kMaxElems || m > kMaxElems / wide || m > kMaxElems / k)
+    return TACO_ERR_INVALID_ARG;
+  return TACO_OK;
+}
+
+// An operand of the matrix cores.
+Checked check_operand(const taco_array& a, int64_t rows, int64_t cols) {
+  Checked c = check_array(a, rows, cols, kRequired, kBf16Only);
+  if (c.status == TACO_OK && c.m.ld > TACO_LINEAR_MAX_STRIDE) c.status = TACO_ERR_SHAPE;
+  return c;
+}
+
+int check_act(int32_t act) { return act >= TACO_ACT_NONE && act <= TACO_ACT_RELU ? TACO_OK : TACO_ERR_FORMAT; }
+
+Operand operand(const Checked& c, bool by_k) { return Operand{static_cast<const uint16_t*>(c.m.p), c.m.ld, by_k}; }
+
+constexpr Mat kAbsent = {nullptr, 0, TACO_F32};
+
+// The workspace of a backward pass: dz as bf16 [m, wide] with rows on 16
+// bytes, then the partial column sums for dbias [groups][n].
+struct BackwardSpace {
+  int64_t ld_dz;
+  size_t dz_bytes, sums_bytes;
+  BackwardSpace(int64_t m, int64_t wide, int64_t n)
+      : ld_dz((wide + 7) / 8 * 8),
+        dz_bytes(((size_t)(m * ld_dz) * 2 + 255) / 256 * 256),
+        sums_bytes((size_t)act_back_groups(m) * (size_t)n * 4) {}
+  size_t total() const { return dz_bytes + sums_bytes; }
+};
+
+// Forward pass of either kind of projection; `wide`: rows of w.
+int linear_forward(const Checked& cx, const Checked& cw, const Epilogue& e, bool gated, int64_t m, int64_t n,
+                   int64_t k, hipStream_t stream) {
+  GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e};
+  clear_stale_error();
+  return hip_status(launch_gemm(g, stream));
+}
+
+// Backward pass of either kind: dz, then dx = dz W and dw = dz^T x.
+int linear_backward(const Checked& cdout, const Checked& cx, const Checked& cw, int act, const Checked& cz,
+                    const Checked& cdx, const Checked& cdw, const Checked& cdb, bool gated, int64_t m, int64_t n,
+                    int64_t k, void* ws, hipStream_t stream) {
+  const int64_t wide = gated ? 2 * n : n;
+  const BackwardSpace space(m, wide, n);
+  Operand dz = operand(cdout, false);
+  clear_stale_error();
+  if (gated || act != TACO_ACT_NONE || cdb.m.p) {
+    ActBackArgs b = {cdout.m, cz.m, m, (int)n, act, gated, nullptr, space.ld_dz, nullptr, cdb.m};
+    if (gated || act != TACO_ACT_NONE) {
+      b.dz = static_cast<uint16_t*>(ws);
+      dz = Operand{b.dz, space.ld_dz, false};
+    }
+    if (cdb.m.p) b.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + space.dz_bytes);
+    const hipError_t err = launch_act_back(b, stream);
+    if (err != hipSuccess) return TACO_ERR_HIP;
+  }
+  if (cdx.m.p && m > 0) {
+    const GemmArgs g = {dz, operand(cw, true), m, (int)k, wide, false, {kAbsent, kAbsent, kAbsent, cdx.m, kActNone}};
+    const hipError_t err = launch_gemm(g, stream);
+    if (err != hipSuccess) return TACO_ERR_HIP;
+  }
+  if (cdw.m.p) {
+    dz.by_k = true;
+    const GemmArgs g = {dz, operand(cx, true), wide, (int)k, m, false, {kAbsent, kAbsent, kAbsent, cdw.m, kActNone}};
+    const hipError_t err = launch_gemm(g, stream);
+    if (err != hipSuccess) return TACO_ERR_HIP;
+  }
+  return TACO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,6 +207,102 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
                           static_cast<float*>(cws.m.p)};
   clear_stale_error();
   return hip_status(launch_norm_back(a, stream));
+}
+
+size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  (void)M;
+  (void)N;
+  (void)K;
+  return 0;
+}
+
+int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_array residual, taco_array out,
+                taco_array preact, int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                hipStream_t stream) {
+  int st = check_linear_sizes(M, N, N, K);
+  if (st != TACO_OK) return st;
+  st = check_act(act);
+  if (st != TACO_OK) return st;
+  const Checked cx = check_operand(x, M, K), cw = check_operand(w, N, K), cb = check_vector(bias, N, kOptional);
+  const Checked cr = check_array(residual, M, N, kOptional), co = check_array(out, M, N, kRequired);
+  const Checked cz = check_array(preact, M, N, kOptional);
+  const Checked cws = check_workspace(workspace, ws_bytes, taco_linear_workspace_bytes(M, N, K));
+  st = first_error({&cx, &cw, &cb, &cr, &co, &cz, &cws});
+  if (st != TACO_OK) return st;
+  if (any_overlap({&cx, &cw, &cb, &cr}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
+  if (M == 0) return TACO_OK;
+  return linear_forward(cx, cw, {cb.m, cr.m, cz.m, co.m, act}, false, M, N, K, stream);
+}
+
+size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+  (void)M;
+  (void)F;
+  (void)K;
+  return 0;
+}
+
+int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, taco_array preact, int64_t M,
+                      int64_t F, int64_t K, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  int st = check_linear_sizes(M, F, 2 * F, K);
+  if (st != TACO_OK) return st;
+  st = check_act(act);
+  if (st != TACO_OK) return st;
+  const Checked cx = check_operand(x, M, K), cw = check_operand(w, 2 * F, K);
+  const Checked co = check_array(out, M, F, kRequired), cz = check_array(preact, M, 2 * F, kOptional);
+  const Checked cws = check_workspace(workspace, ws_bytes, taco_gated_linear_workspace_bytes(M, F, K));
+  st = first_error({&cx, &cw, &co, &cz, &cws});
+  if (st != TACO_OK) return st;
+  if (any_overlap({&cx, &cw}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
+  if (M == 0) return TACO_OK;
+  return linear_forward(cx, cw, {kAbsent, kAbsent, cz.m, co.m, act}, true, M, F, K, stream);
+}
+
+size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_linear_sizes(M, N, N, K) != TACO_OK) return 0;
+  return BackwardSpace(M, N, N).total();
+}
+
+int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
+                         taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
+                         size_t ws_bytes, hipStream_t stream) {
+  int st = check_linear_sizes(M, N, N, K);
+  if (st != TACO_OK) return st;
+  st = check_act(act);
+  if (st != TACO_OK) return st;
+  const Checked cd = check_operand(dout, M, N), cx = check_operand(x, M, K), cw = check_operand(w, N, K);
+  const Checked cz = check_array(preact, M, N, act == TACO_ACT_NONE ? kOptional : kRequired);
+  const Checked cdx = check_array(dx, M, K, kOptional), cdw = check_array(dw, N, K, kOptional);
+  const Checked cdb = check_vector(dbias, N, kOptional);
+  const Checked cws = check_workspace(workspace, ws_bytes, taco_linear_backward_workspace_bytes(M, N, K));
+  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cdb, &cws});
+  if (st != TACO_OK) return st;
+  if (!dx.data && !dw.data && !dbias.data) return TACO_ERR_INVALID_ARG;
+  if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cdb, &cws})) return TACO_ERR_INVALID_ARG;
+  return linear_backward(cd, cx, cw, act, cz, cdx, cdw, cdb, false, M, N, K, workspace, stream);
+}
+
+size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
+  if (check_linear_sizes(M, F, 2 * F, K) != TACO_OK) return 0;
+  return BackwardSpace(M, 2 * F, 0).total();
+}
+
+int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
+                               taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,
+                               size_t ws_bytes, hipStream_t stream) {
+  int st = check_linear_sizes(M, F, 2 * F, K);
+  if (st != TACO_OK) return st;
+  st = check_act(act);
+  if (st != TACO_OK) return st;
+  const Checked cd = check_operand(dout, M, F), cx = check_operand(x, M, K), cw = check_operand(w, 2 * F, K);
+  const Checked cz = check_array(preact, M, 2 * F, kRequired);
+  const Checked cdx = check_array(dx, M, K, kOptional), cdw = check_array(dw, 2 * F, K, kOptional);
+  const Checked cws = check_workspace(workspace, ws_bytes, taco_gated_linear_backward_workspace_bytes(M, F, K));
+  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cws});
+  if (st != TACO_OK) return st;
+  if (!dx.data && !dw.data) return TACO_ERR_INVALID_ARG;
+  if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cws})) return TACO_ERR_INVALID_ARG;
+  const Checked none = {kAbsent, 0, TACO_OK};
+  return linear_backward(cd, cx, cw, act, cz, cdx, cdw, none, true, M, F, K, workspace, stream);
 }
 
 }  // extern "C"

@@ -37,8 +37,57 @@ struct NormBackArgs {
   float* partials;      // [groups][2][cols]
 };
 
+enum Act : int { kActNone = 0, kActGelu = 1, kActSilu = 2, kActRelu = 3 };
+
+// What becomes of the sums z[m, n] of a matrix product.
+struct Epilogue {
+  Mat bias;       // [N], may be absent
+  Mat residual;   // [M, N], may be absent
+  Mat preact;     // receives z (+ bias), may be absent
+  Mat out;
+  int act;
+};
+
+// One operand of a matrix product, bf16: element (i, k) of its [rows, K] view
+// is p[i * ld + k], or p[k * ld + i] if `by_k` (rows contiguous).
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;
+  bool by_k;
+};
+
+// z[M, N] = a b^T over K, then the epilogue. With `gated`, N counts the output
+// columns, b has 2 N rows (the gate's first) and the epilogue is
+// out = act(z[:, :N]) * z[:, N:], preact [M, 2 N].
+struct GemmArgs {
+  Operand a, b;
+  int64_t M;
+  int N;
+  int64_t K;
+  bool gated;
+  Epilogue e;
+};
+
+// dz = dout * act'(z) (gated: both halves), and the column sums of dz.
+struct ActBackArgs {
+  Mat dout, z;          // [M, N], [M, N or 2 N]
+  int64_t M;
+  int N;
+  int act;
+  bool gated;
+  uint16_t* dz;         // bf16 [M, ld_dz], null: not wanted
+  int64_t ld_dz;
+  float* partials;      // [act_back_groups][N], null: no column sums
+  Mat dbias;
+};
+int act_back_groups(int64_t M);
+
 int norm_back_groups(int64_t rows, int64_t cols);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_back(const NormBackArgs& a, hipStream_t s);
+hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
+hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s);
+// out [cols] = the sum of `count` rows of `in`, ld apart (zeros if count is 0).
+void launch_column_sum(const float* in, int64_t ld, int count, int64_t cols, const Mat& out, hipStream_t s);
 
 }  // namespace taco

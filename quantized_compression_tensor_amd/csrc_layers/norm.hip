@@ -13,7 +13,7 @@
 //
 // Rows of up to 512 elements take 16, 32 or 64 lanes of one wave, so that
 // their sums need no barrier and no lane is idle for long; wider rows take a
-// workgroup, with one step up to 8192 elements and up to four beyond.
+// workgroup, with one step up to 8192 elements and two beyond.
 #include "layers_device.h"
 #include "layers_internal.h"
 
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kNormThreads) void k_column_sum(ColumnSumArgs a) {
     store1(a.out.p, a.out.dt, c, (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]));
 }
 
-static void column_sum(const float* in, int64_t ld, int count, int64_t cols, const Mat& out, hipStream_t s) {
+void launch_column_sum(const float* in, int64_t ld, int count, int64_t cols, const Mat& out, hipStream_t s) {
   if (out.p == nullptr) return;
   const ColumnSumArgs a = {in, ld, count, (int)cols, out};
   hipLaunchKernelGGL(k_column_sum, dim3((unsigned)((cols + kWave - 1) / kWave)), dim3(kNormThreads), 0, s, a);
@@ -278,7 +278,7 @@ static void column_sum(const float* in, int64_t ld, int count, int64_t cols, con
 
 // Threads of a workgroup that holds one row: one step of eight elements each
 // where 1024 are enough.
-static int wide_steps(int cols) { return cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4; }
+static int wide_steps(int cols) { return cols <= 8192 ? 1 : 2; }
 static int wide_threads(int cols) {
   const int per = 8 * wide_steps(cols);
   return ((cols + per - 1) / per + kWave - 1) / kWave * kWave;
@@ -296,11 +296,8 @@ static void for_shape(int cols, F f) {
     case 64: return f(integral_constant<int, 64>(), std::false_type(), integral_constant<int, 1>());
     default: break;
   }
-  switch (wide_steps(cols)) {
-    case 1: return f(integral_constant<int, 64>(), std::true_type(), integral_constant<int, 1>());
-    case 2: return f(integral_constant<int, 64>(), std::true_type(), integral_constant<int, 2>());
-    default: return f(integral_constant<int, 64>(), std::true_type(), integral_constant<int, 4>());
-  }
+  if (wide_steps(cols) == 1) f(integral_constant<int, 64>(), std::true_type(), integral_constant<int, 1>());
+  else f(integral_constant<int, 64>(), std::true_type(), integral_constant<int, 2>());
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
@@ -362,8 +359,8 @@ hipError_t launch_norm_back(const NormBackArgs& a, hipStream_t s) {
   }
   if (!sums) return hipGetLastError();
   const int64_t ld = 2 * (int64_t)a.cols;
-  column_sum(a.partials, ld, groups, a.cols, a.dweight, s);
-  column_sum(groups ? a.partials + a.cols : nullptr, ld, groups, a.cols, a.dbias, s);
+  launch_column_sum(a.partials, ld, groups, a.cols, a.dweight, s);
+  launch_column_sum(groups ? a.partials + a.cols : nullptr, ld, groups, a.cols, a.dbias, s);
   return hipGetLastError();
 }
 

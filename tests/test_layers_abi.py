@@ -93,3 +93,74 @@ def test_binding_refuses_other_tensors():
     with pytest.raises(T.TacoError):
         T.taco_layer_norm(x, None, None, 1e-5, x)     # the output is the input
     assert ctypes.sizeof(T.taco_array) == 24
+
+
+def linear(M=4, N=16, K=24, x=None, w=None, bias=None, act=0, residual=None, out=None, preact=None, ws=at(9),
+           ws_bytes=1 << 28):
+    return T.lib().taco_linear(arr(0, 24) if x is None else x, arr(1, 24) if w is None else w, bias or NONE, act,
+                               residual or NONE, arr(2, 16) if out is None else out, preact or NONE, M, N, K, ws,
+                               ws_bytes, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (T.TACO_OK, dict(M=0)), (T.TACO_OK, dict(M=0, x=NONE, out=NONE)),
+    (INVALID, dict(M=-1)), (INVALID, dict(N=0)), (INVALID, dict(K=0)), (INVALID, dict(M=(1 << 30) + 1, N=1, K=1)),
+    (SHAPE, dict(N=T.TACO_LINEAR_MAX_DIM + 1)), (SHAPE, dict(K=T.TACO_LINEAR_MAX_DIM + 1)),
+    (INVALID, dict(M=1 << 29, N=1 << 10)),
+    (FORMAT, dict(act=4)), (FORMAT, dict(act=-1)), (FORMAT, dict(x=arr(0, 24, F))), (FORMAT, dict(w=arr(1, 24, F))),
+    (FORMAT, dict(out=arr(2, 16, 2))), (SHAPE, dict(x=arr(0, 23))), (SHAPE, dict(w=arr(1, 8))),
+    (SHAPE, dict(out=arr(2, 15))), (SHAPE, dict(x=arr(0, T.TACO_LINEAR_MAX_STRIDE + 1))),
+    (INVALID, dict(x=NONE)), (INVALID, dict(w=NONE)), (INVALID, dict(out=NONE)), (ALIGN, dict(x=arr(0, 24, B, 1))),
+    (ALIGN, dict(bias=arr(3, 16, F, 2))), (INVALID, dict(residual=arr(3, 16, B, 0, 1))),
+    (INVALID, dict(out=arr(0, 24))), (INVALID, dict(out=arr(3, 16), residual=arr(3, 16))),
+    (INVALID, dict(preact=arr(2, 16))), (INVALID, dict(preact=arr(1, 24))),
+])
+def test_linear_refusals(want, kw):
+    assert linear(**kw) == want
+
+
+def linear_back(gated=False, M=4, N=16, K=24, d=None, x=None, w=None, act=1, z=None, dx=None, dw=None, db=None,
+                ws=at(9), ws_bytes=1 << 28):
+    f = T.lib().taco_gated_linear_backward if gated else T.lib().taco_linear_backward
+    wide = 32 if gated else 16
+    return f(arr(0, 16) if d is None else d, arr(1, 24) if x is None else x, arr(2, 24) if w is None else w, act,
+             arr(3, wide) if z is None else z, arr(4, 24) if dx is None else dx, arr(5, 24, F) if dw is None else dw,
+             *(() if gated else (arr(6, 16, F) if db is None else db,)), M, N, K, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(M=-1)), (INVALID, dict(N=0)), (INVALID, dict(K=0)), (SHAPE, dict(N=T.TACO_LINEAR_MAX_DIM + 1)),
+    (FORMAT, dict(act=9)), (FORMAT, dict(d=arr(0, 16, F))), (INVALID, dict(d=NONE)), (INVALID, dict(x=NONE)),
+    (INVALID, dict(w=NONE)), (INVALID, dict(z=NONE)), (SHAPE, dict(z=arr(3, 8))), (SHAPE, dict(dx=arr(4, 23))),
+    (FORMAT, dict(dw=arr(5, 24, 5))), (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100)),
+    (WORKSPACE, dict(ws=at(9) + 4)), (INVALID, dict(dx=arr(1, 24))), (INVALID, dict(dw=arr(4, 24, F))),
+    (INVALID, dict(dx=arr(9, 24))),
+])
+def test_projection_backward_refusals(gated, want, kw):
+    assert linear_back(gated, **kw) == want
+
+
+def test_projection_backward_wants_an_output():
+    assert linear_back(dx=NONE, dw=NONE, db=NONE) == INVALID
+    assert linear_back(True, dx=NONE, dw=NONE) == INVALID
+
+
+def gated(M=4, N=16, K=24, x=None, w=None, act=2, out=None, preact=None):
+    return T.lib().taco_gated_linear(arr(0, 24) if x is None else x, arr(1, 24) if w is None else w, act,
+                                     arr(2, 16) if out is None else out, preact or NONE, M, N, K, at(9), 1 << 28, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (T.TACO_OK, dict(M=0)), (INVALID, dict(M=-1)), (INVALID, dict(N=0)), (SHAPE, dict(N=T.TACO_LINEAR_MAX_DIM // 2 + 1)),
+    (FORMAT, dict(act=7)), (FORMAT, dict(x=arr(0, 24, F))), (SHAPE, dict(preact=arr(3, 31))), (INVALID, dict(out=NONE)),
+    (INVALID, dict(out=arr(1, 24, B, 31 * 48))), (ALIGN, dict(w=arr(1, 24, B, 1))),
+])
+def test_gated_refusals(want, kw):
+    assert gated(**kw) == want
+
+
+def test_projection_workspaces_of_refused_sizes():
+    for n in ("linear", "linear_backward", "gated_linear", "gated_linear_backward"):
+        size = getattr(T, f"taco_{n}_workspace_bytes")
+        assert size(-1, 8, 8) == 0 and size(8, 0, 8) == 0 and size(8, 8, 0) == 0 and size(8, 1 << 21, 8) == 0
