@@ -2,6 +2,7 @@
 // every check runs before any work is enqueued.
 #include <math.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "abi_common.h"
@@ -107,23 +108,25 @@ Operand operand(const Checked& c, bool by_k) { return Operand{static_cast<const 
 constexpr Mat kAbsent = {nullptr, 0, TACO_F32};
 
 // The workspace of a backward pass: dz as bf16 [m, wide] with rows on 16
-// bytes, then the partial column sums for dbias [groups][n].
+// bytes; then, in turn, the partial column sums for dbias [groups][n] and the
+// products' partial sums.
 struct BackwardSpace {
   int64_t ld_dz;
-  size_t dz_bytes, sums_bytes;
-  BackwardSpace(int64_t m, int64_t wide, int64_t n)
+  size_t dz_bytes, rest_bytes;
+  BackwardSpace(int64_t m, int64_t wide, int64_t n, int64_t k)
       : ld_dz((wide + 7) / 8 * 8),
         dz_bytes(((size_t)(m * ld_dz) * 2 + 255) / 256 * 256),
-        sums_bytes((size_t)act_back_groups(m) * (size_t)n * 4) {}
-  size_t total() const { return dz_bytes + sums_bytes; }
+        rest_bytes(std::max({(size_t)act_back_groups(m) * (size_t)n * 4, gemm_partial_bytes(m, k, wide, false),
+                             gemm_partial_bytes(wide, k, m, false)})) {}
+  size_t total() const { return dz_bytes + rest_bytes; }
 };
 
 // Forward pass of either kind of projection; `wide`: rows of w.
 int linear_forward(const Checked& cx, const Checked& cw, const Epilogue& e, bool gated, int64_t m, int64_t n,
-                   int64_t k, hipStream_t stream) {
-  GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e};
+                   int64_t k, void* ws, hipStream_t stream) {
+  const GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e, 1, k, nullptr, 0};
   clear_stale_error();
-  return hip_status(launch_gemm(g, stream));
+  return hip_status(launch_gemm(g, ws, stream));
 }
 
 // Backward pass of either kind: dz, then dx = dz W and dw = dz^T x.
@@ -131,7 +134,8 @@ int linear_backward(const Checked& cdout, const Checked& cx, const Checked& cw, 
                     const Checked& cdx, const Checked& cdw, const Checked& cdb, bool gated, int64_t m, int64_t n,
                     int64_t k, void* ws, hipStream_t stream) {
   const int64_t wide = gated ? 2 * n : n;
-  const BackwardSpace space(m, wide, n);
+  const BackwardSpace space(m, wide, gated ? 0 : n, k);
+  void* rest = static_cast<char*>(ws) + space.dz_bytes;
   Operand dz = operand(cdout, false);
   clear_stale_error();
   if (gated || act != TACO_ACT_NONE || cdb.m.p) {
@@ -140,19 +144,21 @@ int linear_backward(const Checked& cdout, const Checked& cx, const Checked& cw, 
       b.dz = static_cast<uint16_t*>(ws);
       dz = Operand{b.dz, space.ld_dz, false};
     }
-    if (cdb.m.p) b.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + space.dz_bytes);
+    if (cdb.m.p) b.partials = static_cast<float*>(rest);
     const hipError_t err = launch_act_back(b, stream);
     if (err != hipSuccess) return TACO_ERR_HIP;
   }
   if (cdx.m.p && m > 0) {
-    const GemmArgs g = {dz, operand(cw, true), m, (int)k, wide, false, {kAbsent, kAbsent, kAbsent, cdx.m, kActNone}};
-    const hipError_t err = launch_gemm(g, stream);
+    const GemmArgs g = {dz, operand(cw, true), m, (int)k, wide, false, {kAbsent, kAbsent, kAbsent, cdx.m, kActNone},
+                        1, wide, nullptr, 0};
+    const hipError_t err = launch_gemm(g, rest, stream);
     if (err != hipSuccess) return TACO_ERR_HIP;
   }
   if (cdw.m.p) {
     dz.by_k = true;
-    const GemmArgs g = {dz, operand(cx, true), wide, (int)k, m, false, {kAbsent, kAbsent, kAbsent, cdw.m, kActNone}};
-    const hipError_t err = launch_gemm(g, stream);
+    const GemmArgs g = {dz, operand(cx, true), wide, (int)k, m, false, {kAbsent, kAbsent, kAbsent, cdw.m, kActNone},
+                        1, m, nullptr, 0};
+    const hipError_t err = launch_gemm(g, rest, stream);
     if (err != hipSuccess) return TACO_ERR_HIP;
   }
   return TACO_OK;
@@ -210,10 +216,7 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
 }
 
 size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  return check_linear_sizes(M, N, N, K) == TACO_OK ? gemm_partial_bytes(M, N, K, false) : 0;
 }
 
 int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_array residual, taco_array out,
@@ -231,14 +234,11 @@ int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_a
   if (st != TACO_OK) return st;
   if (any_overlap({&cx, &cw, &cb, &cr}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
   if (M == 0) return TACO_OK;
-  return linear_forward(cx, cw, {cb.m, cr.m, cz.m, co.m, act}, false, M, N, K, stream);
+  return linear_forward(cx, cw, {cb.m, cr.m, cz.m, co.m, act}, false, M, N, K, workspace, stream);
 }
 
 size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-  (void)M;
-  (void)F;
-  (void)K;
-  return 0;
+  return check_linear_sizes(M, F, 2 * F, K) == TACO_OK ? gemm_partial_bytes(M, F, K, true) : 0;
 }
 
 int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, taco_array preact, int64_t M,
@@ -254,12 +254,12 @@ int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, t
   if (st != TACO_OK) return st;
   if (any_overlap({&cx, &cw}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
   if (M == 0) return TACO_OK;
-  return linear_forward(cx, cw, {kAbsent, kAbsent, cz.m, co.m, act}, true, M, F, K, stream);
+  return linear_forward(cx, cw, {kAbsent, kAbsent, cz.m, co.m, act}, true, M, F, K, workspace, stream);
 }
 
 size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (check_linear_sizes(M, N, N, K) != TACO_OK) return 0;
-  return BackwardSpace(M, N, N).total();
+  return BackwardSpace(M, N, N, K).total();
 }
 
 int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
@@ -283,7 +283,7 @@ int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t ac
 
 size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
   if (check_linear_sizes(M, F, 2 * F, K) != TACO_OK) return 0;
-  return BackwardSpace(M, 2 * F, 0).total();
+  return BackwardSpace(M, 2 * F, 0, K).total();
 }
 
 int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,

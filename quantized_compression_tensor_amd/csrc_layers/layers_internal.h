@@ -66,6 +66,12 @@ struct GemmArgs {
   int64_t K;
   bool gated;
   Epilogue e;
+  // set by launch_gemm: K cut into `splits` parts of `part` (a multiple of
+  // 64), whose sums go to partials [splits][M][ld_partials] in float32
+  int splits;
+  int64_t part;
+  float* partials;
+  int64_t ld_partials;
 };
 
 // dz = dout * act'(z) (gated: both halves), and the column sums of dz.
@@ -85,7 +91,9 @@ int act_back_groups(int64_t M);
 int norm_back_groups(int64_t rows, int64_t cols);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_back(const NormBackArgs& a, hipStream_t s);
-hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
+// Bytes of partial sums that a product of this size takes (0: K is not cut).
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
+hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
 hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s);
 // out [cols] = the sum of `count` rows of `in`, ld apart (zeros if count is 0).
 void launch_column_sum(const float* in, int64_t ld, int count, int64_t cols, const Mat& out, hipStream_t s);

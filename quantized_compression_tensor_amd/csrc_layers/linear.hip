@@ -5,6 +5,8 @@
 // in float32 on the bf16 matrix cores. An operand lies in memory with its k
 // contiguous (x and W of the forward pass) or with its rows contiguous (W for
 // dx = dz W, dz and x for dw = dz^T x).
+#include <type_traits>
+
 #include "layers_device.h"
 #include "layers_internal.h"
 
@@ -82,9 +84,13 @@ struct Tiles {
   static constexpr int kThreads = kWave * WGM * WGN;
   static constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;   // 32 x 32 MFMA tiles of a wave
   static constexpr int kStage = (BM + BN) * BK;                  // elements of one LDS stage
+  static constexpr int kTurnLd = TN * 32 + 4;                    // floats of a row in the epilogue's turn
+  static constexpr int kLdsBytes = 2 * kStage * 2;
+  static_assert(WGM * WGN * 32 * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
 using TilesLarge = Tiles<256, 256, 2, 4>;
 using TilesSmall = Tiles<128, 128, 2, 2>;
+constexpr int kGroupM = 8;   // tile rows walked together (their b rows are shared through L2)
 
 // A tile of R rows by 64 k in LDS, without padding, in chunks of 8 elements.
 // A matrix product reads a chunk column (k contiguous) or a block of 4 k by 16
@@ -103,8 +109,7 @@ struct LdsTile {
   static TACO_DEV int swizzle(int line) {
     return BY_K ? 4 * (line & 3) + 2 * ((line >> 3) & 1) : (line >> 1) & 7;
   }
-  // Line and chunk of the chunk at position q of the tile in LDS.
-  static TACO_DEV int line_of(int q) { return q / kPerLine; }
+  // Number in its line of the chunk at position q of the tile in LDS.
   static TACO_DEV int chunk_of(int q) { return (q % kPerLine) ^ swizzle(q / kPerLine); }
   // Operand of a 32 x 32 x 16 product: lane l holds row r0 + l % 32 and the
   // eight k of 16 kk + 8 (l / 32).
@@ -132,44 +137,167 @@ struct LdsTile {
   }
 };
 
-// Moves one tile's chunks of one operand from memory into LDS.
-template <bool BY_K, int R, int NT>
-struct Loader {
+// How a thread's chunks of one operand's tile get from memory into LDS.
+// GATED (k contiguous only): of each 64 lines the first 32 are rows of the
+// gate's projection, from p, and the others rows of the other one, from p2.
+template <bool BY_K, int R, int NT, bool GATED>
+struct Chunks {
   using Tile = LdsTile<BY_K, R>;
-  static constexpr int kPer = Tile::kChunks / NT;
+  static constexpr int kPer = Tile::kChunks / NT;   // of a thread
+  static constexpr int kLines = NT / Tile::kPerLine;   // between two of its chunks
   static_assert(Tile::kChunks % NT == 0, "whole chunks for every thread");
-  u32x4 reg[kPer];
-  TACO_DEV void load(const uint16_t* p, int64_t ld, int rows, int64_t k0, int64_t K, int tid) {
+  static_assert(!GATED || (!BY_K && (NT == 256 || NT == 512)), "gated tiles");
+  // The swizzle has a period of 16 lines: a thread's chunks have one chunk number.
+  static_assert(kLines % 16 == 0, "one chunk number per thread");
+  static TACO_DEV int line(int tid, int i) { return tid / Tile::kPerLine + i * kLines; }
+  static TACO_DEV int chunk(int tid) { return Tile::chunk_of(tid); }
+  static TACO_DEV int row(int l) { return GATED ? l / 64 * 32 + l % 32 : l; }
+  // Whether chunk i of this wave comes from p2 (wave-uniform).
+  static TACO_DEV bool second(int wave, int i) { return GATED && (NT == 512 ? wave >= 4 : (i & 1) != 0); }
+};
+
+// 16 bytes per lane from byte offset `off` of the resource to LDS: lane l's to
+// t + 8 l.
+TACO_DEV void load_to_lds(rsrc_t r, int off, uint16_t* t) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (TACO_LDS void*)t, 16, off, 0, 0, 0);
+}
+
+// Straight into LDS, 16 bytes per lane without passing the registers. Wants
+// rows on 16 bytes and a multiple of 8 elements along the contiguous axis.
+// What lies outside the operand reads as zeros: past its last row by the size
+// of the buffer resource, past its last k (k contiguous) by an offset that is
+// outside it.
+template <bool BY_K, int R, int NT, bool GATED>
+struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
+  using C = Chunks<BY_K, R, NT, GATED>;
+  static constexpr int kOutside = 0x7FFFFFF0;
+  const char *p, *p2;
+  int64_t bytes;    // of the operand from p on
+  int64_t step;     // bytes from one K step to the next
+  int off[C::kPer];
+  int chunk_k;      // k of this thread's chunks in a step (k contiguous)
+  TACO_DEV void init(const uint16_t* base, const uint16_t* base2, int64_t ld, int rows, int64_t K, int tid) {
+    p = reinterpret_cast<const char*>(base);
+    p2 = reinterpret_cast<const char*>(base2);
+    bytes = 2 * (BY_K ? (K - 1) * ld + rows : (rows - 1) * ld + K);
+    step = BY_K ? 128 * ld : 128;
+    const int c = C::chunk(tid);
+    chunk_k = BY_K ? 0 : 8 * c;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int q = tid + i * NT, line = Tile::line_of(q), c = Tile::chunk_of(q);
-      const int64_t k = k0 + (BY_K ? line : 8 * c);
-      const int r = BY_K ? 8 * c : line;
-      const int64_t left = BY_K ? (k < K ? rows - r : 0) : (r < rows ? K - k : 0);
-      Oct<kBF16> o;
-      o.load(p, BY_K ? k * ld + r : r * ld + k, left > 8 ? 8 : (int)left);
-      reg[i] = o.v;
-    }
+    for (int i = 0; i < C::kPer; ++i) off[i] = C::row(C::line(tid, i)) * (int)ld * 2 + 16 * c;
   }
-  TACO_DEV void store(uint16_t* t, int tid) const {
+  // Starts the loads of a step whose first k has `left` k after it (and moves
+  // on to the next step).
+  TACO_DEV void issue(uint16_t* t, int wave, int64_t left) {
+    const int64_t size = left > 0 ? bytes : 0;   // past the last step: no access
+    const bool in = BY_K || chunk_k < left;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) *reinterpret_cast<u32x4*>(t + (tid + i * NT) * 8) = reg[i];
+    for (int i = 0; i < C::kPer; ++i)
+      load_to_lds(make_rsrc(C::second(wave, i) ? p2 : p, size), in ? off[i] : kOutside,
+                  t + (i * NT + wave * kWave) * 8);
+    p += step;
+    p2 += step;
+    bytes -= step;
+  }
+  TACO_DEV void store(uint16_t*, int) const {}
+};
+
+// Through registers, for rows that start anywhere.
+template <bool BY_K, int R, int NT, bool GATED>
+struct StagedLoader : Chunks<BY_K, R, NT, GATED> {
+  using C = Chunks<BY_K, R, NT, GATED>;
+  const uint16_t *p, *p2;
+  int64_t ld;
+  int rows, tid;
+  u32x4 reg[C::kPer];
+  TACO_DEV void init(const uint16_t* base, const uint16_t* base2, int64_t ld_, int rows_, int64_t, int tid_) {
+    p = base;
+    p2 = base2;
+    ld = ld_;
+    rows = rows_;
+    tid = tid_;
+  }
+  TACO_DEV void issue(uint16_t*, int wave, int64_t left) {
+    const int c = 8 * C::chunk(tid);
+    const bool whole = rows >= (GATED ? R / 2 : R) && left >= 64;
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) {
+      const int l = C::line(tid, i), r = BY_K ? c : C::row(l), k = BY_K ? l : c;
+      const uint16_t* at = (C::second(wave, i) ? p2 : p) + (BY_K ? k * ld + r : r * ld + k);
+      if (whole) {
+        __builtin_memcpy(&reg[i], at, 16);
+      } else {
+        const int64_t n = BY_K ? (k < left ? rows - r : 0) : (r < rows ? left - k : 0);
+        Oct<kBF16> o;
+        o.load(at, 0, n > 8 ? 8 : (int)n);
+        reg[i] = o.v;
+      }
+    }
+    const int64_t step = BY_K ? 64 * ld : 64;
+    p += step;
+    p2 += step;
+  }
+  TACO_DEV void store(uint16_t* t, int) const {
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) *reinterpret_cast<u32x4*>(t + (tid + i * NT) * 8) = reg[i];
   }
 };
 
-template <class TL, bool AK, bool BK_>
-__global__ __launch_bounds__(TL::kThreads) void k_gemm(GemmArgs a) {
+// Output tile of this workgroup: each XCD walks one contiguous range of tiles,
+// and inside it groups of kGroupM tile rows column by column, so the
+// workgroups resident on an XCD share rows of a and of b through its L2.
+TACO_DEV void tile_of(unsigned t, unsigned ntm, unsigned ntn, unsigned* tm, unsigned* tn) {
+  const unsigned per_group = kGroupM * ntn, group = t / per_group, in_group = t % per_group;
+  const unsigned first = group * kGroupM, rows = ntm - first < kGroupM ? ntm - first : kGroupM;
+  *tm = first + in_group % rows;
+  *tn = in_group / rows;
+}
+
+// Waits until this wave's loads into LDS have landed. The compiler does not
+// count them, so every barrier that hands their data over has this before it.
+TACO_DEV void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0), the other counters as they are
+  asm volatile("" ::: "memory");
+}
+template <bool DIRECT>
+TACO_DEV void barrier() {
+  if (DIRECT) wait_loads();
+  __syncthreads();
+}
+
+// The kernel of every product: a workgroup sums one output tile over one part
+// of K, in steps of 64 k through two LDS stages. A step is four slices of 16
+// k; the operands of the next slice are read while one is multiplied. Before
+// its last slice a step waits for the loads of the next one, which have had a
+// whole step's time, and starts those of the step after next into the stage
+// that has just been read to its end.
+template <class TL, bool AK, bool BK_, bool GATED, bool DIRECT>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
+  constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
+  constexpr int kSlices = BK / 16;
+  static_assert(!GATED || TN == 2, "a wave holds the two projections of its columns");
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
-  const int ntn = (a.N + BN - 1) / BN;
-  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * BM;
-  const int n0 = (int)(blockIdx.x % ntn) * BN;
-  const int rows_a = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_b = a.N - n0 < BN ? a.N - n0 : BN;
-  const uint16_t* pa = a.a.p + (AK ? m0 : m0 * a.a.ld);
-  const uint16_t* pb = a.b.p + (BK_ ? n0 : n0 * a.b.ld);
+  const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
+  const unsigned block = xcd_ordered_block(), split = block / (ntm * ntn);
+  unsigned tm, tn;
+  tile_of(block - split * (ntm * ntn), ntm, ntn, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, k0 = split * a.part;
+  const int n0 = (int)tn * kCols;
+  const int64_t K = a.K - k0 < a.part ? a.K - k0 : a.part;   // of this part
+  const int rows_a = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_b = a.N - n0 < kCols ? a.N - n0 : kCols;
+  const uint16_t* pa = a.a.p + (AK ? m0 + k0 * a.a.ld : m0 * a.a.ld + k0);
+  const uint16_t* pb = a.b.p + (BK_ ? n0 + k0 * a.b.ld : n0 * a.b.ld + k0);
+  const uint16_t* pb2 = GATED ? pb + (int64_t)a.N * a.b.ld : pb;
+  using LA = std::conditional_t<DIRECT, DirectLoader<AK, BM, NT, false>, StagedLoader<AK, BM, NT, false>>;
+  using LB = std::conditional_t<DIRECT, DirectLoader<BK_, BN, NT, GATED>, StagedLoader<BK_, BN, NT, GATED>>;
+  LA la;
+  LB lb;
+  la.init(pa, pa, a.a.ld, rows_a, K, tid);
+  lb.init(pb, pb2, a.b.ld, rows_b, K, tid);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -177,38 +305,74 @@ __global__ __launch_bounds__(TL::kThreads) void k_gemm(GemmArgs a) {
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  Loader<AK, BM, NT> la;
-  Loader<BK_, BN, NT> lb;
-  la.load(pa, a.a.ld, rows_a, 0, a.K, tid);
-  lb.load(pb, a.b.ld, rows_b, 0, a.K, tid);
-  for (int64_t k0 = 0; k0 < a.K; k0 += BK) {
-    __syncthreads();
-    la.store(lds, tid);
-    lb.store(lds + BM * BK, tid);
-    __syncthreads();
-    if (k0 + BK < a.K) {
-      la.load(pa, a.a.ld, rows_a, k0 + BK, a.K, tid);
-      lb.load(pb, a.b.ld, rows_b, k0 + BK, a.K, tid);
+
+  const int steps = (int)((K + BK - 1) / BK);
+  auto issue = [&](int ks, int stage) {
+    const int64_t left = K - (int64_t)ks * BK;
+    if (DIRECT || left > 0) {
+      la.issue(lds + stage * TL::kStage, wave, left);
+      lb.issue(lds + stage * TL::kStage + BM * BK, wave, left);
     }
-#pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      bf16x8 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = LdsTile<AK, BM>::operand(lds, wm * TM * 32 + i * 32, kk, lane);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = LdsTile<BK_, BN>::operand(lds + BM * BK, wn * TN * 32 + j * 32, kk, lane);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+  };
+  auto store = [&](int ks, int stage) {   // nothing where the loads went into LDS themselves
+    if (!DIRECT && ks < steps) {
+      la.store(lds + stage * TL::kStage, wave);
+      lb.store(lds + stage * TL::kStage + BM * BK, wave);
     }
+  };
+  bf16x8 fa[2][TM], fb[2][TN];
+  auto read = [&](int stage, int kk, int set) {
+    const uint16_t* t = lds + stage * TL::kStage;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[set][i] = LdsTile<AK, BM>::operand(t, (wm * TM + i) * 32, kk, lane);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[set][j] = LdsTile<BK_, BN>::operand(t + BM * BK, (wn * TN + j) * 32, kk, lane);
+  };
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+  };
+  auto step = [&](int ks, int stage) {
+#pragma unroll
+    for (int kk = 0; kk < kSlices; ++kk) {
+      if (kk + 1 < kSlices) {
+        read(stage, kk + 1, (kk + 1) & 1);
+        if (!DIRECT && kk == 1) {
+          store(ks + 1, stage ^ 1);
+          issue(ks + 2, stage ^ 1);
+        }
+      } else {
+        barrier<DIRECT>();
+        read(stage ^ 1, 0, 0);   // past the last step: what is read is not used
+        if (DIRECT) issue(ks + 2, stage);
+      }
+      multiply(kk & 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (steps > 0) {
+    issue(0, 0);
+    store(0, 0);
+    if (DIRECT) wait_loads();
+    issue(1, 1);
+    __syncthreads();
+    read(0, 0, 0);
+    int ks = 0;
+    for (; ks + 1 < steps; ks += 2) {
+      step(ks, 0);
+      step(ks + 1, 1);
+    }
+    if (ks < steps) step(ks, 0);
   }
-  __syncthreads();
+  barrier<DIRECT>();
+
   // Accumulator e of lane l holds row 8 (e / 4) + 4 (l / 32) + e % 4, column
   // l % 32 of its tile. Each wave turns 32 rows at a time round through its
   // own part of LDS, so that a lane has eight neighbouring columns of a row.
-  constexpr int kCols = TN * 32, kLd = kCols + 4;
+  constexpr int kLd = TL::kTurnLd, kWaveCols = GATED ? 32 : TN * 32, kLanes = kWaveCols / 8;
   float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -218,111 +382,127 @@ __global__ __launch_bounds__(TL::kThreads) void k_gemm(GemmArgs a) {
       for (int e = 0; e < 16; ++e)
         turn[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * kLd + j * 32 + (lane & 31)] = acc[i][j][e];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    constexpr int kLanes = kCols / 8;   // per row
+    const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c;
+#pragma unroll 1
     for (int r = lane / kLanes; r < 32; r += kWave / kLanes) {
-      const int c = (lane % kLanes) * 8, n = n0 + wn * kCols + c;
       const int64_t m = m0 + (wm * TM + i) * 32 + r;
-      float z[8];
-      *reinterpret_cast<f32x4*>(z) = *reinterpret_cast<const f32x4*>(turn + r * kLd + c);
-      *reinterpret_cast<f32x4*>(z + 4) = *reinterpret_cast<const f32x4*>(turn + r * kLd + c + 4);
-      if (m < a.M && n < a.N) finish(a.e, m, n, a.N - n, z);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
-}
-
-// The gated layer: a tile of 64 output columns, the gate's 64 rows of b and
-// then the other projection's.
-__global__ __launch_bounds__(256) void k_gated(GemmArgs a) {
-  constexpr int BM = 128, BN = 128, BK = 64, NT = 256, F = BN / 2;
-  extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
-  const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
-  const int wm = wave / 2, wn = wave % 2;
-  const int ntn = (a.N + F - 1) / F;
-  const int64_t m0 = (int64_t)(blockIdx.x / ntn) * BM;
-  const int n0 = (int)(blockIdx.x % ntn) * F;
-  const int rows_a = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_b = a.N - n0 < F ? a.N - n0 : F;
-  const uint16_t* pa = a.a.p + m0 * a.a.ld;
-  const uint16_t* pg = a.b.p + n0 * a.b.ld;
-  const uint16_t* pu = a.b.p + (n0 + (int64_t)a.N) * a.b.ld;
-  f32x16 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  Loader<false, BM, NT> la;
-  Loader<false, F, NT> lg, lu;
-  for (int64_t k0 = 0; k0 < a.K; k0 += BK) {
-    la.load(pa, a.a.ld, rows_a, k0, a.K, tid);
-    lg.load(pg, a.b.ld, rows_b, k0, a.K, tid);
-    lu.load(pu, a.b.ld, rows_b, k0, a.K, tid);
-    __syncthreads();
-    la.store(lds, tid);
-    lg.store(lds + BM * BK, tid);
-    lu.store(lds + (BM + F) * BK, tid);
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      bf16x8 fa[2], fb[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = LdsTile<false, BM>::operand(lds, wm * 64 + i * 32, kk, lane);
-        fb[i] = LdsTile<false, F>::operand(lds + (BM + i * F) * BK, wn * 32, kk, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  __syncthreads();
-  constexpr int kLd = 64 + 4;
-  float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        turn[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * kLd + j * 32 + (lane & 31)] = acc[i][j][e];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    for (int r = lane / 4; r < 32; r += 16) {
-      const int c = (lane % 4) * 8, n = n0 + wn * 32 + c;
-      const int64_t m = m0 + (wm * 2 + i) * 32 + r;
       float z[8], u[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + c + 4 * h);
-        *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + 32 + c + 4 * h);
+        if (GATED)
+          *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + 32 + c + 4 * h);
       }
-      if (m < a.M && n < a.N) finish_gated(a.e, a.N, m, n, a.N - n, z, u);
+      if (m >= a.M || n >= a.N) continue;
+      const int count = a.N - n;
+      if (a.splits > 1) {
+        float* part = a.partials + (split * a.M + m) * a.ld_partials;
+        store8(part, kF32, n, count, z);
+        if (GATED) store8(part, kF32, a.N + n, count, u);
+      } else if (GATED) {
+        finish_gated(a.e, a.N, m, n, count, z, u);
+      } else {
+        finish(a.e, m, n, count, z);
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
-template <class TL>
-static void launch_tiles(const GemmArgs& a, hipStream_t s) {
-  const int64_t tiles = ((a.M + TL::BM - 1) / TL::BM) * (((int64_t)a.N + TL::BN - 1) / TL::BN);
-  const dim3 grid((unsigned)tiles), block(TL::kThreads);
-  const size_t stage = TL::kStage * 2, turn = (size_t)TL::kThreads / kWave * 32 * (TL::TN * 32 + 4) * 4;
-  const size_t lds = stage > turn ? stage : turn;
-  if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false>), grid, block, lds, s, a);
-  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_gemm<TL, true, true>), grid, block, lds, s, a);
+// Joins the parts of K, in order, and finishes: a lane takes eight columns.
+template <bool GATED>
+__global__ __launch_bounds__(256) void k_join(GemmArgs a) {
+  const int64_t per_row = (a.N + 7) / 8, total = a.M * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / per_row;
+    const int n = (int)(i % per_row) * 8, count = a.N - n;
+    float z[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = 0.0f, u[e] = 0.0f;
+    for (int s = 0; s < a.splits; ++s) {
+      const float* part = a.partials + (s * a.M + m) * a.ld_partials;
+      float f[8];
+      load8(part, kF32, n, count, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] += f[e];
+      if (GATED) {
+        load8(part, kF32, a.N + n, count, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] += f[e];
+      }
+    }
+    if (GATED) finish_gated(a.e, a.N, m, n, count, z, u);
+    else finish(a.e, m, n, count, z);
+  }
 }
 
-hipError_t launch_gemm(const GemmArgs& a, hipStream_t s) {
+// ----------------------------------------------------------------- launch --
+
+// Which tiles a product takes and into how many parts its K is cut. Decided by
+// the sizes alone, so that the workspace is known before the call.
+struct Plan {
+  bool large;
+  int splits;
+  int64_t part;
+};
+
+static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
+
+static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
+  Plan p = {tiles_of(M, N, 256, gated ? 128 : 256) >= 192, 1, (K + 63) / 64 * 64};
+  if (p.large) return p;
+  const int64_t tiles = tiles_of(M, N, 128, gated ? 64 : 128), steps = (K + 63) / 64;
+  // two workgroups of 128 x 128 fit on a CU; at least 8 steps for a part
+  int64_t splits = tiles > 0 ? 512 / tiles : 1;
+  if (splits > steps / 8) splits = steps / 8;
+  if (splits > 16) splits = 16;
+  if (splits > 1) {
+    const int64_t per = (steps + splits - 1) / splits;
+    p.part = per * 64;
+    p.splits = (int)((steps + per - 1) / per);
+  }
+  return p;
+}
+
+static int64_t partial_ld(int64_t N, bool gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
+
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  const Plan p = plan_of(M, N, K, gated);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)partial_ld(N, gated) * 4 : 0;
+}
+
+// Rows on 16 bytes, and a multiple of 8 elements along the contiguous axis.
+static bool direct(const Operand& o, int64_t rows, int64_t K) {
+  return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && (o.by_k ? rows : K) % 8 == 0;
+}
+
+template <class TL, bool DIRECT>
+static void launch_tiles(const GemmArgs& a, hipStream_t s) {
+  const int64_t tiles = tiles_of(a.M, a.N, TL::BM, a.gated ? TL::BN / 2 : TL::BN);
+  const dim3 grid((unsigned)(tiles * a.splits)), block(TL::kThreads);
+  constexpr size_t lds = TL::kLdsBytes;
+  if (a.gated) hipLaunchKernelGGL((k_gemm<TL, false, false, true, DIRECT>), grid, block, lds, s, a);
+  else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false, DIRECT>), grid, block, lds, s, a);
+  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false, DIRECT>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_gemm<TL, true, true, false, DIRECT>), grid, block, lds, s, a);
+}
+
+hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
-  if (a.gated) {
-    const int64_t tiles = ((a.M + 127) / 128) * (((int64_t)a.N + 63) / 64);
-    hipLaunchKernelGGL(k_gated, dim3((unsigned)tiles), dim3(256), 4 * 32 * 68 * 4, s, a);
-  } else {
-    launch_tiles<TilesSmall>(a, s);
+  const Plan p = plan_of(a.M, a.N, a.K, a.gated);
+  a.splits = p.splits;
+  a.part = p.part;
+  a.partials = static_cast<float*>(partials);
+  a.ld_partials = partial_ld(a.N, a.gated);
+  const bool d = direct(a.a, a.M, a.K) && direct(a.b, a.N, a.K);
+  if (p.large && d) launch_tiles<TilesLarge, true>(a, s);
+  else if (d) launch_tiles<TilesSmall, true>(a, s);
+  else launch_tiles<TilesSmall, false>(a, s);
+  if (a.splits > 1) {
+    const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
+    if (a.gated) hipLaunchKernelGGL((k_join<true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_join<false>), grid, dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
