@@ -13,7 +13,6 @@
 namespace taco {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TACO_LDS __attribute__((address_space(3)))
 
@@ -82,46 +81,56 @@ template <int BM_, int BN_, int WGM_, int WGN_>
 struct Tiles {
   static constexpr int BM = BM_, BN = BN_, BK = 64, WGM = WGM_, WGN = WGN_;
   static constexpr int kThreads = kWave * WGM * WGN;
-  static constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;   // 32 x 32 MFMA tiles of a wave
-  static constexpr int kStage = (BM + BN) * BK;                  // elements of one LDS stage
-  static constexpr int kTurnLd = TN * 32 + 4;                    // floats of a row in the epilogue's turn
-  static constexpr int kLdsBytes = 2 * kStage * 2;
+  static constexpr int TM = BM / WGM / 16, TN = BN / WGN / 16;   // 16 x 16 MFMA tiles of a wave
+  static constexpr int kA = BM * BK, kB = BN * BK;               // elements of an LDS stage
+  static constexpr int kStagesA = 3, kStagesB = 2;
+  // After how many of a slice's rows of MFMA tiles a stage is handed back: b's
+  // in the first slice, a's in the second
+  static constexpr int kFreeB = TM / 2, kFreeA = TM / 4;
+  static constexpr int kTurnLd = TN * 16 + 4;                    // floats of a row in the epilogue's turn
+  static constexpr int kLdsBytes = (kStagesA * kA + kStagesB * kB) * 2;
   static_assert(WGM * WGN * 32 * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
 using TilesLarge = Tiles<256, 256, 2, 4>;
 using TilesSmall = Tiles<128, 128, 2, 2>;
 constexpr int kGroupM = 8;   // tile rows walked together (their b rows are shared through L2)
 
+// An LDS read that transposes (see LdsTile::operand). The pointer is marked
+// restrict because the compiler otherwise has each such read wait for every
+// load into LDS that is under way; hand_over() waits for those that matter.
+TACO_DEV s16x4 read_transposed(TACO_LDS s16x4* __restrict__ at) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(at); }
+
 // A tile of R rows by 64 k in LDS, without padding, in chunks of 8 elements.
-// A matrix product reads a chunk column (k contiguous) or a block of 4 k by 16
+// A matrix product reads a chunk column (k contiguous) or blocks of 4 k by 16
 // rows (rows contiguous, transposed by the LDS read itself); the chunks of a
 // line are permuted by an xor of their number so that either read touches all
 // LDS banks evenly.
 //   k contiguous      line = row, 8 chunks of 8 k;  chunk c at c ^ ((row >> 1) & 7):
 //                     16 neighbouring rows of one chunk column fill 256 bytes
 //   rows contiguous   line = k, R / 8 chunks of 8 rows;  chunk c at
-//                     c ^ (4 (k & 3) + 2 ((k >> 3) & 1)): the 4 k of a read,
-//                     64 bytes each, fill 256 bytes
+//                     c ^ (4 (k & 3) + 2 ((k >> 3) & 1)): the 8 k that half a
+//                     wave reads, 32 bytes each, fill 256 bytes
 template <bool BY_K, int R>
 struct LdsTile {
-  static constexpr int kPerLine = BY_K ? R / 8 : 8;
-  static constexpr int kChunks = R * 8;
+  static constexpr int BK = 64;
+  static constexpr int kPerLine = BY_K ? R / 8 : BK / 8;
+  static constexpr int kChunks = R * BK / 8;
   static TACO_DEV int swizzle(int line) {
     return BY_K ? 4 * (line & 3) + 2 * ((line >> 3) & 1) : (line >> 1) & 7;
   }
   // Number in its line of the chunk at position q of the tile in LDS.
   static TACO_DEV int chunk_of(int q) { return (q % kPerLine) ^ swizzle(q / kPerLine); }
-  // Operand of a 32 x 32 x 16 product: lane l holds row r0 + l % 32 and the
-  // eight k of 16 kk + 8 (l / 32).
+  // Operand of a 16 x 16 x 32 product: lane l holds row r0 + l % 16 and the
+  // eight k of 32 kk + 8 (l / 16).
   static TACO_DEV bf16x8 operand(const uint16_t* t, int r0, int kk, int lane) {
     if constexpr (!BY_K) {
-      const int r = r0 + (lane & 31), c = 2 * kk + (lane >> 5);
-      return *reinterpret_cast<const bf16x8*>(t + r * 64 + (c ^ swizzle(r)) * 8);
+      const int r = r0 + (lane & 15), c = 4 * kk + (lane >> 4);
+      return *reinterpret_cast<const bf16x8*>(t + r * BK + (c ^ swizzle(r)) * 8);
     } else {
       // a read takes, for each 16 lanes, 4 k of 16 rows from addresses of 4
       // rows each, and gives lane i of them the four k of row i
-      const int k = 16 * kk + 8 * (lane >> 5) + ((lane >> 2) & 3);
-      const int r = r0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      const int k = 32 * kk + 8 * (lane >> 4) + ((lane >> 2) & 3);
+      const int r = r0 + 4 * (lane & 3);
       union {
         s16x4 h[2];
         bf16x8 v;
@@ -129,8 +138,8 @@ struct LdsTile {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int kl = k + 4 * i;
-        const uint16_t* at = t + kl * R + ((r >> 3) ^ swizzle(kl)) * 8 + (r & 7);
-        u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TACO_LDS s16x4*)at);
+        TACO_LDS uint16_t* at = (TACO_LDS uint16_t*)t + (kl * R + ((r >> 3) ^ swizzle(kl)) * 8 + (r & 7));
+        u.h[i] = read_transposed((TACO_LDS s16x4*)at);
       }
       return u.v;
     }
@@ -143,17 +152,22 @@ struct LdsTile {
 template <bool BY_K, int R, int NT, bool GATED>
 struct Chunks {
   using Tile = LdsTile<BY_K, R>;
+  static constexpr int BK = Tile::BK;
   static constexpr int kPer = Tile::kChunks / NT;   // of a thread
   static constexpr int kLines = NT / Tile::kPerLine;   // between two of its chunks
   static_assert(Tile::kChunks % NT == 0, "whole chunks for every thread");
   static_assert(!GATED || (!BY_K && (NT == 256 || NT == 512)), "gated tiles");
-  // The swizzle has a period of 16 lines: a thread's chunks have one chunk number.
-  static_assert(kLines % 16 == 0, "one chunk number per thread");
   static TACO_DEV int line(int tid, int i) { return tid / Tile::kPerLine + i * kLines; }
-  static TACO_DEV int chunk(int tid) { return Tile::chunk_of(tid); }
+  static TACO_DEV int chunk(int tid, int i) { return Tile::chunk_of(tid + i * NT); }
+  // (k contiguous: the swizzle has a period of 16 lines, so all of a thread's
+  // chunks have one number)
+  static_assert(BY_K || kLines % 16 == 0, "one chunk number per thread");
   static TACO_DEV int row(int l) { return GATED ? l / 64 * 32 + l % 32 : l; }
-  // Whether chunk i of this wave comes from p2 (wave-uniform).
-  static TACO_DEV bool second(int wave, int i) { return GATED && (NT == 512 ? wave >= 4 : (i & 1) != 0); }
+  // Whether chunk i of this wave comes from p2 (wave-uniform: a wave's lines
+  // lie within 32).
+  static TACO_DEV bool second(int wave, int i) {
+    return GATED && ((wave * (kWave / Tile::kPerLine) + i * kLines) / 32 & 1) != 0;
+  }
 };
 
 // 16 bytes per lane from byte offset `off` of the resource to LDS: lane l's to
@@ -170,6 +184,7 @@ TACO_DEV void load_to_lds(rsrc_t r, int off, uint16_t* t) {
 template <bool BY_K, int R, int NT, bool GATED>
 struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
   using C = Chunks<BY_K, R, NT, GATED>;
+  static constexpr int BK = C::BK;
   static constexpr int kOutside = 0x7FFFFFF0;
   const char *p, *p2;
   int64_t bytes;    // of the operand from p on
@@ -180,32 +195,30 @@ struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
     p = reinterpret_cast<const char*>(base);
     p2 = reinterpret_cast<const char*>(base2);
     bytes = 2 * (BY_K ? (K - 1) * ld + rows : (rows - 1) * ld + K);
-    step = BY_K ? 128 * ld : 128;
-    const int c = C::chunk(tid);
-    chunk_k = BY_K ? 0 : 8 * c;
+    step = 2 * (BY_K ? BK * ld : BK);
+    chunk_k = BY_K ? 0 : 8 * C::chunk(tid, 0);
 #pragma unroll
-    for (int i = 0; i < C::kPer; ++i) off[i] = C::row(C::line(tid, i)) * (int)ld * 2 + 16 * c;
+    for (int i = 0; i < C::kPer; ++i) off[i] = C::row(C::line(tid, i)) * (int)ld * 2 + 16 * C::chunk(tid, i);
   }
-  // Starts the loads of a step whose first k has `left` k after it (and moves
-  // on to the next step).
-  TACO_DEV void issue(uint16_t* t, int wave, int64_t left) {
+  // Starts load i of a step whose first k has `left` k after it; after the
+  // last one, moves on to the next step.
+  TACO_DEV void issue(uint16_t* t, int wave, int64_t left, int i) {
     const int64_t size = left > 0 ? bytes : 0;   // past the last step: no access
     const bool in = BY_K || chunk_k < left;
-#pragma unroll
-    for (int i = 0; i < C::kPer; ++i)
-      load_to_lds(make_rsrc(C::second(wave, i) ? p2 : p, size), in ? off[i] : kOutside,
-                  t + (i * NT + wave * kWave) * 8);
-    p += step;
-    p2 += step;
-    bytes -= step;
+    load_to_lds(make_rsrc(C::second(wave, i) ? p2 : p, size), in ? off[i] : kOutside, t + (i * NT + wave * kWave) * 8);
+    if (i == C::kPer - 1) {
+      p += step;
+      p2 += step;
+      bytes -= step;
+    }
   }
-  TACO_DEV void store(uint16_t*, int) const {}
 };
 
 // Through registers, for rows that start anywhere.
 template <bool BY_K, int R, int NT, bool GATED>
 struct StagedLoader : Chunks<BY_K, R, NT, GATED> {
   using C = Chunks<BY_K, R, NT, GATED>;
+  static constexpr int BK = C::BK;
   const uint16_t *p, *p2;
   int64_t ld;
   int rows, tid;
@@ -217,12 +230,11 @@ struct StagedLoader : Chunks<BY_K, R, NT, GATED> {
     rows = rows_;
     tid = tid_;
   }
-  TACO_DEV void issue(uint16_t*, int wave, int64_t left) {
-    const int c = 8 * C::chunk(tid);
-    const bool whole = rows >= (GATED ? R / 2 : R) && left >= 64;
+  TACO_DEV void load(int wave, int64_t left) {
+    const bool whole = rows >= (GATED ? R / 2 : R) && left >= BK;
 #pragma unroll
     for (int i = 0; i < C::kPer; ++i) {
-      const int l = C::line(tid, i), r = BY_K ? c : C::row(l), k = BY_K ? l : c;
+      const int c = 8 * C::chunk(tid, i), l = C::line(tid, i), r = BY_K ? c : C::row(l), k = BY_K ? l : c;
       const uint16_t* at = (C::second(wave, i) ? p2 : p) + (BY_K ? k * ld + r : r * ld + k);
       if (whole) {
         __builtin_memcpy(&reg[i], at, 16);
@@ -233,11 +245,11 @@ struct StagedLoader : Chunks<BY_K, R, NT, GATED> {
         reg[i] = o.v;
       }
     }
-    const int64_t step = BY_K ? 64 * ld : 64;
+    const int64_t step = BY_K ? BK * ld : BK;
     p += step;
     p2 += step;
   }
-  TACO_DEV void store(uint16_t* t, int) const {
+  TACO_DEV void store(uint16_t* t) const {
 #pragma unroll
     for (int i = 0; i < C::kPer; ++i) *reinterpret_cast<u32x4*>(t + (tid + i * NT) * 8) = reg[i];
   }
@@ -253,30 +265,37 @@ TACO_DEV void tile_of(unsigned t, unsigned ntm, unsigned ntn, unsigned* tm, unsi
   *tn = in_group / rows;
 }
 
-// Waits until this wave's loads into LDS have landed. The compiler does not
-// count them, so every barrier that hands their data over has this before it.
-TACO_DEV void wait_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0), the other counters as they are
+// A barrier before which a wave waits until at most LDS of its latest LDS
+// accesses and LOADS of its latest loads into LDS are under way (LOADS < 0:
+// any number; both complete in order). Written out because the compiler's own
+// barrier would wait for all of them.
+template <int LDS, int LOADS>
+TACO_DEV void hand_over() {
+  // s_waitcnt: vmcnt in bits 0-3 and 14-15, lgkmcnt in bits 8-11, expcnt (no wait) in bits 4-6
+  constexpr int kVm = LOADS < 0 ? 63 : LOADS;
+  static_assert(LDS < 16 && kVm < 64, "counters");
   asm volatile("" ::: "memory");
-}
-template <bool DIRECT>
-TACO_DEV void barrier() {
-  if (DIRECT) wait_loads();
-  __syncthreads();
+  __builtin_amdgcn_s_waitcnt((kVm & 15) | (kVm >> 4) << 14 | LDS << 8 | 0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // The kernel of every product: a workgroup sums one output tile over one part
-// of K, in steps of 64 k through two LDS stages. A step is four slices of 16
-// k; the operands of the next slice are read while one is multiplied. Before
-// its last slice a step waits for the loads of the next one, which have had a
-// whole step's time, and starts those of the step after next into the stage
-// that has just been read to its end.
+// of K, in steps of 64 k, two slices of 32 each. What bounds it is how far
+// ahead of their use loads can be under way (a step lasts about 0.9 us, a load
+// about 1.3 us when every CU loads), so the LDS holds three steps of a and two
+// of b, and a stage is handed back as soon as it has been read: b's operands
+// are all in registers early in a step, a's follow one 16-row tile behind the
+// products that used the registers before. Every load has then one and a half
+// or two steps' time. The 16 x 16 x 32 products were faster than 32 x 32 x 16
+// (8192^3: 750 against 815 us) although they leave more gaps: this size is
+// bound by power, and they move half as many sums through the registers.
 template <class TL, bool AK, bool BK_, bool GATED, bool DIRECT>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
-  constexpr int kSlices = BK / 16;
-  static_assert(!GATED || TN == 2, "a wave holds the two projections of its columns");
+  
+  static_assert(!GATED || TN % 4 == 0, "a wave holds the two projections of its columns");
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
@@ -298,100 +317,122 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   LB lb;
   la.init(pa, pa, a.a.ld, rows_a, K, tid);
   lb.init(pb, pb2, a.b.ld, rows_b, K, tid);
-  f32x16 acc[TM][TN];
+  f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
 
   const int steps = (int)((K + BK - 1) / BK);
-  auto issue = [&](int ks, int stage) {
-    const int64_t left = K - (int64_t)ks * BK;
-    if (DIRECT || left > 0) {
-      la.issue(lds + stage * TL::kStage, wave, left);
-      lb.issue(lds + stage * TL::kStage + BM * BK, wave, left);
-    }
+  uint16_t *const lds_a = lds, *const lds_b = lds + TL::kStagesA * TL::kA;
+  bf16x8 fa[TM], fb[2][TN];
+  auto read_a = [&](const uint16_t* t, int kk, int i) { fa[i] = LdsTile<AK, BM>::operand(t, (wm * TM + i) * 16, kk, lane); };
+  auto read_b = [&](const uint16_t* t, int kk) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[kk][j] = LdsTile<BK_, BN>::operand(t, (wn * TN + j) * 16, kk, lane);
   };
-  auto store = [&](int ks, int stage) {   // nothing where the loads went into LDS themselves
-    if (!DIRECT && ks < steps) {
-      la.store(lds + stage * TL::kStage, wave);
-      lb.store(lds + stage * TL::kStage + BM * BK, wave);
-    }
+  auto multiply = [&](int kk, int i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[kk][j], acc[i][j], 0, 0, 0);
   };
-  bf16x8 fa[2][TM], fb[2][TN];
-  auto read = [&](int stage, int kk, int set) {
-    const uint16_t* t = lds + stage * TL::kStage;
+  // Part `part` of `parts` of the loads of step ks into stage t; staged, the
+  // stage gets what was loaded a step ago and the next step's loads start.
+  auto load = [&](auto& l, int ks, uint16_t* t, int part, int parts) {
+    constexpr int kPer = std::remove_reference_t<decltype(l)>::kPer;
+    if constexpr (DIRECT) {
+      const int each = (kPer + parts - 1) / parts;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[set][i] = LdsTile<AK, BM>::operand(t, (wm * TM + i) * 32, kk, lane);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fb[set][j] = LdsTile<BK_, BN>::operand(t + BM * BK, (wn * TN + j) * 32, kk, lane);
-  };
-  auto multiply = [&](int set) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
-  };
-  auto step = [&](int ks, int stage) {
-#pragma unroll
-    for (int kk = 0; kk < kSlices; ++kk) {
-      if (kk + 1 < kSlices) {
-        read(stage, kk + 1, (kk + 1) & 1);
-        if (!DIRECT && kk == 1) {
-          store(ks + 1, stage ^ 1);
-          issue(ks + 2, stage ^ 1);
-        }
-      } else {
-        barrier<DIRECT>();
-        read(stage ^ 1, 0, 0);   // past the last step: what is read is not used
-        if (DIRECT) issue(ks + 2, stage);
-      }
-      multiply(kk & 1);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < kPer; ++i)
+        if (i / each == part) l.issue(t, wave, K - (int64_t)ks * BK, i);
+    } else if (part == 0) {
+      if (ks < steps) l.store(t);
+      if (ks + 1 < steps) l.load(wave, K - (int64_t)(ks + 1) * BK);
     }
   };
   if (steps > 0) {
-    issue(0, 0);
-    store(0, 0);
-    if (DIRECT) wait_loads();
-    issue(1, 1);
-    __syncthreads();
-    read(0, 0, 0);
-    int ks = 0;
-    for (; ks + 1 < steps; ks += 2) {
-      step(ks, 0);
-      step(ks + 1, 1);
+    uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
+    uint16_t *b0 = lds_b, *b1 = lds_b + TL::kB;
+    if constexpr (!DIRECT) {
+      la.load(wave, K);
+      lb.load(wave, K);
     }
-    if (ks < steps) step(ks, 0);
+    load(la, 0, a0, 0, 1);
+    load(lb, 0, b0, 0, 1);
+    load(la, 1, a1, 0, 1);
+    load(lb, 1, b1, 0, 1);
+    load(la, 2, a2, 0, 1);
+    hand_over<0, DIRECT ? 2 * LA::kPer + LB::kPer : -1>();
+#pragma unroll
+    for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
+    read_b(b0, 0);
+    constexpr int kFreeA = TL::kFreeA, kFreeB = TL::kFreeB;
+#pragma unroll 1
+    for (int ks = 0; ks < steps; ++ks) {
+      read_b(b0, 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        // b0 has been read to its end: the reads since are those of kFreeB operands of a
+        if (i == kFreeB) hand_over<kFreeB * (AK ? 2 : 1), -1>();
+        if (i >= kFreeB) load(lb, ks + 2, b0, i - kFreeB, TM - kFreeB);
+        multiply(0, i);
+        read_a(a0, 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if (i == kFreeA) {
+          // a0 has been read to its end, a1 and b1 are there; past the last
+          // step what is read from them is not used
+          hand_over<0, DIRECT ? LA::kPer + LB::kPer : -1>();
+#pragma unroll
+          for (int q = 0; q < i; ++q) read_a(a1, 0, q);
+        }
+        if (i >= kFreeA) load(la, ks + 3, a0, i - kFreeA, TM - kFreeA);
+        multiply(1, i);
+        if (i >= kFreeA) read_a(a1, 0, i);
+        if (i == kFreeA + 1) read_b(b1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      uint16_t* t = a0;
+      a0 = a1;
+      a1 = a2;
+      a2 = t;
+      t = b0;
+      b0 = b1;
+      b1 = t;
+    }
   }
-  barrier<DIRECT>();
+  hand_over<0, 0>();
 
-  // Accumulator e of lane l holds row 8 (e / 4) + 4 (l / 32) + e % 4, column
-  // l % 32 of its tile. Each wave turns 32 rows at a time round through its
-  // own part of LDS, so that a lane has eight neighbouring columns of a row.
-  constexpr int kLd = TL::kTurnLd, kWaveCols = GATED ? 32 : TN * 32, kLanes = kWaveCols / 8;
+  // Accumulator e of lane l holds row 4 (l / 16) + e, column l % 16 of its
+  // tile. Each wave turns 32 rows at a time round through its own part of LDS,
+  // so that a lane has eight neighbouring columns of a row.
+  constexpr int kLd = TL::kTurnLd, kWaveCols = GATED ? TN * 8 : TN * 16, kLanes = kWaveCols / 8;
   float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  for (int i = 0; i < TM / 2; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        turn[(8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * kLd + j * 32 + (lane & 31)] = acc[i][j][e];
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          turn[(16 * h + 4 * (lane >> 4) + e) * kLd + j * 16 + (lane & 15)] = acc[2 * i + h][j][e];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c;
+    const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c, zc = GATED ? c / 32 * 64 + c % 32 : c;
 #pragma unroll 1
     for (int r = lane / kLanes; r < 32; r += kWave / kLanes) {
-      const int64_t m = m0 + (wm * TM + i) * 32 + r;
+      const int64_t m = m0 + wm * TM * 16 + i * 32 + r;
       float z[8], u[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + c + 4 * h);
+        *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + zc + 4 * h);
         if (GATED)
-          *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + 32 + c + 4 * h);
+          *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + 32 + zc + 4 * h);
       }
       if (m >= a.M || n >= a.N) continue;
       const int count = a.N - n;
