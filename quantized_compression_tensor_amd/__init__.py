@@ -155,9 +155,18 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    if torch.cuda.is_available() and torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
+    if torch.cuda.is_initialized():
+        return _current_stream(torch.cuda.current_device())
     return None
+
+
+def _current_stream(device):
+    """The handle of torch's current stream. torch builds a Stream object for
+    torch.cuda.current_stream() (about 3 us, as long as a launch); the plain
+    handle is taken from the function beneath where torch has it."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(status, where):
@@ -296,7 +305,7 @@ def taco_e5m2_encode(x, codes, n, stream=None):
 # any row stride, vectors [n]; sizes, strides and element types come from them.
 
 _ABSENT = taco_array(None, 0, TACO_F32, 0)
-_DTYPES = {}   # torch dtype -> TACO_F32 / TACO_BF16, filled with torch's import
+_DTYPES = {}   # torch dtype -> TACO_F32 / TACO_BF16, filled on first use
 
 
 def _dtype(t, what):
@@ -317,7 +326,8 @@ def _matrix(t, rows, cols, what):
     stride, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
-    return taco_array(t.data_ptr(), stride, _dtype(t, what), 0)
+    dt = _DTYPES.get(t.dtype)
+    return taco_array(t.data_ptr(), stride, _dtype(t, what) if dt is None else dt, 0)
 
 
 def _vector(t, n, what):
@@ -325,15 +335,18 @@ def _vector(t, n, what):
         return _ABSENT
     if t.shape != (n,):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n,)}")
-    if n > 1 and t.stride(0) != 1:
+    if n > 1 and not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    return taco_array(t.data_ptr(), n, _dtype(t, what), 0)
+    dt = _DTYPES.get(t.dtype)
+    return taco_array(t.data_ptr(), n, _dtype(t, what) if dt is None else dt, 0)
 
 
 def _floats(t, n, what):
     if t is None:
         return None
-    if _vector(t, n, what).dtype != TACO_F32:
+    if t.shape != (n,) or (n > 1 and not t.is_contiguous()):
+        raise ValueError(f"{what}: expected {n} contiguous values, got shape {tuple(t.shape)}")
+    if _dtype(t, what) != TACO_F32:
         raise TypeError(f"{what}: must be float32")
     return t.data_ptr()
 

@@ -180,7 +180,7 @@ int taco_layer_norm(taco_array x, int64_t rows, int64_t cols, taco_array weight,
   if (st != TACO_OK) return st;
   if (any_overlap({&cx, &cw, &cb}, {&cy, &cm, &cr})) return TACO_ERR_INVALID_ARG;
   if (rows == 0) return TACO_OK;
-  const NormArgs a = {cx.m, cw.m, cb.m, cy.m, rows, (int)cols, eps, mean, rstd};
+  const NormArgs a = {cx.m, cw.m, cb.m, cy.m, rows, (int)cols, eps, mean, rstd, 0};
   clear_stale_error();
   return hip_status(launch_norm(a, stream));
 }
@@ -210,7 +210,7 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
   if (any_overlap({&cdy, &cx, &cw, &cm, &cr}, {&cdx, &cdw, &cdb, &cws})) return TACO_ERR_INVALID_ARG;
   if (rows == 0 && !sums) return TACO_OK;
   const NormBackArgs a = {cdy.m, cx.m, cw.m, cdx.m, cdw.m, cdb.m, rows, (int)cols, mean, rstd,
-                          static_cast<float*>(cws.m.p)};
+                          static_cast<float*>(cws.m.p), 0};
   clear_stale_error();
   return hip_status(launch_norm_back(a, stream));
 }

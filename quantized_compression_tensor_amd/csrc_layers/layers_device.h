@@ -26,6 +26,9 @@ struct Oct;
 template <>
 struct Oct<kBF16> {
   u32x4 v;
+  TACO_DEV void clear() { v = u32x4{0u, 0u, 0u, 0u}; }
+  TACO_DEV void opaque() { asm volatile("" : "+v"(v)); }   // the compiler forgets where the value came from
+  TACO_DEV void load(const void* base, int64_t at) { __builtin_memcpy(&v, static_cast<const uint16_t*>(base) + at, 16); }
   TACO_DEV void load(const void* base, int64_t at, int n) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
     if (n >= 8) {
@@ -49,6 +52,13 @@ struct Oct<kBF16> {
 template <>
 struct Oct<kF32> {
   f32x4 lo, hi;
+  TACO_DEV void clear() { lo = hi = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+  TACO_DEV void opaque() { asm volatile("" : "+v"(lo), "+v"(hi)); }
+  TACO_DEV void load(const void* base, int64_t at) {
+    const float* p = static_cast<const float*>(base) + at;
+    __builtin_memcpy(&lo, p, 16);
+    __builtin_memcpy(&hi, p + 4, 16);
+  }
   TACO_DEV void load(const void* base, int64_t at, int n) {
     const float* p = static_cast<const float*>(base) + at;
     if (n >= 8) {
@@ -83,6 +93,7 @@ TACO_DEV void load8(const void* base, int dt, int64_t at, int n, float* f) {
     o.get(f);
   }
 }
+TACO_DEV void load8(const void* base, int dt, int64_t at, float* f) { load8(base, dt, at, 8, f); }
 TACO_DEV void store8(void* base, int dt, int64_t at, int n, const float* f) {
   if (dt == kBF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + at;
@@ -106,16 +117,37 @@ TACO_DEV void store8(void* base, int dt, int64_t at, int n, const float* f) {
     }
   }
 }
+TACO_DEV void store8(void* base, int dt, int64_t at, const float* f) { store8(base, dt, at, 8, f); }
+TACO_DEV float load1(const void* base, int dt, int64_t at) {
+  return dt == kBF16 ? (float)static_cast<const __bf16*>(base)[at] : static_cast<const float*>(base)[at];
+}
 TACO_DEV void store1(void* base, int dt, int64_t at, float f) {
   if (dt == kBF16) static_cast<__bf16*>(base)[at] = (__bf16)f;
   else static_cast<float*>(base)[at] = f;
 }
 
-// Sum over the L lanes (a power of two) of an aligned group: every lane has it.
+// v plus the value of another lane of the same 16 (a DPP control).
+template <int CTRL>
+TACO_DEV float add_dpp(float v) {
+  const int i = __builtin_bit_cast(int, v);
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+}
+
+// Sum over the L lanes (16, 32 or 64) of an aligned group: every lane has it.
+// Inside 16 lanes by DPP, which costs an add each; a wave's four sixteens
+// through scalar registers.
 template <int L>
 TACO_DEV float lanes_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < L; m *= 2) v += __shfl_xor(v, m, kWave);
+  v = add_dpp<0xB1>(v);    // quad_perm 1 0 3 2
+  v = add_dpp<0x4E>(v);    // quad_perm 2 3 0 1
+  v = add_dpp<0x141>(v);   // row_half_mirror
+  v = add_dpp<0x140>(v);   // row_mirror
+  if constexpr (L == 32) v += __shfl_xor(v, 16, kWave);
+  if constexpr (L == 64) {
+    const int i = __builtin_bit_cast(int, v);
+    auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(i, l)); };
+    v = (lane(0) + lane(16)) + (lane(32) + lane(48));
+  }
   return v;
 }
 

@@ -22,12 +22,14 @@ struct NormArgs {
   int cols;
   float eps;
   float *mean, *rstd;   // nullable
+  int waves;            // that hold a row (set by launch_norm)
 };
 
-// Workgroups of the norm's backward pass: two for each CU of the device. Each
-// adds up the weight's gradient over its rows and writes one partial sum per
-// column, so their number is also what the workspace holds.
-constexpr int kNormBackGroups = 512;
+// Workgroups of the norm's kernels: two for each CU of the device. In the
+// backward pass each adds up the weight's gradient over its rows and writes
+// one partial sum per column, so their number is also what the workspace
+// holds.
+constexpr int kNormGroups = 512;
 
 struct NormBackArgs {
   Mat dy, x, weight, dx, dweight, dbias;
@@ -35,6 +37,7 @@ struct NormBackArgs {
   int cols;
   const float *mean, *rstd;
   float* partials;      // [groups][2][cols]
+  int waves;            // that hold a row (set by launch_norm_back)
 };
 
 enum Act : int { kActNone = 0, kActGelu = 1, kActSilu = 2, kActRelu = 3 };
@@ -89,13 +92,16 @@ struct ActBackArgs {
 int act_back_groups(int64_t M);
 
 int norm_back_groups(int64_t rows, int64_t cols);
-hipError_t launch_norm(const NormArgs& a, hipStream_t s);
-hipError_t launch_norm_back(const NormBackArgs& a, hipStream_t s);
+hipError_t launch_norm(NormArgs a, hipStream_t s);
+hipError_t launch_norm_back(NormBackArgs a, hipStream_t s);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
 hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s);
-// out [cols] = the sum of `count` rows of `in`, ld apart (zeros if count is 0).
-void launch_column_sum(const float* in, int64_t ld, int count, int64_t cols, const Mat& out, hipStream_t s);
+// out0 [cols] = the sum of `count` rows of `in`, ld apart, and out1 that of
+// the columns `second` floats further on (zeros if count is 0; each may be
+// absent).
+void launch_column_sum(const float* in, int64_t ld, int64_t second, int count, int64_t cols, const Mat& out0,
+                       const Mat& out1, hipStream_t s);
 
 }  // namespace taco

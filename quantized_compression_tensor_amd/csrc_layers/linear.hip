@@ -612,7 +612,7 @@ hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s) {
     if (a.gated) hipLaunchKernelGGL((k_act_back<true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_act_back<false>), grid, dim3(256), 0, s, a);
   }
-  launch_column_sum(a.partials, a.N, groups, a.N, a.dbias, s);
+  launch_column_sum(a.partials, a.N, 0, groups, a.N, a.dbias, Mat{nullptr, 0, kF32}, s);
   return hipGetLastError();
 }
 

@@ -69,9 +69,11 @@ def test_layer_norm_backward_refusals(want, kw):
 def test_norm_workspace():
     size = T.taco_layer_norm_backward_workspace_bytes
     assert size(0, 64) == 0 and size(-1, 64) == 0 and size(4, 0) == 0 and size(4, T.TACO_NORM_MAX_COLS + 1) == 0
-    assert size(1, 64) == 2 * 64 * 4                 # one workgroup takes 16 rows of 64
-    assert size(4, 1000) == 4 * 2 * 1000 * 4
-    assert size(1 << 20, 5120) == 512 * 2 * 5120 * 4  # and never more than 512 workgroups
+    # a partial sum of two vectors for each workgroup: one takes the rows that
+    # its sixteen waves hold at a time, and there are at most 512
+    assert size(1, 64) == size(64, 64) == 2 * 64 * 4 and size(65, 64) == 2 * 2 * 64 * 4
+    assert size(8, 1000) == 2 * 1000 * 4 and size(9, 1000) == 2 * 2 * 1000 * 4
+    assert size(7, 5120) == 7 * 2 * 5120 * 4 and size(1 << 20, 5120) == 512 * 2 * 5120 * 4
 
 
 def test_binding_refuses_other_tensors():
