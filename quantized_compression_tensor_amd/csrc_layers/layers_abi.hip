@@ -124,7 +124,7 @@ struct BackwardSpace {
 // Forward pass of either kind of projection; `wide`: rows of w.
 int linear_forward(const Checked& cx, const Checked& cw, const Epilogue& e, bool gated, int64_t m, int64_t n,
                    int64_t k, void* ws, hipStream_t stream) {
-  const GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e, 1, k, nullptr, 0};
+  const GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e, 1, k, nullptr, 0, 0};
   clear_stale_error();
   return hip_status(launch_gemm(g, ws, stream));
 }
@@ -150,14 +150,14 @@ int linear_backward(const Checked& cdout, const Checked& cx, const Checked& cw, 
   }
   if (cdx.m.p && m > 0) {
     const GemmArgs g = {dz, operand(cw, true), m, (int)k, wide, false, {kAbsent, kAbsent, kAbsent, cdx.m, kActNone},
-                        1, wide, nullptr, 0};
+                        1, wide, nullptr, 0, 0};
     const hipError_t err = launch_gemm(g, rest, stream);
     if (err != hipSuccess) return TACO_ERR_HIP;
   }
   if (cdw.m.p) {
     dz.by_k = true;
     const GemmArgs g = {dz, operand(cx, true), wide, (int)k, m, false, {kAbsent, kAbsent, kAbsent, cdw.m, kActNone},
-                        1, m, nullptr, 0};
+                        1, m, nullptr, 0, 0};
     const hipError_t err = launch_gemm(g, rest, stream);
     if (err != hipSuccess) return TACO_ERR_HIP;
   }

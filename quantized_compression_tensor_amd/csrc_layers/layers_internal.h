@@ -75,6 +75,7 @@ struct GemmArgs {
   int64_t part;
   float* partials;
   int64_t ld_partials;
+  int cols;   // output columns of a workgroup, for few rows
 };
 
 // dz = dout * act'(z) (gated: both halves), and the column sums of dz.

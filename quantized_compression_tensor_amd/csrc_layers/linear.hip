@@ -5,6 +5,7 @@
 // in float32 on the bf16 matrix cores. An operand lies in memory with its k
 // contiguous (x and W of the forward pass) or with its rows contiguous (W for
 // dx = dz W, dz and x for dw = dz^T x).
+#include <algorithm>
 #include <type_traits>
 
 #include "layers_device.h"
@@ -477,6 +478,104 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
   }
 }
 
+// --------------------------------------------------------------- few rows --
+
+// Up to 32 rows of x: the weight's bytes bound it, so every weight is read
+// once, straight into the registers of a 16 x 16 x 32 product whose other
+// operand is x (rows past the last one repeat it; their sums are not stored).
+// A workgroup takes up to 16 weight rows (gated: eight of each projection;
+// as many as give every CU the same number of workgroups), its sixteen waves units of 64 k in turn, so that a row's bytes are read 2 KiB at
+// a time, two units of a wave together. The waves' sums are joined in LDS.
+// Rows may start anywhere. One row, 8192 x 8192 weights: 27.8 us, 4.8 TB/s
+// (eight waves with eight units each 31.8 us); 4096 x 4096: 7.9 us.
+constexpr int kFewRows = 32, kFewWaves = 16;
+
+template <int TM, bool GATED>
+__global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
+  constexpr int kUnits = 2;   // of a wave, loaded together
+  __shared__ float parts[kFewWaves][TM][4 * kWave];
+  __shared__ float sums[16 * TM][16];
+  const int tid = (int)threadIdx.x, lane = tid & (kWave - 1), wave = wave_in_group();
+  const int n0 = (int)blockIdx.x * a.cols, r = lane & 15;
+  const int cols = a.N - n0 < a.cols ? a.N - n0 : a.cols;   // of this workgroup; lanes past them repeat the last
+  int n = GATED ? r & 7 : r;
+  n = n0 + (n < cols ? n : cols - 1);
+  const uint16_t* pw = a.b.p + (GATED && r >= 8 ? n + (int64_t)a.N : n) * a.b.ld + 8 * (lane >> 4);
+  const uint16_t* px[TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    const int64_t m = 16 * t + r;
+    px[t] = a.a.p + (m < a.M ? m : a.M - 1) * a.a.ld + 8 * (lane >> 4);
+  }
+  f32x4 acc[TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto product = [&](const Oct<kBF16>& w, const Oct<kBF16>& x, int t) {
+    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v), __builtin_bit_cast(bf16x8, x.v),
+                                                     acc[t], 0, 0, 0);
+  };
+  const int units = (int)(a.K / 64);
+  for (int first = wave; first < units; first += kFewWaves * kUnits) {
+    Oct<kBF16> w[kUnits][2], x[kUnits][TM][2];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int unit = first + u * kFewWaves;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[u][h].clear();
+        if (unit < units) w[u][h].load(pw, 64 * (int64_t)unit + 32 * h);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          x[u][t][h].clear();
+          if (unit < units) x[u][t][h].load(px[t], 64 * (int64_t)unit + 32 * h);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) product(w[u][h], x[u][t][h], t);
+  }
+  if (wave == units % kFewWaves) {
+    // the last k, fewer than 64
+    for (int64_t k = 64 * (int64_t)units; k < a.K; k += 32) {
+      const int64_t left = a.K - k - 8 * (lane >> 4);
+      const int count = left > 8 ? 8 : left > 0 ? (int)left : 0;
+      Oct<kBF16> w, x;
+      w.load(pw, k, count);
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        x.load(px[t], k, count);
+        product(w, x, t);
+      }
+    }
+  }
+  // accumulator e of lane l holds weight row 4 (l / 16) + e, row l % 16 of x
+#pragma unroll
+  for (int t = 0; t < TM; ++t) *reinterpret_cast<f32x4*>(&parts[wave][t][4 * lane]) = acc[t];
+  __syncthreads();
+  for (int i = tid; i < TM * 4 * kWave; i += kFewWaves * kWave) {
+    const int t = i / (4 * kWave), q = i % (4 * kWave), l = q / 4;
+    float z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) z += parts[w][t][q];
+    sums[16 * t + l % 16][4 * (l / 16) + q % 4] = z;
+  }
+  __syncthreads();
+  const int m = GATED ? tid : tid / 2, c = GATED ? 0 : tid % 2 * 8;
+  if (m >= a.M || m >= 16 * TM || c >= cols) return;
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    z[e] = sums[m][c + e];
+    u[e] = sums[m][(c + 8 + e) % 16];
+  }
+  if (GATED) finish_gated(a.e, a.N, m, n0, cols, z, u);
+  else finish(a.e, m, n0 + c, cols - c, z);
+}
+
 // ----------------------------------------------------------------- launch --
 
 // Which tiles a product takes and into how many parts its K is cut. Decided by
@@ -488,6 +587,16 @@ struct Plan {
 };
 
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
+
+// Both operands with k contiguous and few rows of the first. Every workgroup
+// reads all of x, so tiles are faster where rows times weights are many (16
+// rows of 8192 x 8192: 33.2 against 39.5 us; 8 of 5120 x 20480: 46.5 against
+// 53.7), and not where they are few (8 of 8192 x 8192: 30.8 against 32.7 us;
+// 24 of 3456 x 5120: 15.6 against 19.9).
+static bool few_rows(const GemmArgs& a) {
+  const int64_t weights = (a.gated ? 2 : 1) * (int64_t)a.N * a.K;
+  return !a.a.by_k && !a.b.by_k && (a.M <= 4 || (a.M <= kFewRows && weights * a.M <= int64_t(1) << 29));
+}
 
 static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
   Plan p = {tiles_of(M, N, 256, gated ? 128 : 256) >= 192, 1, (K + 63) / 64 * 64};
@@ -528,8 +637,29 @@ static void launch_tiles(const GemmArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_gemm<TL, true, true, false, DIRECT>), grid, block, lds, s, a);
 }
 
+static void launch_few_rows(GemmArgs a, hipStream_t s) {
+  // as many columns for a workgroup as give each CU the same number of them
+  // (one row, 5120 x 20480: 41.9 us with 512 workgroups of 10 columns, 52.6
+  // with 320 of 16); a few workgroups more than that run beside the others
+  const int most = a.gated ? 8 : 16, cus = device_cu_count();
+  const int groups = (a.N + most - 1) / most, rounds = std::max(1, (groups - cus / 8 + cus - 1) / cus);
+  a.cols = std::min(most, (a.N + rounds * cus - 1) / (rounds * cus));
+  const dim3 grid((unsigned)((a.N + a.cols - 1) / a.cols)), block(kFewWaves * kWave);
+  if (a.M <= 16) {
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_few_rows<1, false>), grid, block, 0, s, a);
+  } else {
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_few_rows<2, false>), grid, block, 0, s, a);
+  }
+}
+
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
+  if (few_rows(a)) {
+    launch_few_rows(a, s);
+    return hipGetLastError();
+  }
   const Plan p = plan_of(a.M, a.N, a.K, a.gated);
   a.splits = p.splits;
   a.part = p.part;
