@@ -311,7 +311,8 @@ int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, cons
  * of a wider tensor can be given. `data` NULL: the array is absent, where a
  * function says that it may be. Arrays need the alignment of their elements
  * (not 16 bytes); rows that start on 16 bytes and hold a multiple of 8
- * elements are read fastest. Vectors (weight, bias) have one row: their stride
+ * elements are read fastest (the projections copy x and w into the workspace
+ * otherwise). Vectors (weight, bias) have one row: their stride
  * is not looked at.
  * Errors, for every function here: TACO_ERR_FORMAT for an element type or an
  * activation that it does not take; TACO_ERR_SHAPE for a stride below the
@@ -319,7 +320,8 @@ int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, cons
  * TACO_ERR_INVALID_ARG for sizes below zero, tensors above 2^35 elements, a
  * missing array or an output that overlaps an input or another output;
  * TACO_ERR_ALIGN; TACO_ERR_WORKSPACE for a workspace that is missing, smaller
- * than the function's *_workspace_bytes or not 16-byte aligned. Workspaces are
+ * than the call needs or not 16-byte aligned. The function's *_workspace_bytes
+ * is enough for arrays of any alignment and all outputs. Workspaces are
  * scratch: nothing is kept in them between calls, they need no clearing, and
  * calls that may run at the same time need one each. Results do not depend on
  * timing: the same call gives the same bits. Inputs may hold infinities and

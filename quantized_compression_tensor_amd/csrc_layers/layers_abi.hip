@@ -107,61 +107,139 @@ Operand operand(const Checked& c, bool by_k) { return Operand{static_cast<const 
 
 constexpr Mat kAbsent = {nullptr, 0, TACO_F32};
 
-// The workspace of a backward pass: dz as bf16 [m, wide] with rows on 16
-// bytes; then, in turn, the partial column sums for dbias [groups][n] and the
-// products' partial sums.
-struct BackwardSpace {
-  int64_t ld_dz;
-  size_t dz_bytes, rest_bytes;
-  BackwardSpace(int64_t m, int64_t wide, int64_t n, int64_t k)
-      : ld_dz((wide + 7) / 8 * 8),
-        dz_bytes(((size_t)(m * ld_dz) * 2 + 255) / 256 * 256),
-        rest_bytes(std::max({(size_t)act_back_groups(m) * (size_t)n * 4, gemm_partial_bytes(m, k, wide, false),
-                             gemm_partial_bytes(wide, k, m, false)})) {}
-  size_t total() const { return dz_bytes + rest_bytes; }
-};
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Forward pass of either kind of projection; `wide`: rows of w.
-int linear_forward(const Checked& cx, const Checked& cw, const Epilogue& e, bool gated, int64_t m, int64_t n,
-                   int64_t k, void* ws, hipStream_t stream) {
-  const GemmArgs g = {operand(cx, false), operand(cw, false), m, (int)n, k, gated, e, 1, k, nullptr, 0, 0};
-  clear_stale_error();
-  return hip_status(launch_gemm(g, ws, stream));
+// Whether the tiles can be loaded from where a matrix lies: rows on 16 bytes,
+// whole eights in each.
+bool in_place(const Mat& m, int64_t cols) {
+  return aligned16(m.p) && m.ld % 8 == 0 && cols % 8 == 0;
 }
 
-// Backward pass of either kind: dz, then dx = dz W and dw = dz^T x.
-int linear_backward(const Checked& cdout, const Checked& cx, const Checked& cw, int act, const Checked& cz,
-                    const Checked& cdx, const Checked& cdw, const Checked& cdb, bool gated, int64_t m, int64_t n,
-                    int64_t k, void* ws, hipStream_t stream) {
-  const int64_t wide = gated ? 2 * n : n;
-  const BackwardSpace space(m, wide, gated ? 0 : n, k);
-  void* rest = static_cast<char*>(ws) + space.dz_bytes;
-  Operand dz = operand(cdout, false);
-  clear_stale_error();
-  if (gated || act != TACO_ACT_NONE || cdb.m.p) {
-    ActBackArgs b = {cdout.m, cz.m, m, (int)n, act, gated, nullptr, space.ld_dz, nullptr, cdb.m};
-    if (gated || act != TACO_ACT_NONE) {
-      b.dz = static_cast<uint16_t*>(ws);
-      dz = Operand{b.dz, space.ld_dz, false};
+// Takes parts of a workspace, each a multiple of 256 bytes; without a base it
+// only counts.
+struct Space {
+  char* base;
+  size_t used;
+  void* take(size_t bytes) {
+    void* p = base ? base + used : nullptr;
+    used += (size_t)up((int64_t)bytes, 256);
+    return p;
+  }
+};
+
+// What a pass over a call is for: the workspace that arrays of any alignment
+// would need with all outputs asked for, the workspace that this call needs,
+// or its launches.
+enum Pass { kSizeOfAny, kSize, kRun };
+
+// A bf16 matrix [rows, cols] as an operand: in place, or packed into `space`
+// (added to `pack`).
+Operand packed(const Mat& m, int64_t rows, int64_t cols, bool by_k, bool whole, Space* space, PackArgs* pack) {
+  if (whole) return Operand{static_cast<const uint16_t*>(m.p), m.ld, by_k};
+  const int64_t ld = up(cols, 8);
+  uint16_t* dst = static_cast<uint16_t*>(space->take((size_t)(rows * ld) * 2));
+  pack->m[pack->count++] = {m, rows, cols, dst, ld};
+  return Operand{dst, ld, by_k};
+}
+
+// A call of either kind of projection: what it needs of the workspace, and
+// its launches. `wide`: rows of w.
+struct Forward {
+  Checked x, w;
+  Epilogue e;
+  bool gated;
+  int64_t m, n, k;
+  hipError_t pass(Pass what, Space* space, hipStream_t stream) const {
+    const bool worst = what == kSizeOfAny;
+    const int64_t wide = gated ? 2 * n : n;
+    const bool few = few_rows(m, n, k, gated);
+    PackArgs pack = {};
+    GemmArgs g = {};
+    g.a = packed(x.m, m, k, false, few || (!worst && in_place(x.m, k)), space, &pack);
+    g.b = packed(w.m, wide, k, false, few || (!worst && in_place(w.m, k)), space, &pack);
+    g.M = m; g.N = (int)n; g.K = k; g.gated = gated; g.e = e;
+    void* partials = space->take(few ? 0 : gemm_partial_bytes(m, n, k, gated));
+    if (what != kRun) return hipSuccess;
+    if (pack.count > 0) {
+      const hipError_t err = launch_pack(pack, stream);
+      if (err != hipSuccess) return err;
     }
-    if (cdb.m.p) b.partials = static_cast<float*>(rest);
-    const hipError_t err = launch_act_back(b, stream);
-    if (err != hipSuccess) return TACO_ERR_HIP;
+    return launch_gemm(g, partials, stream);
   }
-  if (cdx.m.p && m > 0) {
-    const GemmArgs g = {dz, operand(cw, true), m, (int)k, wide, false, {kAbsent, kAbsent, kAbsent, cdx.m, kActNone},
-                        1, wide, nullptr, 0, 0};
-    const hipError_t err = launch_gemm(g, rest, stream);
-    if (err != hipSuccess) return TACO_ERR_HIP;
+};
+
+struct Backward {
+  Checked dout, x, w, z, dx, dw, db;
+  int act;
+  bool gated;
+  int64_t m, n, k;
+  hipError_t pass(Pass what, Space* space, hipStream_t stream) const {
+    const bool worst = what == kSizeOfAny;
+    const int64_t wide = gated ? 2 * n : n, ld_dz = up(wide, 8);
+    const bool want_dx = worst || (dx.m.p && m > 0), want_dw = worst || dw.m.p, want_db = !gated && (worst || db.m.p);
+    // dz is dout itself where there is no activation and the tiles can take it
+    const bool own_dz = worst || gated || act != TACO_ACT_NONE || ((want_dx || want_dw) && !in_place(dout.m, n));
+    PackArgs pack = {};
+    ActBackArgs b = {};
+    b.dout = dout.m; b.z = z.m; b.M = m; b.N = (int)n; b.act = act; b.gated = gated; b.ld_dz = ld_dz; b.dbias = db.m;
+    Operand dz = {static_cast<const uint16_t*>(dout.m.p), dout.m.ld, false};
+    if (own_dz) {
+      b.dz = static_cast<uint16_t*>(space->take((size_t)(m * ld_dz) * 2));
+      dz = Operand{b.dz, ld_dz, false};
+    }
+    Operand ox = {}, ow = {};
+    if (want_dw) ox = packed(x.m, m, k, true, !worst && in_place(x.m, k), space, &pack);
+    if (want_dx) ow = packed(w.m, wide, k, true, !worst && in_place(w.m, k), space, &pack);
+    // used in turn
+    const size_t dx_bytes = want_dx ? gemm_partial_bytes(m, k, wide, false) : 0;
+    const size_t dw_bytes = want_dw ? gemm_partial_bytes(wide, k, m, false) : 0;
+    const size_t db_bytes = want_db ? (size_t)act_back_groups(m) * (size_t)n * sizeof(float) : 0;
+    void* rest = space->take(std::max({dx_bytes, dw_bytes, db_bytes}));
+    if (what != kRun) return hipSuccess;
+    if (want_db) b.partials = static_cast<float*>(rest);
+    hipError_t err = hipSuccess;
+    if (own_dz || want_db) err = launch_act_back(b, stream);
+    if (err == hipSuccess && pack.count > 0) err = launch_pack(pack, stream);
+    GemmArgs g = {};
+    g.e.act = kActNone;
+    if (err == hipSuccess && want_dx) {
+      g.a = dz; g.b = ow; g.M = m; g.N = (int)k; g.K = wide; g.e.out = dx.m;
+      err = launch_gemm(g, rest, stream);
+    }
+    if (err == hipSuccess && want_dw) {
+      dz.by_k = true;
+      g.a = dz; g.b = ox; g.M = wide; g.N = (int)k; g.K = m; g.e.out = dw.m;
+      err = launch_gemm(g, rest, stream);
+    }
+    return err;
   }
-  if (cdw.m.p) {
-    dz.by_k = true;
-    const GemmArgs g = {dz, operand(cx, true), wide, (int)k, m, false, {kAbsent, kAbsent, kAbsent, cdw.m, kActNone},
-                        1, m, nullptr, 0, 0};
-    const hipError_t err = launch_gemm(g, rest, stream);
-    if (err != hipSuccess) return TACO_ERR_HIP;
-  }
-  return TACO_OK;
+};
+
+template <class Call>
+size_t space_of(const Call& c, Pass what) {
+  Space s = {nullptr, 0};
+  (void)c.pass(what, &s, nullptr);
+  return s.used;
+}
+
+template <class Call>
+int run(const Call& c, void* ws, hipStream_t stream) {
+  Space s = {static_cast<char*>(ws), 0};
+  clear_stale_error();
+  return hip_status(c.pass(kRun, &s, stream));
+}
+
+size_t forward_bytes(bool gated, int64_t m, int64_t n, int64_t k) {
+  if (check_linear_sizes(m, n, gated ? 2 * n : n, k) != TACO_OK) return 0;
+  Forward f = {};
+  f.gated = gated; f.m = m; f.n = n; f.k = k;
+  return space_of(f, kSizeOfAny);
+}
+size_t backward_bytes(bool gated, int64_t m, int64_t n, int64_t k) {
+  if (check_linear_sizes(m, n, gated ? 2 * n : n, k) != TACO_OK) return 0;
+  Backward b = {};
+  b.gated = gated; b.m = m; b.n = n; b.k = k;
+  return space_of(b, kSizeOfAny);
 }
 
 }  // namespace
@@ -215,9 +293,7 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
   return hip_status(launch_norm_back(a, stream));
 }
 
-size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return check_linear_sizes(M, N, N, K) == TACO_OK ? gemm_partial_bytes(M, N, K, false) : 0;
-}
+size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return forward_bytes(false, M, N, K); }
 
 int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_array residual, taco_array out,
                 taco_array preact, int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
@@ -229,17 +305,16 @@ int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_a
   const Checked cx = check_operand(x, M, K), cw = check_operand(w, N, K), cb = check_vector(bias, N, kOptional);
   const Checked cr = check_array(residual, M, N, kOptional), co = check_array(out, M, N, kRequired);
   const Checked cz = check_array(preact, M, N, kOptional);
-  const Checked cws = check_workspace(workspace, ws_bytes, taco_linear_workspace_bytes(M, N, K));
-  st = first_error({&cx, &cw, &cb, &cr, &co, &cz, &cws});
+  st = first_error({&cx, &cw, &cb, &cr, &co, &cz});
   if (st != TACO_OK) return st;
+  const Forward f = {cx, cw, {cb.m, cr.m, cz.m, co.m, act}, false, M, N, K};
+  const Checked cws = check_workspace(workspace, ws_bytes, space_of(f, kSize));
+  if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cx, &cw, &cb, &cr}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
-  if (M == 0) return TACO_OK;
-  return linear_forward(cx, cw, {cb.m, cr.m, cz.m, co.m, act}, false, M, N, K, workspace, stream);
+  return M == 0 ? TACO_OK : run(f, cws.m.p, stream);
 }
 
-size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-  return check_linear_sizes(M, F, 2 * F, K) == TACO_OK ? gemm_partial_bytes(M, F, K, true) : 0;
-}
+size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) { return forward_bytes(true, M, F, K); }
 
 int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, taco_array preact, int64_t M,
                       int64_t F, int64_t K, void* workspace, size_t ws_bytes, hipStream_t stream) {
@@ -249,18 +324,16 @@ int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, t
   if (st != TACO_OK) return st;
   const Checked cx = check_operand(x, M, K), cw = check_operand(w, 2 * F, K);
   const Checked co = check_array(out, M, F, kRequired), cz = check_array(preact, M, 2 * F, kOptional);
-  const Checked cws = check_workspace(workspace, ws_bytes, taco_gated_linear_workspace_bytes(M, F, K));
-  st = first_error({&cx, &cw, &co, &cz, &cws});
+  st = first_error({&cx, &cw, &co, &cz});
   if (st != TACO_OK) return st;
+  const Forward f = {cx, cw, {kAbsent, kAbsent, cz.m, co.m, act}, true, M, F, K};
+  const Checked cws = check_workspace(workspace, ws_bytes, space_of(f, kSize));
+  if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cx, &cw}, {&co, &cz, &cws})) return TACO_ERR_INVALID_ARG;
-  if (M == 0) return TACO_OK;
-  return linear_forward(cx, cw, {kAbsent, kAbsent, cz.m, co.m, act}, true, M, F, K, workspace, stream);
+  return M == 0 ? TACO_OK : run(f, cws.m.p, stream);
 }
 
-size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_linear_sizes(M, N, N, K) != TACO_OK) return 0;
-  return BackwardSpace(M, N, N, K).total();
-}
+size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { return backward_bytes(false, M, N, K); }
 
 int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
                          taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -273,17 +346,18 @@ int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t ac
   const Checked cz = check_array(preact, M, N, act == TACO_ACT_NONE ? kOptional : kRequired);
   const Checked cdx = check_array(dx, M, K, kOptional), cdw = check_array(dw, N, K, kOptional);
   const Checked cdb = check_vector(dbias, N, kOptional);
-  const Checked cws = check_workspace(workspace, ws_bytes, taco_linear_backward_workspace_bytes(M, N, K));
-  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cdb, &cws});
+  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cdb});
   if (st != TACO_OK) return st;
   if (!dx.data && !dw.data && !dbias.data) return TACO_ERR_INVALID_ARG;
+  const Backward b = {cd, cx, cw, cz, cdx, cdw, cdb, act, false, M, N, K};
+  const Checked cws = check_workspace(workspace, ws_bytes, space_of(b, kSize));
+  if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cdb, &cws})) return TACO_ERR_INVALID_ARG;
-  return linear_backward(cd, cx, cw, act, cz, cdx, cdw, cdb, false, M, N, K, workspace, stream);
+  return run(b, cws.m.p, stream);
 }
 
 size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K) {
-  if (check_linear_sizes(M, F, 2 * F, K) != TACO_OK) return 0;
-  return BackwardSpace(M, 2 * F, 0, K).total();
+  return backward_bytes(true, M, F, K);
 }
 
 int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
@@ -296,13 +370,14 @@ int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int3
   const Checked cd = check_operand(dout, M, F), cx = check_operand(x, M, K), cw = check_operand(w, 2 * F, K);
   const Checked cz = check_array(preact, M, 2 * F, kRequired);
   const Checked cdx = check_array(dx, M, K, kOptional), cdw = check_array(dw, 2 * F, K, kOptional);
-  const Checked cws = check_workspace(workspace, ws_bytes, taco_gated_linear_backward_workspace_bytes(M, F, K));
-  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cws});
+  st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw});
   if (st != TACO_OK) return st;
   if (!dx.data && !dw.data) return TACO_ERR_INVALID_ARG;
+  const Backward b = {cd, cx, cw, cz, cdx, cdw, {kAbsent, 0, TACO_OK}, act, true, M, F, K};
+  const Checked cws = check_workspace(workspace, ws_bytes, space_of(b, kSize));
+  if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cws})) return TACO_ERR_INVALID_ARG;
-  const Checked none = {kAbsent, 0, TACO_OK};
-  return linear_backward(cd, cx, cw, act, cz, cdx, cdw, none, true, M, F, K, workspace, stream);
+  return run(b, cws.m.p, stream);
 }
 
 }  // extern "C"

@@ -52,12 +52,27 @@ struct Epilogue {
 };
 
 // One operand of a matrix product, bf16: element (i, k) of its [rows, K] view
-// is p[i * ld + k], or p[k * ld + i] if `by_k` (rows contiguous).
+// is p[i * ld + k], or p[k * ld + i] if `by_k` (rows contiguous). Except for
+// few rows, lines start on 16 bytes and may be read to the next multiple of
+// eight elements, which hold zeros past the last k (k contiguous).
 struct Operand {
   const uint16_t* p;
   int64_t ld;
   bool by_k;
 };
+
+// Up to two matrices to be copied with rows on 16 bytes and zeros up to the
+// next multiple of eight elements.
+struct PackArgs {
+  struct One {
+    Mat src;
+    int64_t rows, cols;
+    uint16_t* dst;
+    int64_t ld;   // a multiple of 8, at least cols
+  } m[2];
+  int count;
+};
+hipError_t launch_pack(const PackArgs& a, hipStream_t s);
 
 // z[M, N] = a b^T over K, then the epilogue. With `gated`, N counts the output
 // columns, b has 2 N rows (the gate's first) and the epilogue is
@@ -95,6 +110,9 @@ int act_back_groups(int64_t M);
 int norm_back_groups(int64_t rows, int64_t cols);
 hipError_t launch_norm(NormArgs a, hipStream_t s);
 hipError_t launch_norm_back(NormBackArgs a, hipStream_t s);
+// Whether a forward product of this size takes the kernel for few rows, which
+// takes operands as they are.
+bool few_rows(int64_t M, int64_t N, int64_t K, bool gated);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);

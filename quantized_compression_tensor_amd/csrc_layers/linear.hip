@@ -19,10 +19,40 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------ activations --
 
+// Phi(z), the normal distribution's function, and e = exp(-z^2 / 2). For z < 0
+// Phi = erfc(x) / 2 with x = |z| / sqrt(2), and erfc(x) = t Q(t) exp(-x^2),
+// t = 1 / (1 + p x): Q is a polynomial of degree 8 fitted to
+// exp(x^2) erfc(x) / t over x in [0, 9.5] by iteratively reweighted least
+// squares, relative error below 1.2e-8; for z > 0 Phi = 1 - that. In float32
+// Phi is within 2.1e-7, and within 2e-6 of its value for |z| < 6 (the rounding
+// of exp's argument). About 20 instructions; erff takes two to three times as
+// many, which showed in the epilogue and bound the backward pass.
+TACO_DEV float normal_cdf(float z, float* e) {
+  constexpr float kHalfLog2E = 0.72134752044448170f, kP = 0.26516504294495535f;   // kP = 0.375 / sqrt(2)
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(kP, __builtin_fabsf(z), 1.0f));
+  float q = 0.0616967704f;
+  q = __builtin_fmaf(q, t, -0.288076138f);
+  q = __builtin_fmaf(q, t, 0.433895343f);
+  q = __builtin_fmaf(q, t, -0.231078206f);
+  q = __builtin_fmaf(q, t, 0.274845342f);
+  q = __builtin_fmaf(q, t, 0.121038450f);
+  q = __builtin_fmaf(q, t, 0.205430551f);
+  q = __builtin_fmaf(q, t, 0.210633482f);
+  q = __builtin_fmaf(q, t, 0.211614416f);
+  *e = __builtin_amdgcn_exp2f(-(z * z) * kHalfLog2E);
+  const float h = 0.5f * t * q * *e;
+  return z < 0.0f ? h : 1.0f - h;
+}
+// 1 / (1 + exp(-z)), to a few units in the last place.
+TACO_DEV float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
 TACO_DEV float act_value(float t, int act) {
+  float e;
   switch (act) {
-    case kActGelu: return 0.5f * t * (1.0f + erff(t * 0.70710678118654752f));
-    case kActSilu: return t / (1.0f + expf(-t));
+    case kActGelu: return t * normal_cdf(t, &e);
+    case kActSilu: return t * sigmoid(t);
     case kActRelu: return t < 0.0f ? 0.0f : t;   // NaN stays
     default: return t;
   }
@@ -31,14 +61,33 @@ TACO_DEV float act_value(float t, int act) {
 // act'(t): Phi(t) + t phi(t); s (1 + t (1 - s)) with s = 1 / (1 + exp(-t)); t > 0.
 TACO_DEV float act_slope(float t, int act) {
   switch (act) {
-    case kActGelu:
-      return 0.5f * (1.0f + erff(t * 0.70710678118654752f)) + t * (expf(-0.5f * t * t) * 0.39894228040143268f);
+    case kActGelu: {
+      float e;
+      const float cdf = normal_cdf(t, &e);
+      return __builtin_fmaf(t * e, 0.39894228040143268f, cdf);
+    }
     case kActSilu: {
-      const float s = 1.0f / (1.0f + expf(-t));
-      return s * (1.0f + t * (1.0f - s));
+      const float s = sigmoid(t);
+      return s * __builtin_fmaf(t, 1.0f - s, 1.0f);
     }
     case kActRelu: return t > 0.0f ? 1.0f : 0.0f;
     default: return 1.0f;
+  }
+}
+// Both of the gated layer's, with what they share.
+TACO_DEV void act_both(float t, int act, float* value, float* slope) {
+  if (act == kActGelu) {
+    float e;
+    const float cdf = normal_cdf(t, &e);
+    *value = t * cdf;
+    *slope = __builtin_fmaf(t * e, 0.39894228040143268f, cdf);
+  } else if (act == kActSilu) {
+    const float s = sigmoid(t);
+    *value = t * s;
+    *slope = s * __builtin_fmaf(t, 1.0f - s, 1.0f);
+  } else {
+    *value = act_value(t, act);
+    *slope = act_slope(t, act);
   }
 }
 
@@ -177,13 +226,13 @@ TACO_DEV void load_to_lds(rsrc_t r, int off, uint16_t* t) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (TACO_LDS void*)t, 16, off, 0, 0, 0);
 }
 
-// Straight into LDS, 16 bytes per lane without passing the registers. Wants
-// rows on 16 bytes and a multiple of 8 elements along the contiguous axis.
-// What lies outside the operand reads as zeros: past its last row by the size
-// of the buffer resource, past its last k (k contiguous) by an offset that is
-// outside it.
+// Moves an operand's tiles straight into LDS, 16 bytes per lane without
+// passing the registers. Wants rows on 16 bytes and eights along the
+// contiguous axis (k_pack makes others so). What lies outside the operand
+// reads as zeros: past its last row by the size of the buffer resource, past
+// its last k (k contiguous) by an offset that is outside it.
 template <bool BY_K, int R, int NT, bool GATED>
-struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
+struct Loader : Chunks<BY_K, R, NT, GATED> {
   using C = Chunks<BY_K, R, NT, GATED>;
   static constexpr int BK = C::BK;
   static constexpr int kOutside = 0x7FFFFFF0;
@@ -195,7 +244,8 @@ struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
   TACO_DEV void init(const uint16_t* base, const uint16_t* base2, int64_t ld, int rows, int64_t K, int tid) {
     p = reinterpret_cast<const char*>(base);
     p2 = reinterpret_cast<const char*>(base2);
-    bytes = 2 * (BY_K ? (K - 1) * ld + rows : (rows - 1) * ld + K);
+    // whole eights along the contiguous axis: what lies past it is readable
+    bytes = 2 * (BY_K ? (K - 1) * ld + (rows + 7) / 8 * 8 : (rows - 1) * ld + (K + 7) / 8 * 8);
     step = 2 * (BY_K ? BK * ld : BK);
     chunk_k = BY_K ? 0 : 8 * C::chunk(tid, 0);
 #pragma unroll
@@ -212,47 +262,6 @@ struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
       p2 += step;
       bytes -= step;
     }
-  }
-};
-
-// Through registers, for rows that start anywhere.
-template <bool BY_K, int R, int NT, bool GATED>
-struct StagedLoader : Chunks<BY_K, R, NT, GATED> {
-  using C = Chunks<BY_K, R, NT, GATED>;
-  static constexpr int BK = C::BK;
-  const uint16_t *p, *p2;
-  int64_t ld;
-  int rows, tid;
-  u32x4 reg[C::kPer];
-  TACO_DEV void init(const uint16_t* base, const uint16_t* base2, int64_t ld_, int rows_, int64_t, int tid_) {
-    p = base;
-    p2 = base2;
-    ld = ld_;
-    rows = rows_;
-    tid = tid_;
-  }
-  TACO_DEV void load(int wave, int64_t left) {
-    const bool whole = rows >= (GATED ? R / 2 : R) && left >= BK;
-#pragma unroll
-    for (int i = 0; i < C::kPer; ++i) {
-      const int c = 8 * C::chunk(tid, i), l = C::line(tid, i), r = BY_K ? c : C::row(l), k = BY_K ? l : c;
-      const uint16_t* at = (C::second(wave, i) ? p2 : p) + (BY_K ? k * ld + r : r * ld + k);
-      if (whole) {
-        __builtin_memcpy(&reg[i], at, 16);
-      } else {
-        const int64_t n = BY_K ? (k < left ? rows - r : 0) : (r < rows ? left - k : 0);
-        Oct<kBF16> o;
-        o.load(at, 0, n > 8 ? 8 : (int)n);
-        reg[i] = o.v;
-      }
-    }
-    const int64_t step = BY_K ? BK * ld : BK;
-    p += step;
-    p2 += step;
-  }
-  TACO_DEV void store(uint16_t* t) const {
-#pragma unroll
-    for (int i = 0; i < C::kPer; ++i) *reinterpret_cast<u32x4*>(t + (tid + i * NT) * 8) = reg[i];
   }
 };
 
@@ -291,7 +300,7 @@ TACO_DEV void hand_over() {
 // or two steps' time. The 16 x 16 x 32 products were faster than 32 x 32 x 16
 // (8192^3: 750 against 815 us) although they leave more gaps: this size is
 // bound by power, and they move half as many sums through the registers.
-template <class TL, bool AK, bool BK_, bool GATED, bool DIRECT>
+template <class TL, bool AK, bool BK_, bool GATED>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
@@ -312,8 +321,8 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   const uint16_t* pa = a.a.p + (AK ? m0 + k0 * a.a.ld : m0 * a.a.ld + k0);
   const uint16_t* pb = a.b.p + (BK_ ? n0 + k0 * a.b.ld : n0 * a.b.ld + k0);
   const uint16_t* pb2 = GATED ? pb + (int64_t)a.N * a.b.ld : pb;
-  using LA = std::conditional_t<DIRECT, DirectLoader<AK, BM, NT, false>, StagedLoader<AK, BM, NT, false>>;
-  using LB = std::conditional_t<DIRECT, DirectLoader<BK_, BN, NT, GATED>, StagedLoader<BK_, BN, NT, GATED>>;
+  using LA = Loader<AK, BM, NT, false>;
+  using LB = Loader<BK_, BN, NT, GATED>;
   LA la;
   LB lb;
   la.init(pa, pa, a.a.ld, rows_a, K, tid);
@@ -339,33 +348,23 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
     for (int j = 0; j < TN; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[kk][j], acc[i][j], 0, 0, 0);
   };
-  // Part `part` of `parts` of the loads of step ks into stage t; staged, the
-  // stage gets what was loaded a step ago and the next step's loads start.
+  // Part `part` of `parts` of the loads of step ks into stage t.
   auto load = [&](auto& l, int ks, uint16_t* t, int part, int parts) {
     constexpr int kPer = std::remove_reference_t<decltype(l)>::kPer;
-    if constexpr (DIRECT) {
-      const int each = (kPer + parts - 1) / parts;
+    const int each = (kPer + parts - 1) / parts;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i / each == part) l.issue(t, wave, K - (int64_t)ks * BK, i);
-    } else if (part == 0) {
-      if (ks < steps) l.store(t);
-      if (ks + 1 < steps) l.load(wave, K - (int64_t)(ks + 1) * BK);
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (i / each == part) l.issue(t, wave, K - (int64_t)ks * BK, i);
   };
   if (steps > 0) {
     uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
     uint16_t *b0 = lds_b, *b1 = lds_b + TL::kB;
-    if constexpr (!DIRECT) {
-      la.load(wave, K);
-      lb.load(wave, K);
-    }
     load(la, 0, a0, 0, 1);
     load(lb, 0, b0, 0, 1);
     load(la, 1, a1, 0, 1);
     load(lb, 1, b1, 0, 1);
     load(la, 2, a2, 0, 1);
-    hand_over<0, DIRECT ? 2 * LA::kPer + LB::kPer : -1>();
+    hand_over<0, 2 * LA::kPer + LB::kPer>();
 #pragma unroll
     for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
     read_b(b0, 0);
@@ -388,7 +387,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
         if (i == kFreeA) {
           // a0 has been read to its end, a1 and b1 are there; past the last
           // step what is read from them is not used
-          hand_over<0, DIRECT ? LA::kPer + LB::kPer : -1>();
+          hand_over<0, LA::kPer + LB::kPer>();
 #pragma unroll
           for (int q = 0; q < i; ++q) read_a(a1, 0, q);
         }
@@ -588,14 +587,14 @@ struct Plan {
 
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
 
-// Both operands with k contiguous and few rows of the first. Every workgroup
+// Whether a forward product takes the kernel for few rows. Every workgroup
 // reads all of x, so tiles are faster where rows times weights are many (16
 // rows of 8192 x 8192: 33.2 against 39.5 us; 8 of 5120 x 20480: 46.5 against
 // 53.7), and not where they are few (8 of 8192 x 8192: 30.8 against 32.7 us;
 // 24 of 3456 x 5120: 15.6 against 19.9).
-static bool few_rows(const GemmArgs& a) {
-  const int64_t weights = (a.gated ? 2 : 1) * (int64_t)a.N * a.K;
-  return !a.a.by_k && !a.b.by_k && (a.M <= 4 || (a.M <= kFewRows && weights * a.M <= int64_t(1) << 29));
+bool few_rows(int64_t M, int64_t N, int64_t K, bool gated) {
+  const int64_t weights = (gated ? 2 : 1) * N * K;
+  return M <= 4 || (M <= kFewRows && weights * M <= int64_t(1) << 29);
 }
 
 static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
@@ -621,20 +620,15 @@ size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
   return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)partial_ld(N, gated) * 4 : 0;
 }
 
-// Rows on 16 bytes, and a multiple of 8 elements along the contiguous axis.
-static bool direct(const Operand& o, int64_t rows, int64_t K) {
-  return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 && (o.by_k ? rows : K) % 8 == 0;
-}
-
-template <class TL, bool DIRECT>
+template <class TL>
 static void launch_tiles(const GemmArgs& a, hipStream_t s) {
   const int64_t tiles = tiles_of(a.M, a.N, TL::BM, a.gated ? TL::BN / 2 : TL::BN);
   const dim3 grid((unsigned)(tiles * a.splits)), block(TL::kThreads);
   constexpr size_t lds = TL::kLdsBytes;
-  if (a.gated) hipLaunchKernelGGL((k_gemm<TL, false, false, true, DIRECT>), grid, block, lds, s, a);
-  else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false, DIRECT>), grid, block, lds, s, a);
-  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false, DIRECT>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_gemm<TL, true, true, false, DIRECT>), grid, block, lds, s, a);
+  if (a.gated) hipLaunchKernelGGL((k_gemm<TL, false, false, true>), grid, block, lds, s, a);
+  else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false>), grid, block, lds, s, a);
+  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_gemm<TL, true, true, false>), grid, block, lds, s, a);
 }
 
 static void launch_few_rows(GemmArgs a, hipStream_t s) {
@@ -656,7 +650,7 @@ static void launch_few_rows(GemmArgs a, hipStream_t s) {
 
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
   if (a.M == 0) return hipSuccess;
-  if (few_rows(a)) {
+  if (!a.a.by_k && !a.b.by_k && few_rows(a.M, a.N, a.K, a.gated)) {
     launch_few_rows(a, s);
     return hipGetLastError();
   }
@@ -665,10 +659,8 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
   a.part = p.part;
   a.partials = static_cast<float*>(partials);
   a.ld_partials = partial_ld(a.N, a.gated);
-  const bool d = direct(a.a, a.M, a.K) && direct(a.b, a.N, a.K);
-  if (p.large && d) launch_tiles<TilesLarge, true>(a, s);
-  else if (d) launch_tiles<TilesSmall, true>(a, s);
-  else launch_tiles<TilesSmall, false>(a, s);
+  if (p.large) launch_tiles<TilesLarge>(a, s);
+  else launch_tiles<TilesSmall>(a, s);
   if (a.splits > 1) {
     const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
     const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
@@ -678,12 +670,39 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ----------------------------------------------------------------- packing --
+
+// Copies bf16 matrices so that rows start on 16 bytes and hold a multiple of
+// eight elements, zeros past the last: the tiles' loads into LDS want that,
+// and a copy at memory's speed costs less than loads that do not (4096 x 4096
+// x 4097 forward: 190 us with tiles staged through registers). A lane takes
+// eight elements; blockIdx.y is the matrix.
+__global__ __launch_bounds__(256) void k_pack(PackArgs a) {
+  const PackArgs::One m = a.m[blockIdx.y];
+  const int64_t octs = m.ld / 8, total = m.rows * octs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / octs, c = (i - row * octs) * 8, left = m.cols - c;
+    Oct<kBF16> o;
+    o.load(m.src.p, row * m.src.ld + c, left < 8 ? (int)left : 8);
+    *reinterpret_cast<u32x4*>(m.dst + row * m.ld + c) = o.v;
+  }
+}
+
+hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
+  int64_t most = 0;
+  for (int i = 0; i < a.count; ++i) most = std::max(most, a.m[i].rows * (a.m[i].ld / 8));
+  if (most == 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<int64_t>((most + 255) / 256, 4096), (unsigned)a.count);
+  hipLaunchKernelGGL(k_pack, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 // ------------------------------------------------- backward of activations --
 
 // A workgroup takes 512 columns (blockIdx.y) of a range of rows, a wave every
-// fourth row of them, a lane eight neighbouring columns. 64 rows are a range;
-// more where there would be over kActMaxGroups ranges.
-constexpr int kActRows = 64, kActMaxGroups = 1024;
+// fourth row of them, two at a time, a lane eight neighbouring columns. Eight
+// rows are a range; more where there would be over kActMaxGroups ranges.
+constexpr int kActRows = 8, kActMaxGroups = 1024;
 int act_back_groups(int64_t M) {
   const int64_t g = (M + kActRows - 1) / kActRows;
   return (int)(g < kActMaxGroups ? g : kActMaxGroups);
@@ -699,39 +718,58 @@ __global__ __launch_bounds__(256) void k_act_back(ActBackArgs a) {
   float db[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) db[e] = 0.0f;
-  for (int64_t m = first + wave; m < end; m += 4) {
-    if (n <= 0) break;
-    float d[8], z[8];
-    load8(a.dout.p, a.dout.dt, m * a.dout.ld + c, n, d);
-    if (GATED || a.act != kActNone) load8(a.z.p, a.z.dt, m * a.z.ld + c, n, z);
-    if constexpr (GATED) {
-      float u[8], dg[8];
-      load8(a.z.p, a.z.dt, m * a.z.ld + a.N + c, n, u);
+  // dz's rows are whole eights: zeros past the last column
+  const int pad = n < 8 && n > 0 && !GATED ? 8 : n;
+  for (int64_t m = first + wave; m < end && n > 0; m += 8) {
+    float d[2][8], z[2][8], u[2][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dg[e] = d[e] * u[e] * act_slope(z[e], a.act);
-        d[e] = d[e] * act_value(z[e], a.act);
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = m + 4 * i;
+      if (row >= end) break;
+      load8(a.dout.p, a.dout.dt, row * a.dout.ld + c, n, d[i]);
+      if (GATED || a.act != kActNone) load8(a.z.p, a.z.dt, row * a.z.ld + c, n, z[i]);
+      if (GATED) load8(a.z.p, a.z.dt, row * a.z.ld + a.N + c, n, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = m + 4 * i;
+      if (row >= end) break;
+      if constexpr (GATED) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float value, slope;
+          act_both(z[i][e], a.act, &value, &slope);
+          u[i][e] = d[i][e] * u[i][e] * slope;
+          d[i][e] = d[i][e] * value;
+        }
+        store8(a.dz, kBF16, row * a.ld_dz + c, n, u[i]);
+        store8(a.dz, kBF16, row * a.ld_dz + a.N + c, n, d[i]);
+      } else {
+        if (a.act != kActNone) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[i][e] = e < n ? d[i][e] * act_slope(z[i][e], a.act) : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) db[e] += d[i][e];
+        if (a.dz) store8(a.dz, kBF16, row * a.ld_dz + c, pad, d[i]);
       }
-      store8(a.dz, kBF16, m * a.ld_dz + c, n, dg);
-      store8(a.dz, kBF16, m * a.ld_dz + a.N + c, n, d);
-    } else {
-      if (a.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = d[e] * act_slope(z[e], a.act);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) db[e] += d[e];
-      if (a.dz) store8(a.dz, kBF16, m * a.ld_dz + c, n, d);
     }
   }
-  if (GATED || a.partials == nullptr) return;
+  if constexpr (GATED) {
+    // zeros past the last column of the second half
+    const int64_t rest = a.ld_dz - 2 * (int64_t)a.N;
+    if (blockIdx.y == 0 && threadIdx.x < rest)
+      for (int64_t m = first; m < end; ++m) a.dz[m * a.ld_dz + 2 * (int64_t)a.N + threadIdx.x] = 0;
+  } else {
+    if (a.partials == nullptr) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = db[e];
-  __syncthreads();
-  for (int i = (int)threadIdx.x; i < 512; i += 256) {
-    const int col = (int)blockIdx.y * 512 + i;
-    if (col < a.N)
-      a.partials[(int64_t)blockIdx.x * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+    for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = db[e];
+    __syncthreads();
+    for (int i = (int)threadIdx.x; i < 512; i += 256) {
+      const int col = (int)blockIdx.y * 512 + i;
+      if (col < a.N)
+        a.partials[(int64_t)blockIdx.x * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+    }
   }
 }
 
