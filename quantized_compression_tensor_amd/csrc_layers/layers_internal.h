@@ -84,12 +84,12 @@ struct GemmArgs {
   int64_t K;
   bool gated;
   Epilogue e;
-  // set by launch_gemm: K cut into `splits` parts of `part` (a multiple of
-  // 64), whose sums go to partials [splits][M][ld_partials] in float32
-  int splits;
+  // set by launch_gemm: the first `whole` tiles take all of K; K is cut into
+  // `parts` parts of `part` (a multiple of 64) for the `rest` others, whose
+  // sums go to partials [parts][rest] tiles in float32
+  unsigned whole, rest, parts;
   int64_t part;
   float* partials;
-  int64_t ld_partials;
   int cols;   // output columns of a workgroup, for few rows
 };
 

@@ -268,6 +268,10 @@ struct Loader : Chunks<BY_K, R, NT, GATED> {
 // Output tile of this workgroup: each XCD walks one contiguous range of tiles,
 // and inside it groups of kGroupM tile rows column by column, so the
 // workgroups resident on an XCD share rows of a and of b through its L2.
+TACO_DEV unsigned xcd_ordered(unsigned b, unsigned G) {
+  const unsigned x = b % kXcds, l = b / kXcds, q = G / kXcds, r = G % kXcds;
+  return x * q + (x < r ? x : r) + l;
+}
 TACO_DEV void tile_of(unsigned t, unsigned ntm, unsigned ntn, unsigned* tm, unsigned* tn) {
   const unsigned per_group = kGroupM * ntn, group = t / per_group, in_group = t % per_group;
   const unsigned first = group * kGroupM, rows = ntm - first < kGroupM ? ntm - first : kGroupM;
@@ -311,12 +315,16 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
-  const unsigned block = xcd_ordered_block(), split = block / (ntm * ntn);
+  // the tiles with all of K, then the parts of the others, each in its own order
+  const bool whole = blockIdx.x < a.whole;
+  const unsigned index =
+      whole ? xcd_ordered(blockIdx.x, a.whole) : xcd_ordered(blockIdx.x - a.whole, a.rest * a.parts);
+  const unsigned part = whole ? 0 : index / a.rest;
   unsigned tm, tn;
-  tile_of(block - split * (ntm * ntn), ntm, ntn, &tm, &tn);
-  const int64_t m0 = (int64_t)tm * BM, k0 = split * a.part;
+  tile_of(whole ? index : a.whole + index % a.rest, ntm, ntn, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, k0 = part * a.part;
   const int n0 = (int)tn * kCols;
-  const int64_t K = a.K - k0 < a.part ? a.K - k0 : a.part;   // of this part
+  const int64_t K = whole || a.K - k0 < a.part ? a.K - k0 : a.part;   // of this part
   const int rows_a = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_b = a.N - n0 < kCols ? a.N - n0 : kCols;
   const uint16_t* pa = a.a.p + (AK ? m0 + k0 * a.a.ld : m0 * a.a.ld + k0);
   const uint16_t* pb = a.b.p + (BK_ ? n0 + k0 * a.b.ld : n0 * a.b.ld + k0);
@@ -436,10 +444,10 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
       }
       if (m >= a.M || n >= a.N) continue;
       const int count = a.N - n;
-      if (a.splits > 1) {
-        float* part = a.partials + (split * a.M + m) * a.ld_partials;
-        store8(part, kF32, n, count, z);
-        if (GATED) store8(part, kF32, a.N + n, count, u);
+      if (!whole) {
+        float* row = a.partials + ((int64_t)index * BM + (m - m0)) * BN + (n - n0);
+        store8(row, kF32, 0, z);
+        if (GATED) store8(row, kF32, kCols, u);
       } else if (GATED) {
         finish_gated(a.e, a.N, m, n, count, z, u);
       } else {
@@ -450,31 +458,35 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   }
 }
 
-// Joins the parts of K, in order, and finishes: a lane takes eight columns.
-template <bool GATED>
+// Joins the parts of the tiles whose K is cut, in order, and finishes: a
+// workgroup takes some rows of a tile (blockIdx.x), a lane eight columns.
+template <class TL, bool GATED>
 __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
-  const int64_t per_row = (a.N + 7) / 8, total = a.M * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per_row;
-    const int n = (int)(i % per_row) * 8, count = a.N - n;
-    float z[8], u[8];
+  constexpr int BM = TL::BM, BN = TL::BN, kCols = GATED ? BN / 2 : BN, kOcts = kCols / 8, kRows = 256 / kOcts;
+  const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
+  unsigned tm, tn;
+  tile_of(a.whole + blockIdx.x, ntm, ntn, &tm, &tn);
+  const int row = (int)blockIdx.y * kRows + (int)threadIdx.x / kOcts, col = (int)threadIdx.x % kOcts * 8;
+  const int64_t m = (int64_t)tm * BM + row;
+  const int n = (int)tn * kCols + col;
+  if (m >= a.M || n >= a.N) return;
+  float z[8], u[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = 0.0f, u[e] = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-      const float* part = a.partials + (s * a.M + m) * a.ld_partials;
-      float f[8];
-      load8(part, kF32, n, count, f);
+  for (int e = 0; e < 8; ++e) z[e] = 0.0f, u[e] = 0.0f;
+  for (unsigned p = 0; p < a.parts; ++p) {
+    const float* at = a.partials + (((int64_t)p * a.rest + blockIdx.x) * BM + row) * BN + col;
+    float f[8];
+    load8(at, kF32, 0, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] += f[e];
-      if (GATED) {
-        load8(part, kF32, a.N + n, count, f);
+    for (int e = 0; e < 8; ++e) z[e] += f[e];
+    if (GATED) {
+      load8(at, kF32, kCols, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] += f[e];
-      }
+      for (int e = 0; e < 8; ++e) u[e] += f[e];
     }
-    if (GATED) finish_gated(a.e, a.N, m, n, count, z, u);
-    else finish(a.e, m, n, count, z);
   }
+  if (GATED) finish_gated(a.e, a.N, m, n, a.N - n, z, u);
+  else finish(a.e, m, n, a.N - n, z);
 }
 
 // --------------------------------------------------------------- few rows --
@@ -577,15 +589,61 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
 
 // ----------------------------------------------------------------- launch --
 
-// Which tiles a product takes and into how many parts its K is cut. Decided by
+// Which tiles a product takes, and how many of them take all of K. Decided by
 // the sizes alone, so that the workspace is known before the call.
 struct Plan {
   bool large;
-  int splits;
+  unsigned whole, rest, parts;
   int64_t part;
 };
 
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
+
+static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
+  const int64_t large = tiles_of(M, N, 256, gated ? 128 : 256), steps = (K + 63) / 64;
+  const bool is_large = large >= 192;
+  const int64_t tiles = is_large ? large : tiles_of(M, N, 128, gated ? 64 : 128);
+  // Tiles that run at once: one of 256 x 256 on a CU, or two of 128 x 128.
+  const int64_t slots = is_large ? 256 : 512;
+  // The last round of tiles, if it fills less than half of them, has its K cut
+  // so that it does. A part keeps at least eight steps (with four, 128 x 4096 x
+  // 4096 took 23.4 us, with eight 18.8).
+  const int64_t rest = tiles % slots;
+  int64_t parts = rest > 0 ? std::min<int64_t>(std::min(slots / rest, steps / 8), 16) : 1;
+  // What that saves (a step of the last round takes 1.5 us, or 0.9 us) against
+  // the parts' way through memory, 30 us for a full round of large tiles and
+  // half of that for small ones, and the launch that joins them.
+  if (parts > 1) {
+    const double saved = (double)(steps - (steps + parts - 1) / parts) * (is_large ? 1.5 : 0.9);
+    const double cost = 5.0 + (is_large ? 30.0 : 15.0) * (double)(rest * parts) / (double)slots;
+    if (saved < cost) parts = 1;
+  }
+  if (parts <= 1) return Plan{is_large, (unsigned)tiles, 0, 1, 0};
+  const int64_t per = (steps + parts - 1) / parts;
+  return Plan{is_large, (unsigned)(tiles - rest), (unsigned)rest, (unsigned)((steps + per - 1) / per), per * 64};
+}
+
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  if (M == 0) return 0;
+  const Plan p = plan_of(M, N, K, gated);
+  const size_t tile = p.large ? 256 * 256 : 128 * 128;
+  return (size_t)p.rest * p.parts * tile * sizeof(float);
+}
+
+template <class TL>
+static void launch_tiles(const GemmArgs& a, hipStream_t s) {
+  const dim3 grid(a.whole + a.rest * a.parts), block(TL::kThreads);
+  constexpr size_t lds = TL::kLdsBytes;
+  if (a.gated) hipLaunchKernelGGL((k_gemm<TL, false, false, true>), grid, block, lds, s, a);
+  else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false>), grid, block, lds, s, a);
+  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_gemm<TL, true, true, false>), grid, block, lds, s, a);
+  if (a.rest == 0) return;
+  const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
+  const dim3 join(a.rest, (unsigned)(TL::BM / rows));
+  if (a.gated) hipLaunchKernelGGL((k_join<TL, true>), join, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_join<TL, false>), join, dim3(256), 0, s, a);
+}
 
 // Whether a forward product takes the kernel for few rows. Every workgroup
 // reads all of x, so tiles are faster where rows times weights are many (16
@@ -595,40 +653,6 @@ static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + b
 bool few_rows(int64_t M, int64_t N, int64_t K, bool gated) {
   const int64_t weights = (gated ? 2 : 1) * N * K;
   return M <= 4 || (M <= kFewRows && weights * M <= int64_t(1) << 29);
-}
-
-static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
-  Plan p = {tiles_of(M, N, 256, gated ? 128 : 256) >= 192, 1, (K + 63) / 64 * 64};
-  if (p.large) return p;
-  const int64_t tiles = tiles_of(M, N, 128, gated ? 64 : 128), steps = (K + 63) / 64;
-  // two workgroups of 128 x 128 fit on a CU; at least 8 steps for a part
-  int64_t splits = tiles > 0 ? 512 / tiles : 1;
-  if (splits > steps / 8) splits = steps / 8;
-  if (splits > 16) splits = 16;
-  if (splits > 1) {
-    const int64_t per = (steps + splits - 1) / splits;
-    p.part = per * 64;
-    p.splits = (int)((steps + per - 1) / per);
-  }
-  return p;
-}
-
-static int64_t partial_ld(int64_t N, bool gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
-
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-  const Plan p = plan_of(M, N, K, gated);
-  return p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)partial_ld(N, gated) * 4 : 0;
-}
-
-template <class TL>
-static void launch_tiles(const GemmArgs& a, hipStream_t s) {
-  const int64_t tiles = tiles_of(a.M, a.N, TL::BM, a.gated ? TL::BN / 2 : TL::BN);
-  const dim3 grid((unsigned)(tiles * a.splits)), block(TL::kThreads);
-  constexpr size_t lds = TL::kLdsBytes;
-  if (a.gated) hipLaunchKernelGGL((k_gemm<TL, false, false, true>), grid, block, lds, s, a);
-  else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false>), grid, block, lds, s, a);
-  else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_gemm<TL, true, true, false>), grid, block, lds, s, a);
 }
 
 static void launch_few_rows(GemmArgs a, hipStream_t s) {
@@ -655,18 +679,13 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
     return hipGetLastError();
   }
   const Plan p = plan_of(a.M, a.N, a.K, a.gated);
-  a.splits = p.splits;
+  a.whole = p.whole;
+  a.rest = p.rest;
+  a.parts = p.parts;
   a.part = p.part;
   a.partials = static_cast<float*>(partials);
-  a.ld_partials = partial_ld(a.N, a.gated);
   if (p.large) launch_tiles<TilesLarge>(a, s);
   else launch_tiles<TilesSmall>(a, s);
-  if (a.splits > 1) {
-    const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
-    if (a.gated) hipLaunchKernelGGL((k_join<true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_join<false>), grid, dim3(256), 0, s, a);
-  }
   return hipGetLastError();
 }
 
