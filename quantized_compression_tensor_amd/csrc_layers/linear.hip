@@ -93,35 +93,59 @@ TACO_DEV void act_both(float t, int act, float* value, float* slope) {
 
 // --------------------------------------------------------------- epilogue --
 
-// Eight neighbouring columns n ... of row m, of which `count` exist.
-TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z) {
+TACO_DEV void act_values(float* z, int act) {
+  if (act == kActNone) return;
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kActGelu);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kActSilu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], kActRelu);
+  }
+}
+
+// What an output reads besides its sum, where there is any (finish() uses it
+// under the same condition).
+TACO_DEV void load_bias(const Epilogue& e, int n, int count, float* b) {
+  if (e.bias.p && count > 0) load8(e.bias.p, e.bias.dt, n, count, b);
+}
+TACO_DEV void load_residual(const Epilogue& e, int64_t m, int n, int count, float* r) {
+  if (e.residual.p && count > 0) load8(e.residual.p, e.residual.dt, m * e.residual.ld + n, count, r);
+}
+
+// Eight neighbouring columns n ... of row m, of which `count` exist, with
+// their bias b and residual r.
+TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z, const float* b, const float* r) {
   if (e.bias.p) {
-    float b[8];
-    load8(e.bias.p, e.bias.dt, n, count, b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += b[i];
   }
   if (e.preact.p) store8(e.preact.p, e.preact.dt, m * e.preact.ld + n, count, z);
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], e.act);
-  }
+  act_values(z, e.act);
   if (e.residual.p) {
-    float r[8];
-    load8(e.residual.p, e.residual.dt, m * e.residual.ld + n, count, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += r[i];
   }
   store8(e.out.p, e.out.dt, m * e.out.ld + n, count, z);
 }
+TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z) {
+  float b[8], r[8];
+  load_bias(e, n, count, b);
+  load_residual(e, m, n, count, r);
+  finish(e, m, n, count, z, b, r);
+}
 // The same of a gated layer with `width` output columns: z gate, u the other.
-TACO_DEV void finish_gated(const Epilogue& e, int width, int64_t m, int n, int count, float* z, float* u) {
+TACO_DEV void finish_gated(const Epilogue& e, int width, int64_t m, int n, int count, float* z, const float* u) {
   if (e.preact.p) {
     store8(e.preact.p, e.preact.dt, m * e.preact.ld + n, count, z);
     store8(e.preact.p, e.preact.dt, m * e.preact.ld + width + n, count, u);
   }
+  act_values(z, e.act);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], e.act) * u[i];
+  for (int i = 0; i < 8; ++i) z[i] *= u[i];
   store8(e.out.p, e.out.dt, m * e.out.ld + n, count, z);
 }
 
@@ -137,9 +161,9 @@ struct Tiles {
   // After how many of a slice's rows of MFMA tiles a stage is handed back: b's
   // in the first slice, a's in the second
   static constexpr int kFreeB = TM / 2, kFreeA = TM / 4;
-  static constexpr int kTurnLd = TN * 16 + 4;                    // floats of a row in the epilogue's turn
+  static constexpr int kTurnLd = TN * 16 + 4, kTurnRows = 32;    // the epilogue's turn: floats of a row, rows
   static constexpr int kLdsBytes = (kStagesA * kA + kStagesB * kB) * 2;
-  static_assert(WGM * WGN * 32 * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
+  static_assert(WGM * WGN * kTurnRows * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
 using TilesLarge = Tiles<256, 256, 2, 4>;
 using TilesSmall = Tiles<128, 128, 2, 2>;
@@ -309,7 +333,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
   
-  static_assert(!GATED || TN % 4 == 0, "a wave holds the two projections of its columns");
+  static_assert(!GATED || TN == 4, "a wave holds the two projections of its columns");
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
@@ -417,41 +441,55 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   hand_over<0, 0>();
 
   // Accumulator e of lane l holds row 4 (l / 16) + e, column l % 16 of its
-  // tile. Each wave turns 32 rows at a time round through its own part of LDS,
-  // so that a lane has eight neighbouring columns of a row.
-  constexpr int kLd = TL::kTurnLd, kWaveCols = GATED ? TN * 8 : TN * 16, kLanes = kWaveCols / 8;
-  float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kLd;
+  // tile. Each wave turns kTurnRows rows at a time round through its own part
+  // of LDS, so that a lane has eight neighbouring columns of a row, and has the
+  // residuals of all of its rows under way together.
+  constexpr int kLd = TL::kTurnLd, kTurnRows = TL::kTurnRows;
+  constexpr int kWaveCols = GATED ? TN * 8 : TN * 16, kLanes = kWaveCols / 8;
+  constexpr int kPass = kWave / kLanes, kRound = kTurnRows / kPass;   // rows of a pass, passes
+  float* turn = reinterpret_cast<float*>(lds) + wave * kTurnRows * kLd;
+  const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c, count = a.N - n;
+  float bias[8];
+  constexpr bool kPlain = BK_;   // a gradient: the sum itself is the output
+  if (!GATED && !kPlain) load_bias(a.e, n, whole ? count : 0, bias);
 #pragma unroll
-  for (int i = 0; i < TM / 2; ++i) {
+  for (int i0 = 0; i0 < TM; i0 += kTurnRows / 16) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kTurnRows / 16; ++h)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          turn[(16 * h + 4 * (lane >> 4) + e) * kLd + j * 16 + (lane & 15)] = acc[2 * i + h][j][e];
+          turn[(16 * h + 4 * (lane >> 4) + e) * kLd + j * 16 + (lane & 15)] = acc[i0 + h][j][e];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c, zc = GATED ? c / 32 * 64 + c % 32 : c;
-#pragma unroll 1
-    for (int r = lane / kLanes; r < 32; r += kWave / kLanes) {
-      const int64_t m = m0 + wm * TM * 16 + i * 32 + r;
+    const int64_t m_first = m0 + (wm * TM + i0) * 16 + lane / kLanes;
+    float res[kRound][8];
+    if (!GATED && !kPlain && whole) {
+#pragma unroll
+      for (int q = 0; q < kRound; ++q)
+        load_residual(a.e, m_first + q * kPass, n, m_first + q * kPass < a.M ? count : 0, res[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kRound; ++q) {
+      const int64_t m = m_first + q * kPass;
+      const float* row = turn + (lane / kLanes + q * kPass) * kLd;
       float z[8], u[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + zc + 4 * h);
-        if (GATED)
-          *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(turn + r * kLd + 32 + zc + 4 * h);
+        *reinterpret_cast<f32x4*>(z + 4 * h) = *reinterpret_cast<const f32x4*>(row + c + 4 * h);
+        if (GATED) *reinterpret_cast<f32x4*>(u + 4 * h) = *reinterpret_cast<const f32x4*>(row + kWaveCols + c + 4 * h);
       }
-      if (m >= a.M || n >= a.N) continue;
-      const int count = a.N - n;
+      if (m >= a.M || count <= 0) continue;
       if (!whole) {
-        float* row = a.partials + ((int64_t)index * BM + (m - m0)) * BN + (n - n0);
-        store8(row, kF32, 0, z);
-        if (GATED) store8(row, kF32, kCols, u);
+        float* part_row = a.partials + ((int64_t)index * BM + (m - m0)) * BN + (n - n0);
+        store8(part_row, kF32, 0, z);
+        if (GATED) store8(part_row, kF32, kCols, u);
       } else if (GATED) {
         finish_gated(a.e, a.N, m, n, count, z, u);
+      } else if (kPlain) {
+        store8(a.e.out.p, a.e.out.dt, m * a.e.out.ld + n, count, z);
       } else {
-        finish(a.e, m, n, count, z);
+        finish(a.e, m, n, count, z, bias, res[q]);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
