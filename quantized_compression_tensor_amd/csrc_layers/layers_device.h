@@ -94,12 +94,22 @@ TACO_DEV void load8(const void* base, int dt, int64_t at, int n, float* f) {
   }
 }
 TACO_DEV void load8(const void* base, int dt, int64_t at, float* f) { load8(base, dt, at, 8, f); }
+// NT: streamed past the caches, as a tensor that another kernel reads should
+// be where whole 128-byte lines are written (forward norm 8192 x 5120 45.5 us
+// cached, 43.1 us streamed; 4096 x 4096 x 512 product 24.0 and 21.3).
+template <bool NT>
+TACO_DEV void store16(void* p, u32x4 v) {
+  typedef unsigned any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+  if constexpr (NT) __builtin_nontemporal_store((any_u32x4)v, static_cast<any_u32x4*>(p));
+  else *static_cast<any_u32x4*>(p) = (any_u32x4)v;
+}
+template <bool NT = true>
 TACO_DEV void store8(void* base, int dt, int64_t at, int n, const float* f) {
   if (dt == kBF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + at;
     const u32x4 v = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
     if (n >= 8) {
-      __builtin_memcpy(p, &v, 16);
+      store16<NT>(p, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -108,8 +118,10 @@ TACO_DEV void store8(void* base, int dt, int64_t at, int n, const float* f) {
   } else {
     float* p = static_cast<float*>(base) + at;
     if (n >= 8) {
-      __builtin_memcpy(p, f, 16);
-      __builtin_memcpy(p + 4, f + 4, 16);
+#pragma unroll
+      for (int h = 0; h < 8; h += 4)
+        store16<NT>(p + h, u32x4{__float_as_uint(f[h]), __float_as_uint(f[h + 1]), __float_as_uint(f[h + 2]),
+                                 __float_as_uint(f[h + 3])});
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -118,6 +130,8 @@ TACO_DEV void store8(void* base, int dt, int64_t at, int n, const float* f) {
   }
 }
 TACO_DEV void store8(void* base, int dt, int64_t at, const float* f) { store8(base, dt, at, 8, f); }
+// Eight floats that stay in the caches: partial sums, read again soon.
+TACO_DEV void keep8(float* p, const float* f) { store8<false>(p, kF32, 0, 8, f); }
 TACO_DEV float load1(const void* base, int dt, int64_t at) {
   return dt == kBF16 ? (float)static_cast<const __bf16*>(base)[at] : static_cast<const float*>(base)[at];
 }

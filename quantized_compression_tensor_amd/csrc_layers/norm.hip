@@ -24,8 +24,8 @@
 // on every CU. Sums over lanes go by DPP and one LDS read per lane: with
 // permutes through LDS the same passes took 47 and 78 us.
 //
-// Measured (bf16): forward 8192 x 5120 45 us (3.7 TB/s), 32768 x 5120 161 us
-// (4.2 TB/s); backward with both sums 62 us (4.1 TB/s) and 212 us (4.8 TB/s).
+// Measured (bf16): forward 8192 x 5120 44 us (3.8 TB/s), 32768 x 5120 157 us
+// (4.3 TB/s); backward with both sums 60 us (4.2 TB/s) and 201 us (5.0 TB/s).
 #include <type_traits>
 
 #include "layers_device.h"
@@ -258,8 +258,8 @@ __global__ __launch_bounds__(1024) void k_norm_back(NormBackArgs a) {
     float* part = a.partials + (int64_t)blockIdx.x * 2 * a.cols;
     float* mine = g.blocks == 1 ? part : sums + g.in_block * 2 * a.cols;
     if (g.lane < whole) {
-      store8(mine, kF32, g.lane * 8, dw);
-      store8(mine, kF32, a.cols + g.lane * 8, db);
+      keep8(mine + g.lane * 8, dw);
+      keep8(mine + a.cols + g.lane * 8, db);
     }
     if (g.lane < rest) {
       mine[whole * 8 + g.lane] = dw_last;
@@ -300,8 +300,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_back_sums(NormBackArgs a)
     }
   }
   float* part = a.partials + (int64_t)blockIdx.x * 2 * a.cols;
-  store8(part, kF32, c, n, dw);
-  store8(part, kF32, a.cols + c, n, db);
+  store8<false>(part, kF32, c, n, dw);
+  store8<false>(part, kF32, a.cols + c, n, db);
 }
 
 // Sums over `count` rows of `cols` floats, ld apart, into up to two outputs
