@@ -194,23 +194,21 @@ struct Backward {
     const size_t dx_bytes = want_dx ? gemm_partial_bytes(m, k, wide, false) : 0;
     const size_t dw_bytes = want_dw ? gemm_partial_bytes(wide, k, m, false) : 0;
     const size_t db_bytes = want_db ? (size_t)act_back_groups(m) * (size_t)n * sizeof(float) : 0;
-    void* rest = space->take(std::max({dx_bytes, dw_bytes, db_bytes}));
+    const size_t both_bytes = want_dx && want_dw ? gemm_pair_partial_bytes(m, wide, k) : 0;
+    void* rest = space->take(std::max({dx_bytes, dw_bytes, db_bytes, both_bytes}));
     if (what != kRun) return hipSuccess;
     if (want_db) b.partials = static_cast<float*>(rest);
     hipError_t err = hipSuccess;
     if (own_dz || want_db) err = launch_act_back(b, stream);
     if (err == hipSuccess && pack.count > 0) err = launch_pack(pack, stream);
-    GemmArgs g = {};
-    g.e.act = kActNone;
-    if (err == hipSuccess && want_dx) {
-      g.a = dz; g.b = ow; g.M = m; g.N = (int)k; g.K = wide; g.e.out = dx.m;
-      err = launch_gemm(g, rest, stream);
-    }
-    if (err == hipSuccess && want_dw) {
-      dz.by_k = true;
-      g.a = dz; g.b = ox; g.M = wide; g.N = (int)k; g.K = m; g.e.out = dw.m;
-      err = launch_gemm(g, rest, stream);
-    }
+    if (err != hipSuccess) return err;
+    GemmArgs gx = {}, gw = {};
+    gx.a = dz; gx.b = ow; gx.M = m; gx.N = (int)k; gx.K = wide; gx.e.out = dx.m;
+    dz.by_k = true;
+    gw.a = dz; gw.b = ox; gw.M = wide; gw.N = (int)k; gw.K = m; gw.e.out = dw.m;
+    if (want_dx && want_dw) return launch_gemm_pair(gx, gw, rest, stream);
+    if (want_dx) err = launch_gemm(gx, rest, stream);
+    if (want_dw) err = launch_gemm(gw, rest, stream);
     return err;
   }
 };

@@ -116,6 +116,10 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
+// Both gradients of a projection, dx [M, K] and dw [wide, K], as one launch
+// where they are small; gemm_pair_partial_bytes: for these, else 0.
+size_t gemm_pair_partial_bytes(int64_t M, int64_t wide, int64_t K);
+hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, void* partials, hipStream_t s);
 hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s);
 // out0 [cols] = the sum of `count` rows of `in`, ld apart, and out1 that of
 // the columns `second` floats further on (zeros if count is 0; each may be

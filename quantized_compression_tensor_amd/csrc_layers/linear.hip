@@ -330,8 +330,9 @@ TACO_DEV void hand_over() {
 // or two steps' time. The 16 x 16 x 32 products were faster than 32 x 32 x 16
 // (8192^3: 750 against 815 us) although they leave more gaps: this size is
 // bound by power, and they move half as many sums through the registers.
+// `block`: of the product's a.whole + a.rest * a.parts.
 template <class TL, bool AK, bool BK_, bool GATED>
-__global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
+TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
   
@@ -342,9 +343,8 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
   // the tiles with all of K, then the parts of the others, each in its own order
-  const bool whole = blockIdx.x < a.whole;
-  const unsigned index =
-      whole ? xcd_ordered(blockIdx.x, a.whole) : xcd_ordered(blockIdx.x - a.whole, a.rest * a.parts);
+  const bool whole = block < a.whole;
+  const unsigned index = whole ? xcd_ordered(block, a.whole) : xcd_ordered(block - a.whole, a.rest * a.parts);
   const unsigned part = whole ? 0 : index / a.rest;
   unsigned tm, tn;
   tile_of(whole ? index : a.whole + index % a.rest, ntm, ntn, &tm, &tn);
@@ -498,6 +498,18 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
   }
 }
 
+template <class TL, bool AK, bool BK_, bool GATED>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
+  gemm<TL, AK, BK_, GATED>(a, blockIdx.x);
+}
+// Two gradients at once, where neither fills the device: dx = dz W in the
+// first `count` workgroups, dw = dz^T x in the others.
+template <class TL>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_gemm_pair(GemmArgs dx, GemmArgs dw, unsigned count) {
+  if (blockIdx.x < count) gemm<TL, false, true, false>(dx, blockIdx.x);
+  else gemm<TL, true, true, false>(dw, blockIdx.x - count);
+}
+
 // Joins the parts of the tiles whose K is cut, in order, and finishes: a
 // workgroup takes some rows of a tile (blockIdx.x), a lane eight columns.
 template <class TL, bool GATED>
@@ -639,12 +651,13 @@ struct Plan {
 
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
 
-static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
+// `taken`: slots that another product fills at the same time.
+static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int64_t taken = 0) {
   const int64_t large = tiles_of(M, N, 256, gated ? 128 : 256), steps = (K + 63) / 64;
   const bool is_large = large >= 192;
   const int64_t tiles = is_large ? large : tiles_of(M, N, 128, gated ? 64 : 128);
   // Tiles that run at once: one of 256 x 256 on a CU, or two of 128 x 128.
-  const int64_t slots = is_large ? 256 : 512;
+  const int64_t slots = std::max<int64_t>((is_large ? 256 : 512) - taken, 1);
   // The last round of tiles, if it fills less than half of them, has its K cut
   // so that it does. A part keeps at least eight steps (with four, 128 x 4096 x
   // 4096 took 23.4 us, with eight 18.8).
@@ -663,11 +676,46 @@ static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated) {
   return Plan{is_large, (unsigned)(tiles - rest), (unsigned)rest, (unsigned)((steps + per - 1) / per), per * 64};
 }
 
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-  if (M == 0) return 0;
-  const Plan p = plan_of(M, N, K, gated);
+static size_t partial_bytes(const Plan& p) {
   const size_t tile = p.large ? 256 * 256 : 128 * 128;
   return (size_t)p.rest * p.parts * tile * sizeof(float);
+}
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  return M == 0 ? 0 : partial_bytes(plan_of(M, N, K, gated));
+}
+
+// Both gradients of a projection with `wide` weight rows: together where
+// neither takes large tiles and both fit the slots.
+struct PairPlan {
+  bool together;
+  Plan dx, dw;
+};
+static PairPlan pair_plan_of(int64_t M, int64_t wide, int64_t K) {
+  const int64_t dx_tiles = tiles_of(M, K, 128, 128), dw_tiles = tiles_of(wide, K, 128, 128);
+  PairPlan p = {false, plan_of(M, K, wide, false, dw_tiles), plan_of(wide, K, M, false, dx_tiles)};
+  p.together = M > 0 && !p.dx.large && !p.dw.large && dx_tiles + dw_tiles <= 512;
+  return p;
+}
+size_t gemm_pair_partial_bytes(int64_t M, int64_t wide, int64_t K) {
+  const PairPlan p = pair_plan_of(M, wide, K);
+  return p.together ? partial_bytes(p.dx) + partial_bytes(p.dw) : 0;
+}
+
+static void set_plan(GemmArgs* a, const Plan& p, void* partials) {
+  a->whole = p.whole;
+  a->rest = p.rest;
+  a->parts = p.parts;
+  a->part = p.part;
+  a->partials = static_cast<float*>(partials);
+}
+
+template <class TL>
+static void launch_join(const GemmArgs& a, hipStream_t s) {
+  if (a.rest == 0) return;
+  const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
+  const dim3 join(a.rest, (unsigned)(TL::BM / rows));
+  if (a.gated) hipLaunchKernelGGL((k_join<TL, true>), join, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_join<TL, false>), join, dim3(256), 0, s, a);
 }
 
 template <class TL>
@@ -678,11 +726,7 @@ static void launch_tiles(const GemmArgs& a, hipStream_t s) {
   else if (!a.a.by_k && !a.b.by_k) hipLaunchKernelGGL((k_gemm<TL, false, false, false>), grid, block, lds, s, a);
   else if (!a.a.by_k) hipLaunchKernelGGL((k_gemm<TL, false, true, false>), grid, block, lds, s, a);
   else hipLaunchKernelGGL((k_gemm<TL, true, true, false>), grid, block, lds, s, a);
-  if (a.rest == 0) return;
-  const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
-  const dim3 join(a.rest, (unsigned)(TL::BM / rows));
-  if (a.gated) hipLaunchKernelGGL((k_join<TL, true>), join, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_join<TL, false>), join, dim3(256), 0, s, a);
+  launch_join<TL>(a, s);
 }
 
 // Whether a forward product takes the kernel for few rows. Every workgroup
@@ -719,13 +763,25 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
     return hipGetLastError();
   }
   const Plan p = plan_of(a.M, a.N, a.K, a.gated);
-  a.whole = p.whole;
-  a.rest = p.rest;
-  a.parts = p.parts;
-  a.part = p.part;
-  a.partials = static_cast<float*>(partials);
+  set_plan(&a, p, partials);
   if (p.large) launch_tiles<TilesLarge>(a, s);
   else launch_tiles<TilesSmall>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, void* partials, hipStream_t s) {
+  const PairPlan p = pair_plan_of(dx.M, dw.M, dx.N);
+  if (!p.together) {
+    const hipError_t err = launch_gemm(dx, partials, s);
+    return err == hipSuccess ? launch_gemm(dw, partials, s) : err;
+  }
+  set_plan(&dx, p.dx, partials);
+  set_plan(&dw, p.dw, static_cast<char*>(partials) + partial_bytes(p.dx));
+  const unsigned count = dx.whole + dx.rest * dx.parts;
+  const dim3 grid(count + dw.whole + dw.rest * dw.parts), block(TilesSmall::kThreads);
+  hipLaunchKernelGGL((k_gemm_pair<TilesSmall>), grid, block, TilesSmall::kLdsBytes, s, dx, dw, count);
+  launch_join<TilesSmall>(dx, s);
+  launch_join<TilesSmall>(dw, s);
   return hipGetLastError();
 }
 
