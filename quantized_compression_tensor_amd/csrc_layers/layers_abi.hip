@@ -199,8 +199,8 @@ struct Backward {
     if (what != kRun) return hipSuccess;
     if (want_db) b.partials = static_cast<float*>(rest);
     hipError_t err = hipSuccess;
-    if (own_dz || want_db) err = launch_act_back(b, stream);
-    if (err == hipSuccess && pack.count > 0) err = launch_pack(pack, stream);
+    if (own_dz || want_db) err = launch_act_back(b, pack, stream);
+    else if (pack.count > 0) err = launch_pack(pack, stream);
     if (err != hipSuccess) return err;
     GemmArgs gx = {}, gw = {};
     gx.a = dz; gx.b = ow; gx.M = m; gx.N = (int)k; gx.K = wide; gx.e.out = dx.m;

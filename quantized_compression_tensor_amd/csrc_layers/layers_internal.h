@@ -120,7 +120,7 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
 // where they are small; gemm_pair_partial_bytes: for these, else 0.
 size_t gemm_pair_partial_bytes(int64_t M, int64_t wide, int64_t K);
 hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, void* partials, hipStream_t s);
-hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s);
+hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s);   // and launch_pack's work
 // out0 [cols] = the sum of `count` rows of `in`, ld apart, and out1 that of
 // the columns `second` floats further on (zeros if count is 0; each may be
 // absent).

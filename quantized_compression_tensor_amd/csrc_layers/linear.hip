@@ -790,32 +790,38 @@ hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, void* partials, hipStream_
 // Copies bf16 matrices so that rows start on 16 bytes and hold a multiple of
 // eight elements, zeros past the last: the tiles' loads into LDS want that,
 // and a copy at memory's speed costs less than loads that do not (4096 x 4096
-// x 4097 forward: 190 us with tiles staged through registers). A lane takes
-// eight elements; blockIdx.y is the matrix.
-__global__ __launch_bounds__(256) void k_pack(PackArgs a) {
-  const PackArgs::One m = a.m[blockIdx.y];
+// x 4097 forward: 190 us with tiles staged through registers, 135 packed). A
+// lane takes eight elements; `block` of `blocks` for matrix `which`.
+TACO_DEV void pack(const PackArgs& a, unsigned block, unsigned blocks, unsigned which) {
+  const PackArgs::One m = a.m[which];
   const int64_t octs = m.ld / 8, total = m.rows * octs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
     const int64_t row = i / octs, c = (i - row * octs) * 8, left = m.cols - c;
     Oct<kBF16> o;
     o.load(m.src.p, row * m.src.ld + c, left < 8 ? (int)left : 8);
     *reinterpret_cast<u32x4*>(m.dst + row * m.ld + c) = o.v;
   }
 }
+__global__ __launch_bounds__(256) void k_pack(PackArgs a) { pack(a, blockIdx.x, gridDim.x, blockIdx.y); }
 
-hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
+// Workgroups for each matrix.
+static unsigned pack_blocks(const PackArgs& a) {
   int64_t most = 0;
   for (int i = 0; i < a.count; ++i) most = std::max(most, a.m[i].rows * (a.m[i].ld / 8));
-  if (most == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>((most + 255) / 256, 4096), (unsigned)a.count);
-  hipLaunchKernelGGL(k_pack, grid, dim3(256), 0, s, a);
+  return (unsigned)std::min<int64_t>((most + 255) / 256, 4096);
+}
+
+hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
+  const unsigned blocks = pack_blocks(a);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_pack, dim3(blocks, (unsigned)a.count), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 // ------------------------------------------------- backward of activations --
 
-// A workgroup takes 512 columns (blockIdx.y) of a range of rows, a wave every
-// fourth row of them, two at a time, a lane eight neighbouring columns. Eight
+// Workgroup `group` of `groups` takes 512 columns (`slab`) of a range of rows,
+// a wave every fourth row of them, two at a time, a lane eight neighbouring columns. Eight
 // rows are a range; more where there would be over kActMaxGroups ranges.
 constexpr int kActRows = 8, kActMaxGroups = 1024;
 int act_back_groups(int64_t M) {
@@ -824,11 +830,11 @@ int act_back_groups(int64_t M) {
 }
 
 template <bool GATED>
-__global__ __launch_bounds__(256) void k_act_back(ActBackArgs a) {
+TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, unsigned slab) {
   __shared__ float sums[4][512];
   const int lane = (int)threadIdx.x % kWave, wave = wave_in_group();
-  const int c = ((int)blockIdx.y * kWave + lane) * 8, n = a.N - c;
-  const int64_t per = (a.M + gridDim.x - 1) / gridDim.x, first = blockIdx.x * per;
+  const int c = ((int)slab * kWave + lane) * 8, n = a.N - c;
+  const int64_t per = (a.M + groups - 1) / groups, first = group * per;
   const int64_t end = first + per < a.M ? first + per : a.M;
   float db[8];
 #pragma unroll
@@ -873,7 +879,7 @@ __global__ __launch_bounds__(256) void k_act_back(ActBackArgs a) {
   if constexpr (GATED) {
     // zeros past the last column of the second half
     const int64_t rest = a.ld_dz - 2 * (int64_t)a.N;
-    if (blockIdx.y == 0 && threadIdx.x < rest)
+    if (slab == 0 && threadIdx.x < rest)
       for (int64_t m = first; m < end; ++m) a.dz[m * a.ld_dz + 2 * (int64_t)a.N + threadIdx.x] = 0;
   } else {
     if (a.partials == nullptr) return;
@@ -881,21 +887,31 @@ __global__ __launch_bounds__(256) void k_act_back(ActBackArgs a) {
     for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = db[e];
     __syncthreads();
     for (int i = (int)threadIdx.x; i < 512; i += 256) {
-      const int col = (int)blockIdx.y * 512 + i;
+      const int col = (int)slab * 512 + i;
       if (col < a.N)
-        a.partials[(int64_t)blockIdx.x * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+        a.partials[(int64_t)group * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
     }
   }
 }
 
-hipError_t launch_act_back(const ActBackArgs& a, hipStream_t s) {
-  const int groups = act_back_groups(a.M);
-  if (groups > 0) {
-    const dim3 grid((unsigned)groups, (unsigned)((a.N + 511) / 512));
-    if (a.gated) hipLaunchKernelGGL((k_act_back<true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_act_back<false>), grid, dim3(256), 0, s, a);
+// dz, and in the workgroups after its `blocks` the copies that the products
+// need beside it.
+template <bool GATED>
+__global__ __launch_bounds__(256) void k_act_back(ActBackArgs a, PackArgs p, unsigned groups, unsigned blocks,
+                                                  unsigned packing) {
+  if (blockIdx.x < blocks) act_back<GATED>(a, blockIdx.x % groups, groups, blockIdx.x / groups);
+  else pack(p, (blockIdx.x - blocks) % packing, packing, (blockIdx.x - blocks) / packing);
+}
+
+hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s) {
+  const unsigned groups = (unsigned)act_back_groups(a.M), packing = pack_blocks(p);
+  const unsigned blocks = groups * (unsigned)((a.N + 511) / 512);
+  const dim3 grid(blocks + packing * (unsigned)p.count);
+  if (grid.x > 0) {
+    if (a.gated) hipLaunchKernelGGL((k_act_back<true>), grid, dim3(256), 0, s, a, p, groups, blocks, packing);
+    else hipLaunchKernelGGL((k_act_back<false>), grid, dim3(256), 0, s, a, p, groups, blocks, packing);
   }
-  launch_column_sum(a.partials, a.N, 0, groups, a.N, a.dbias, Mat{nullptr, 0, kF32}, s);
+  launch_column_sum(a.partials, a.N, 0, (int)groups, a.N, a.dbias, Mat{nullptr, 0, kF32}, s);
   return hipGetLastError();
 }
 
