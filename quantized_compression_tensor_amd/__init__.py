@@ -318,9 +318,16 @@ def _dtype(t, what):
     return dt
 
 
+def _on_gpu(t, what):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must be on the GPU")
+
+
 def _matrix(t, rows, cols, what):
     if t is None:
         return _ABSENT
+    if not t.is_cuda:
+        _on_gpu(t, what)
     if t.shape != (rows, cols):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
     stride, inner = t.stride()
@@ -333,6 +340,8 @@ def _matrix(t, rows, cols, what):
 def _vector(t, n, what):
     if t is None:
         return _ABSENT
+    if not t.is_cuda:
+        _on_gpu(t, what)
     if t.shape != (n,):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n,)}")
     if n > 1 and not t.is_contiguous():
@@ -344,6 +353,8 @@ def _vector(t, n, what):
 def _floats(t, n, what):
     if t is None:
         return None
+    if not t.is_cuda:
+        _on_gpu(t, what)
     if t.shape != (n,) or (n > 1 and not t.is_contiguous()):
         raise ValueError(f"{what}: expected {n} contiguous values, got shape {tuple(t.shape)}")
     if _dtype(t, what) != TACO_F32:
@@ -351,8 +362,14 @@ def _floats(t, n, what):
     return t.data_ptr()
 
 
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+def _workspace(t):
+    """Address and bytes of a workspace tensor."""
+    if t is None:
+        return None, 0
+    _on_gpu(t, "workspace")
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def taco_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
@@ -376,7 +393,7 @@ def taco_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, d
     return _check(_lib.taco_layer_norm_backward(
         _matrix(dy, rows, cols, "dy"), _matrix(x, rows, cols, "x"), rows, cols, _vector(weight, cols, "weight"),
         _floats(mean, rows, "mean"), _floats(rstd, rows, "rstd"), _matrix(dx, rows, cols, "dx"),
-        _vector(dweight, cols, "dweight"), _vector(dbias, cols, "dbias"), _ptr(workspace), _bytes(workspace),
+        _vector(dweight, cols, "dweight"), _vector(dbias, cols, "dbias"), *_workspace(workspace),
         _stream(stream)), "taco_layer_norm_backward")
 
 
@@ -391,7 +408,7 @@ def taco_linear(x, w, out, bias=None, act=TACO_ACT_NONE, residual=None, preact=N
     return _check(_lib.taco_linear(
         _matrix(x, M, K, "x"), _matrix(w, N, K, "w"), _vector(bias, N, "bias"), act,
         _matrix(residual, M, N, "residual"), _matrix(out, M, N, "out"), _matrix(preact, M, N, "preact"), M, N, K,
-        _ptr(workspace), _bytes(workspace), _stream(stream)), "taco_linear")
+        *_workspace(workspace), _stream(stream)), "taco_linear")
 
 
 def taco_linear_backward_workspace_bytes(M, N, K):
@@ -405,7 +422,7 @@ def taco_linear_backward(dout, x, w, act=TACO_ACT_NONE, preact=None, dx=None, dw
     return _check(_lib.taco_linear_backward(
         _matrix(dout, M, N, "dout"), _matrix(x, M, K, "x"), _matrix(w, N, K, "w"), act,
         _matrix(preact, M, N, "preact"), _matrix(dx, M, K, "dx"), _matrix(dw, N, K, "dw"),
-        _vector(dbias, N, "dbias"), M, N, K, _ptr(workspace), _bytes(workspace), _stream(stream)),
+        _vector(dbias, N, "dbias"), M, N, K, *_workspace(workspace), _stream(stream)),
         "taco_linear_backward")
 
 
@@ -419,7 +436,7 @@ def taco_gated_linear(x, w, out, act=TACO_ACT_SILU, preact=None, workspace=None,
     (M, K), F = x.shape, w.shape[0] // 2
     return _check(_lib.taco_gated_linear(
         _matrix(x, M, K, "x"), _matrix(w, 2 * F, K, "w"), act, _matrix(out, M, F, "out"),
-        _matrix(preact, M, 2 * F, "preact"), M, F, K, _ptr(workspace), _bytes(workspace), _stream(stream)),
+        _matrix(preact, M, 2 * F, "preact"), M, F, K, *_workspace(workspace), _stream(stream)),
         "taco_gated_linear")
 
 
@@ -434,7 +451,7 @@ def taco_gated_linear_backward(dout, x, w, act=TACO_ACT_SILU, preact=None, dx=No
     return _check(_lib.taco_gated_linear_backward(
         _matrix(dout, M, F, "dout"), _matrix(x, M, K, "x"), _matrix(w, 2 * F, K, "w"), act,
         _matrix(preact, M, 2 * F, "preact"), _matrix(dx, M, K, "dx"), _matrix(dw, 2 * F, K, "dw"), M, F, K,
-        _ptr(workspace), _bytes(workspace), _stream(stream)), "taco_gated_linear_backward")
+        *_workspace(workspace), _stream(stream)), "taco_gated_linear_backward")
 
 
 # ------------------------------------------------- buffer plumbing (torch) --

@@ -21,13 +21,15 @@ struct Checked {
   Mat m;
   int64_t bytes;   // from the first element to the end of the last row
   int status;
+  int64_t row;     // bytes of a row's elements, and from one row to the next
+  int64_t step;    // (0: one row)
 };
 
 enum Need { kOptional, kRequired };
 enum Types { kAnyType, kBf16Only };
 
 Checked check_array(const taco_array& a, int64_t rows, int64_t cols, Need need, Types types = kAnyType) {
-  Checked c = {{a.data, a.stride, a.dtype}, 0, TACO_OK};
+  Checked c = {{a.data, a.stride, a.dtype}, 0, TACO_OK, 0, 0};
   if (a.data == nullptr) {
     if (need == kRequired && rows > 0) c.status = TACO_ERR_INVALID_ARG;
     return c;
@@ -39,7 +41,11 @@ Checked check_array(const taco_array& a, int64_t rows, int64_t cols, Need need, 
   else if (rows > 1 && a.stride > kMaxElems / rows) c.status = TACO_ERR_INVALID_ARG;
   else if (reinterpret_cast<uintptr_t>(a.data) % (uintptr_t)elem_bytes(a.dtype) != 0) c.status = TACO_ERR_ALIGN;
   if (rows <= 1) c.m.ld = cols;
-  if (c.status == TACO_OK && rows > 0) c.bytes = ((rows - 1) * c.m.ld + cols) * elem_bytes(a.dtype);
+  if (c.status == TACO_OK && rows > 0) {
+    c.bytes = ((rows - 1) * c.m.ld + cols) * elem_bytes(a.dtype);
+    c.row = cols * elem_bytes(a.dtype);
+    c.step = rows > 1 ? c.m.ld * elem_bytes(a.dtype) : 0;
+  }
   return c;
 }
 
@@ -47,7 +53,7 @@ Checked check_vector(const taco_array& a, int64_t n, Need need) { return check_a
 
 // Float32 vectors that are not given as taco_array.
 Checked check_floats(const float* p, int64_t n) {
-  Checked c = {{const_cast<float*>(p), n, TACO_F32}, 4 * n, TACO_OK};
+  Checked c = {{const_cast<float*>(p), n, TACO_F32}, 4 * n, TACO_OK, 4 * n, 0};
   if (p == nullptr) c.bytes = 0;
   else if (reinterpret_cast<uintptr_t>(p) % 4 != 0) c.status = TACO_ERR_ALIGN;
   return c;
@@ -59,21 +65,32 @@ int first_error(std::initializer_list<const Checked*> all) {
   return TACO_OK;
 }
 
+// Whether two arrays share a byte. Slices of columns of one tensor, which have
+// one stride, lie within each other's span without sharing any where their
+// columns differ.
+bool share(const Checked& a, const Checked& b) {
+  if (a.m.p == nullptr || b.m.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  if (!overlaps(a.m.p, a.bytes, b.m.p, b.bytes)) return false;
+  if (a.step == 0 || a.step != b.step) return true;
+  const intptr_t apart = reinterpret_cast<intptr_t>(b.m.p) - reinterpret_cast<intptr_t>(a.m.p);
+  const int64_t column = (int64_t)(apart % a.step + a.step) % a.step;   // of b's first element in a's rows
+  return column < a.row || column + b.row > a.step;
+}
+
 // No output may overlap an input or another output.
 bool any_overlap(std::initializer_list<const Checked*> ins, std::initializer_list<const Checked*> outs) {
   for (auto o = outs.begin(); o != outs.end(); ++o) {
-    if ((*o)->m.p == nullptr || (*o)->bytes == 0) continue;
     for (const Checked* i : ins)
-      if (i->m.p && i->bytes && overlaps(i->m.p, i->bytes, (*o)->m.p, (*o)->bytes)) return true;
+      if (share(*i, **o)) return true;
     for (auto q = outs.begin(); q != o; ++q)
-      if ((*q)->m.p && (*q)->bytes && overlaps((*q)->m.p, (*q)->bytes, (*o)->m.p, (*o)->bytes)) return true;
+      if (share(**q, **o)) return true;
   }
   return false;
 }
 
 // A workspace of `need` bytes as an array to check for overlaps.
 Checked check_workspace(void* ws, size_t ws_bytes, size_t need) {
-  Checked c = {{need ? ws : nullptr, 0, TACO_F32}, (int64_t)need, TACO_OK};
+  Checked c = {{need ? ws : nullptr, 0, TACO_F32}, (int64_t)need, TACO_OK, (int64_t)need, 0};
   if (need && (ws == nullptr || ws_bytes < need || !aligned16(ws))) c.status = TACO_ERR_WORKSPACE;
   return c;
 }
@@ -371,7 +388,7 @@ int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int3
   st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw});
   if (st != TACO_OK) return st;
   if (!dx.data && !dw.data) return TACO_ERR_INVALID_ARG;
-  const Backward b = {cd, cx, cw, cz, cdx, cdw, {kAbsent, 0, TACO_OK}, act, true, M, F, K};
+  const Backward b = {cd, cx, cw, cz, cdx, cdw, {kAbsent, 0, TACO_OK, 0, 0}, act, true, M, F, K};
   const Checked cws = check_workspace(workspace, ws_bytes, space_of(b, kSize));
   if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cws})) return TACO_ERR_INVALID_ARG;

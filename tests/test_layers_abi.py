@@ -76,25 +76,51 @@ def test_norm_workspace():
     assert size(7, 5120) == 7 * 2 * 5120 * 4 and size(1 << 20, 5120) == 512 * 2 * 5120 * 4
 
 
+class Fake:
+    """A tensor as the binding looks at it, on a GPU that need not be there."""
+
+    def __init__(self, t, where=0):
+        self.t, self.where, self.is_cuda = t, where, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def data_ptr(self):
+        return at(self.where)
+
+
 def test_binding_refuses_other_tensors():
     import torch
-    x = torch.zeros(4, 8)
+    x, y = Fake(torch.zeros(4, 8)), Fake(torch.zeros(4, 8), 1)
     v = torch.zeros(8)
-    with pytest.raises(TypeError):
-        T.taco_layer_norm(x.double(), None, None, 1e-5, x)
-    with pytest.raises(TypeError):
-        T.taco_layer_norm(x, None, None, 1e-5, x, mean=torch.zeros(4, dtype=torch.bfloat16))
+    for error, kw in [
+            (TypeError, dict(x=Fake(torch.zeros(4, 8).double()))),
+            (TypeError, dict(mean=Fake(torch.zeros(4, dtype=torch.bfloat16), 2))),
+            (ValueError, dict(weight=Fake(torch.zeros(7), 2))),
+            (ValueError, dict(bias=Fake(torch.zeros(16)[::2], 2))),
+            (ValueError, dict(y=Fake(torch.zeros(8, 4).t(), 1))),
+            (ValueError, dict(y=Fake(torch.zeros(4, 9), 1))),
+            (ValueError, dict(y=torch.zeros(4, 8))), (ValueError, dict(weight=v)), (ValueError, dict(rstd=torch.zeros(4))),
+            (T.TacoError, dict(y=x)), (T.TacoError, dict(x=Fake(torch.zeros(1, 8).expand(4, 8)))),
+            (T.TacoError, dict(eps=-1.0))]:
+        a = dict(dict(x=x, weight=None, bias=None, eps=1e-5, y=y), **kw)
+        with pytest.raises(error):
+            T.taco_layer_norm(**a)
     with pytest.raises(ValueError):
-        T.taco_layer_norm(x, torch.zeros(7), None, 1e-5, x)
+        T.taco_layer_norm_backward(x, y, None, None, None, dx=Fake(torch.zeros(4, 8), 2), workspace=torch.zeros(64))
     with pytest.raises(ValueError):
-        T.taco_layer_norm(x, None, v[::2].expand(4), 1e-5, x)
+        T.taco_linear(x, Fake(torch.zeros(3, 7), 2), y)
     with pytest.raises(ValueError):
-        T.taco_layer_norm(x, None, None, 1e-5, torch.zeros(8, 4).t())
-    with pytest.raises(ValueError):
-        T.taco_layer_norm(x, None, None, 1e-5, torch.zeros(4, 9))
-    with pytest.raises(T.TacoError):
-        T.taco_layer_norm(x, None, None, 1e-5, x)     # the output is the input
+        T.taco_gated_linear(x, Fake(torch.zeros(5, 8), 2), Fake(torch.zeros(4, 2), 3))
     assert ctypes.sizeof(T.taco_array) == 24
+
+
+@pytest.mark.parametrize("off", [0, 2, 126, 130, 254, -2, -126, -130, 2 * 256 + 126])
+def test_slices_that_share_columns_overlap(off):
+    """y lies `off` bytes from x in one tensor of 128 columns, 64 of them each
+    (tests on the GPU run on slices that share none)."""
+    wide = 64 + 64
+    assert norm(x=arr(0, wide, B, 1 << 20), y=arr(0, wide, B, (1 << 20) + off)) == INVALID
 
 
 def linear(M=4, N=16, K=24, x=None, w=None, bias=None, act=0, residual=None, out=None, preact=None, ws=at(9),

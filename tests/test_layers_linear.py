@@ -428,3 +428,35 @@ def test_same_bits_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(o, eager[i])), i
+
+
+def test_offsets_beyond_32_bits():
+    """Rows that reach past 2^31 elements (and 2^32 bytes) of their tensor:
+    2^20 rows 2104 elements apart. Whole numbers: exact, the sums over a
+    million rows included."""
+    M, N, K, apart = (1 << 20) + 37, 24, 40, 2104
+    gen = generator(15)
+
+    def far(cols, dtype=BF):
+        return torch.empty(M * apart, dtype=dtype, device=DEV).view(M, apart)[:, :cols]
+
+    x, d = far(K), far(N)
+    x.copy_(torch.randint(-1, 2, (M, K), generator=gen, device=DEV))
+    d.copy_(torch.randint(-1, 2, (M, N), generator=gen, device=DEV))
+    w = whole(gen, N, K, 2)
+    out, dx = far(N), far(K)
+    T.taco_linear(x, w, out, workspace=space(T.taco_linear_workspace_bytes(M, N, K)))
+    dw, db = torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    T.taco_linear_backward(d, x, w, dx=dx, dw=dw, dbias=db,
+                           workspace=space(T.taco_linear_backward_workspace_bytes(M, N, K)))
+    torch.cuda.synchronize()
+    x64, d64 = x.double(), d.double()
+    assert torch.equal(out.double(), x64 @ w.double().t())
+    assert torch.equal(dx.double(), d64 @ w.double())
+    assert torch.equal(dw.double(), d64.t() @ x64)
+    assert torch.equal(db.double(), d64.sum(0))
+    y = far(K)
+    T.taco_layer_norm(x, None, None, 1e-5, y)
+    torch.cuda.synchronize()
+    want = torch.nn.functional.layer_norm(x64[-1000:], (K,))
+    within(y[-1000:], want, 2.0 ** -8 * want.abs() + 1e-4, "norm")

@@ -109,6 +109,22 @@ def test_forward_constant_and_nonfinite_rows():
         assert torch.equal(y.t[good], clean.t)
 
 
+def test_between_slices_of_one_tensor():
+    """x and y are columns of one tensor, side by side; the rest of it stays."""
+    gen = generator(17)
+    rows, cols = 50, 136
+    for dt in (BF, F):
+        wide = matrix(gen, rows, 3 * cols, dt)
+        before = wide.clone()
+        T.taco_layer_norm(wide[:, cols:2 * cols], None, None, EPS, wide[:, :cols])
+        want = torch.empty(rows, cols, dtype=dt, device=DEV)
+        T.taco_layer_norm(before[:, cols:2 * cols].contiguous(), None, None, EPS, want)
+        torch.cuda.synchronize()
+        assert torch.equal(wide[:, :cols], want) and torch.equal(wide[:, cols:], before[:, cols:])
+        with pytest.raises(T.TacoError):
+            T.taco_layer_norm(wide[:, cols:2 * cols], None, None, EPS, wide[:, 2 * cols - 1:3 * cols - 1])
+
+
 def backward64(dy, x, weight, mean, rstd):
     dy, x, mean, rstd = dy.double(), x.double(), mean.double()[:, None], rstd.double()[:, None]
     xhat = (x - mean) * rstd
