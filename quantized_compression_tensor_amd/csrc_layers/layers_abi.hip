@@ -198,7 +198,7 @@ struct Backward {
     const bool own_dz = worst || gated || act != TACO_ACT_NONE || ((want_dx || want_dw) && !in_place(dout.m, n));
     PackArgs pack = {};
     ActBackArgs b = {};
-    b.dout = dout.m; b.z = z.m; b.M = m; b.N = (int)n; b.act = act; b.gated = gated; b.ld_dz = ld_dz; b.dbias = db.m;
+    b.dout = dout.m; b.z = z.m; b.M = m; b.N = (int)n; b.act = act; b.gated = gated; b.ld_dz = ld_dz;
     Operand dz = {static_cast<const uint16_t*>(dout.m.p), dout.m.ld, false};
     if (own_dz) {
       b.dz = static_cast<uint16_t*>(space->take((size_t)(m * ld_dz) * 2));
@@ -212,9 +212,10 @@ struct Backward {
     const size_t dw_bytes = want_dw ? gemm_partial_bytes(wide, k, m, false) : 0;
     const size_t db_bytes = want_db ? (size_t)act_back_groups(m) * (size_t)n * sizeof(float) : 0;
     const size_t both_bytes = want_dx && want_dw ? gemm_pair_partial_bytes(m, wide, k) : 0;
-    void* rest = space->take(std::max({dx_bytes, dw_bytes, db_bytes, both_bytes}));
+    void* rest = space->take(std::max({dx_bytes, dw_bytes, both_bytes}));
+    if (want_db) b.partials = static_cast<float*>(space->take(db_bytes));
     if (what != kRun) return hipSuccess;
-    if (want_db) b.partials = static_cast<float*>(rest);
+    const ColumnSumArgs sum = {b.partials, n, 0, act_back_groups(m), (int)n, {want_db ? db.m : kAbsent, kAbsent}};
     hipError_t err = hipSuccess;
     if (own_dz || want_db) err = launch_act_back(b, pack, stream);
     else if (pack.count > 0) err = launch_pack(pack, stream);
@@ -223,10 +224,11 @@ struct Backward {
     gx.a = dz; gx.b = ow; gx.M = m; gx.N = (int)k; gx.K = wide; gx.e.out = dx.m;
     dz.by_k = true;
     gw.a = dz; gw.b = ox; gw.M = wide; gw.N = (int)k; gw.K = m; gw.e.out = dw.m;
-    if (want_dx && want_dw) return launch_gemm_pair(gx, gw, rest, stream);
-    if (want_dx) err = launch_gemm(gx, rest, stream);
-    if (want_dw) err = launch_gemm(gw, rest, stream);
-    return err;
+    if (want_dx && want_dw) return launch_gemm_pair(gx, gw, sum, rest, stream);
+    launch_column_sum(sum, stream);
+    if (want_dx) return launch_gemm(gx, rest, stream);
+    if (want_dw) return launch_gemm(gw, rest, stream);
+    return hipGetLastError();
   }
 };
 

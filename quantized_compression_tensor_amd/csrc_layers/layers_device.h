@@ -165,4 +165,40 @@ TACO_DEV float lanes_sum(float v) {
   return v;
 }
 
+// Column sums (ColumnSumArgs), output y: `block` takes 64 columns, every
+// sixteenth row by itself, eight loads under way, so that a sum's order is the
+// same for any number of waves. `sums`: 16 * 64 floats of LDS.
+constexpr int kSumParts = 16;
+template <int WAVES>
+TACO_DEV void column_sum(const ColumnSumArgs& a, unsigned block, unsigned y, float* sums) {
+  const int lane = (int)threadIdx.x % kWave, wave = wave_in_group();
+  const int c = (int)block * kWave + lane;
+  const Mat out = a.out[y];
+  if (out.p == nullptr) return;
+  const float* in = a.in + (y ? a.second : 0) + c;
+#pragma unroll
+  for (int part = wave; part < kSumParts; part += WAVES) {
+    float t = 0.0f;
+    if (c < a.cols) {
+      int r = part;
+      for (; r + 7 * kSumParts < a.count; r += 8 * kSumParts) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = in[(r + i * kSumParts) * a.ld];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += f[i];
+      }
+      for (; r < a.count; r += kSumParts) t += in[r * a.ld];
+    }
+    sums[part * kWave + lane] = t;
+  }
+  __syncthreads();
+  if (wave == 0 && c < a.cols) {
+    float t = sums[lane];
+#pragma unroll
+    for (int w = 1; w < kSumParts; ++w) t += sums[w * kWave + lane];
+    store1(out.p, out.dt, c, t);
+  }
+}
+
 }  // namespace taco

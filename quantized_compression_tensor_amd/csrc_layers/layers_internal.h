@@ -31,6 +31,16 @@ struct NormArgs {
 // holds.
 constexpr int kNormGroups = 512;
 
+// out[0] [cols] = the sum of `count` rows of `in`, ld apart, and out[1] that of
+// the columns `second` floats further on (zeros if count is 0; each may be
+// absent).
+struct ColumnSumArgs {
+  const float* in;
+  int64_t ld, second;
+  int count, cols;
+  Mat out[2];
+};
+
 struct NormBackArgs {
   Mat dy, x, weight, dx, dweight, dbias;
   int64_t rows;
@@ -103,7 +113,6 @@ struct ActBackArgs {
   uint16_t* dz;         // bf16 [M, ld_dz], null: not wanted
   int64_t ld_dz;
   float* partials;      // [act_back_groups][N], null: no column sums
-  Mat dbias;
 };
 int act_back_groups(int64_t M);
 
@@ -116,15 +125,12 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
-// Both gradients of a projection, dx [M, K] and dw [wide, K], as one launch
-// where they are small; gemm_pair_partial_bytes: for these, else 0.
+// Both gradients of a projection, dx [M, K] and dw [wide, K], and a column
+// sum, as one launch where they are small; gemm_pair_partial_bytes: for these,
+// else 0.
 size_t gemm_pair_partial_bytes(int64_t M, int64_t wide, int64_t K);
-hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, void* partials, hipStream_t s);
+hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, const ColumnSumArgs& sum, void* partials, hipStream_t s);
 hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s);   // and launch_pack's work
-// out0 [cols] = the sum of `count` rows of `in`, ld apart, and out1 that of
-// the columns `second` floats further on (zeros if count is 0; each may be
-// absent).
-void launch_column_sum(const float* in, int64_t ld, int64_t second, int count, int64_t cols, const Mat& out0,
-                       const Mat& out1, hipStream_t s);
+void launch_column_sum(const ColumnSumArgs& a, hipStream_t s);
 
 }  // namespace taco

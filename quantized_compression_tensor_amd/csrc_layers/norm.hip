@@ -304,51 +304,15 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_back_sums(NormBackArgs a)
   store8<false>(part, kF32, a.cols + c, n, db);
 }
 
-// Sums over `count` rows of `cols` floats, ld apart, into up to two outputs
-// (blockIdx.y; the second's columns `second` floats after the first's): 64
-// columns per workgroup, its sixteen waves every sixteenth row each, eight
-// loads under way.
-struct ColumnSumArgs {
-  const float* in;
-  int64_t ld, second;
-  int count, cols;
-  Mat out[2];
-};
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(kSumWaves * kWave) void k_column_sum(ColumnSumArgs a) {
-  __shared__ float sums[kSumWaves][kWave];
-  const int lane = (int)threadIdx.x % kWave, wave = wave_in_group(), y = (int)blockIdx.y;
-  const int c = (int)blockIdx.x * kWave + lane;
-  const Mat out = a.out[y];
-  if (out.p == nullptr) return;
-  const float* in = a.in + (y ? a.second : 0) + c;
-  float t = 0.0f;
-  if (c < a.cols) {
-    int r = wave;
-    for (; r + 7 * kSumWaves < a.count; r += 8 * kSumWaves) {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = in[(r + i * kSumWaves) * a.ld];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t += f[i];
-    }
-    for (; r < a.count; r += kSumWaves) t += in[r * a.ld];
-  }
-  sums[wave][lane] = t;
-  __syncthreads();
-  if (wave == 0 && c < a.cols) {
-#pragma unroll
-    for (int w = 1; w < kSumWaves; ++w) t += sums[w][lane];
-    store1(out.p, out.dt, c, t);
-  }
+__global__ __launch_bounds__(kSumParts * kWave) void k_column_sum(ColumnSumArgs a) {
+  __shared__ float sums[kSumParts * kWave];
+  column_sum<kSumParts>(a, blockIdx.x, blockIdx.y, sums);
 }
 
-void launch_column_sum(const float* in, int64_t ld, int64_t second, int count, int64_t cols, const Mat& out0,
-                       const Mat& out1, hipStream_t s) {
-  if (out0.p == nullptr && out1.p == nullptr) return;
-  const ColumnSumArgs a = {in, ld, second, count, (int)cols, {out0, out1}};
-  const dim3 grid((unsigned)((cols + kWave - 1) / kWave), out1.p ? 2 : 1);
-  hipLaunchKernelGGL(k_column_sum, grid, dim3(kSumWaves * kWave), 0, s, a);
+void launch_column_sum(const ColumnSumArgs& a, hipStream_t s) {
+  if (a.out[0].p == nullptr && a.out[1].p == nullptr) return;
+  const dim3 grid((unsigned)((a.cols + kWave - 1) / kWave), a.out[1].p ? 2 : 1);
+  hipLaunchKernelGGL(k_column_sum, grid, dim3(kSumParts * kWave), 0, s, a);
 }
 
 // How rows of `cols` elements are held.
@@ -443,7 +407,8 @@ hipError_t launch_norm_back(NormBackArgs a, hipStream_t s) {
       });
     });
   }
-  if (sums) launch_column_sum(a.partials, 2 * (int64_t)a.cols, a.cols, groups, a.cols, a.dweight, a.dbias, s);
+  if (sums)
+    launch_column_sum(ColumnSumArgs{a.partials, 2 * (int64_t)a.cols, a.cols, groups, a.cols, {a.dweight, a.dbias}}, s);
   return hipGetLastError();
 }
 
