@@ -102,6 +102,25 @@ def test_linear_exact(size):
     assert torch.equal(plain.t, (x.double() @ w.double().t()).to(BF))
 
 
+@pytest.mark.parametrize("bias,residual,out", [(F, F, F), (BF, F, BF), (F, BF, F)])
+@pytest.mark.parametrize("size", [(2, 40, 64), (128, 256, 128), (130, 260, 128), (3584, 3840, 64), (3600, 3604, 72)])
+def test_epilogue_types(size, bias, residual, out):
+    """Tiles with and without an edge, of either size, in each element type."""
+    M, N, K = size
+    gen = generator(M + N + K)
+    x, w = whole(gen, M, K, 1), whole(gen, N, K, 1)
+    b, r = whole(gen, 1, N, 8, dtype=bias)[0], whole(gen, M, N, 8, dtype=residual)
+    o, z = Out(M, N, out), Out(M, N, out)
+    T.taco_linear(x, w, o.t, bias=b, act=RELU, residual=r, preact=z.t,
+                  workspace=space(T.taco_linear_workspace_bytes(M, N, K)))
+    torch.cuda.synchronize()
+    o.check("out")
+    z.check("preact")
+    want = x.double() @ w.double().t() + b.double()
+    assert torch.equal(z.t, want.to(out))
+    assert torch.equal(o.t, (want.clamp(min=0) + r.double()).to(out))
+
+
 @pytest.mark.parametrize("size", SIZES, ids=ids)
 def test_gated_exact(size):
     M, N, K, pad, offset = size
