@@ -526,10 +526,11 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   // once (the sums move down instead: its copies did not fit the instruction
   // cache), and tiles without an edge take a path of their own, whose branches
   // are all scalar: 2048 x 2048 x 64 7.4 to 6.3 us, 4096 x 4096 x 512 with
-  // bias, gelu and a residual 38.6 to 32.3. Turns of 32 rows need more
-  // registers with an activation and a residual than there are.
+  // bias, gelu and a residual 38.6 to 32.3. A turn has 32 rows (gated 4096 x
+  // 4096 x 512 43.4 us, with 16 rows 46.4), or 16 where there may be a residual,
+  // whose registers there are not enough of.
   constexpr bool kPlain = BK_;   // a gradient: the sum itself is the output
-  constexpr int kLd = TL::kTurnLd, kTurnRows = kPlain ? TL::kTurnMost : 16, kTurn = kTurnRows / 16;
+  constexpr int kLd = TL::kTurnLd, kTurnRows = kPlain || GATED ? TL::kTurnMost : 16, kTurn = kTurnRows / 16;
   constexpr int kWaveCols = GATED ? TN * 8 : TN * 16, kLanes = kWaveCols / 8;
   constexpr int kPass = kWave / kLanes, kRound = kTurnRows / kPass;   // rows of a pass, passes
   float* turn = reinterpret_cast<float*>(lds) + wave * kTurnRows * kLd;
