@@ -154,19 +154,28 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    if torch.cuda.is_initialized():
-        return _current_stream(torch.cuda.current_device())
-    return None
+    if _current_stream is None:
+        _find_current_stream()
+    return _current_stream() if _current_stream is not None else None
 
 
-def _current_stream(device):
-    """The handle of torch's current stream. torch builds a Stream object for
-    torch.cuda.current_stream() (about 3 us, as long as a launch); the plain
-    handle is taken from the function beneath where torch has it."""
+_current_stream = None   # gives the handle of torch's current stream, once torch has initialised the GPU
+
+
+def _find_current_stream():
+    """torch builds a Stream object for torch.cuda.current_stream() (about 3 us,
+    as long as a launch); the plain handle is taken from the functions beneath
+    where torch has them (0.1 us)."""
     import torch
+    global _current_stream
+    if not torch.cuda.is_initialized():
+        return
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        _current_stream = lambda: raw(device())   # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
 
 
 def _check(status, where):
