@@ -5,6 +5,12 @@
 // in float32 on the bf16 matrix cores. An operand lies in memory with its k
 // contiguous (x and W of the forward pass) or with its rows contiguous (W for
 // dx = dz W, dz and x for dw = dz^T x).
+//
+// The backward pass first makes dz = dout act'(z) (gated: its two halves) in
+// bf16, which is what the matrix cores take: one rounding of 2^-8 that both
+// products share. The bias's gradient is summed from dz before that rounding.
+// Working z out again inside both products would cost an activation for every
+// tile that reads it, and rounding is needed there just the same.
 #include <algorithm>
 #include <type_traits>
 
@@ -399,7 +405,7 @@ TACO_DEV void hand_over() {
 
 // The kernel of every product: a workgroup sums one output tile over one part
 // of K, in steps of 64 k, two slices of 32 each. What bounds it is how far
-// ahead of their use loads can be under way (a step lasts about 0.9 us, a load
+// ahead of their use loads can be under way (a step lasts about 1.4 us, a load
 // about 1.3 us when every CU loads), so the LDS holds three steps of a and two
 // of b, and a stage is handed back as soon as it has been read: b's operands
 // are all in registers early in a step, a's follow one 16-row tile behind the
@@ -407,12 +413,18 @@ TACO_DEV void hand_over() {
 // or two steps' time. The 16 x 16 x 32 products were faster than 32 x 32 x 16
 // (8192^3: 750 against 815 us) although they leave more gaps: this size is
 // bound by power, and they move half as many sums through the registers.
+// Measured, random values: 8192^3 forward 737 us (1490 TFLOP/s), dx 763, dw
+// 798; 4096^3 96 (1425), 100 and 104. The matrix cores are busy 0.73 of the
+// time at 8192^3, at 1.6 GHz, and 0.67 and 0.62 in the gradients, at 2.1.
+// A small tile alone on its CU takes 0.55 us a step, of which LDS accesses are
+// 0.33; five stages of a and four of b instead of three and two changed none of
+// it, and two such workgroups on a CU were faster than one (1024 x 4096 x 4096
+// 50.7 us, with the deeper stages 60.3).
 // `block`: of the product's a.whole + a.rest * a.parts.
 template <class TL, bool AK, bool BK_, bool GATED>
 TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
-  
   static_assert(!GATED || TN == 4, "a wave holds the two projections of its columns");
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
@@ -627,7 +639,9 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm_pair(GemmArgs dx, Gemm
 }
 
 // Joins the parts of the tiles whose K is cut, in order, and finishes: a
-// workgroup takes some rows of a tile (blockIdx.x), a lane eight columns.
+// workgroup takes some rows of a tile (blockIdx.x), a lane eight columns. Bound
+// by the parts' bytes, mostly out of the Infinity Cache: 15 us for 128 gated
+// tiles in two parts with both projections kept (92 MB, 6 TB/s).
 template <class TL, bool GATED>
 __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, kCols = GATED ? BN / 2 : BN, kOcts = kCols / 8, kRows = 256 / kOcts;
@@ -662,11 +676,15 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
 // Up to 32 rows of x: the weight's bytes bound it, so every weight is read
 // once, straight into the registers of a 16 x 16 x 32 product whose other
 // operand is x (rows past the last one repeat it; their sums are not stored).
-// A workgroup takes up to 16 weight rows (gated: eight of each projection;
-// as many as give every CU the same number of workgroups), its sixteen waves units of 64 k in turn, so that a row's bytes are read 2 KiB at
-// a time, two units of a wave together. The waves' sums are joined in LDS.
-// Rows may start anywhere. One row, 8192 x 8192 weights: 27.8 us, 4.8 TB/s
-// (eight waves with eight units each 31.8 us); 4096 x 4096: 7.9 us.
+// A workgroup takes up to 16 weight rows (gated: eight of each projection; as
+// many as give every CU the same number of workgroups), its sixteen waves units
+// of 64 k in turn, so that a row's bytes are read 2 KiB at a time, two units of
+// a wave together. The waves' sums are joined in LDS. Rows may start anywhere.
+// One row, 8192 x 8192 weights: 27.6 us, 4.9 TB/s (eight waves with eight units
+// each 31.8 us); 4096 x 4096: 7.6 us. With 24 rows the reads of x, which every
+// workgroup makes, are as many as those of the weights: 24 x 5120 into 2 x 1728
+// gated 13.8 us (2.6 TB/s). Loading further ahead was slower everywhere (that
+// one 19.7 us and more), and x's lanes without a row left out no faster.
 constexpr int kFewRows = 32, kFewWaves = 16;
 
 template <int TM, bool GATED>
@@ -939,8 +957,11 @@ hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
 // ------------------------------------------------- backward of activations --
 
 // Workgroup `group` of `groups` takes 512 columns (`slab`) of a range of rows,
-// a wave every fourth row of them, two at a time, a lane eight neighbouring columns. Eight
-// rows are a range; more where there would be over kActMaxGroups ranges.
+// a wave every fourth row of them, two at a time, a lane eight neighbouring
+// columns. Eight rows are a range; more where there would be over kActMaxGroups
+// ranges. Memory bounds it: gated 8192 x 5120, silu, 84 us (5.0 TB/s). With
+// gelu's slope the arithmetic takes about as long as the bytes, and the sums
+// of dbias add a tenth of them: 4096 x 4096 27 us (3.9 TB/s).
 constexpr int kActRows = 8, kActMaxGroups = 1024;
 int act_back_groups(int64_t M) {
   const int64_t g = (M + kActRows - 1) / kActRows;
