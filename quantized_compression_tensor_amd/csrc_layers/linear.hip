@@ -932,7 +932,9 @@ TACO_DEV void pack(const PackArgs& a, unsigned block, unsigned blocks, unsigned 
   const PackArgs::One m = a.m[which];
   const int64_t octs = m.ld / 8, total = m.rows * octs;
   for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
-    const int64_t row = i / octs, c = (i - row * octs) * 8, left = m.cols - c;
+    // (a division in 64 bits takes five times as long)
+    const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)octs : i / octs;
+    const int64_t c = (i - row * octs) * 8, left = m.cols - c;
     Oct<kBF16> o;
     o.load(m.src.p, row * m.src.ld + c, left < 8 ? (int)left : 8);
     *reinterpret_cast<u32x4*>(m.dst + row * m.ld + c) = o.v;
@@ -968,6 +970,32 @@ int act_back_groups(int64_t M) {
   return (int)(g < kActMaxGroups ? g : kActMaxGroups);
 }
 
+// d = d act'(z), and of the gated layer u = d u act'(z), d = d act(z).
+TACO_DEV void times_slope(const float* z, float* d, int act) {
+  auto each = [&](int which) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], which);
+  };
+  if (act == kActGelu) each(kActGelu);
+  else if (act == kActSilu) each(kActSilu);
+  else each(kActRelu);
+}
+TACO_DEV void act_back_gated(const float* z, float* u, float* d, int act) {
+  auto each = [&](int which) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float value, slope;
+      act_both(z[e], which, &value, &slope);
+      u[e] = d[e] * u[e] * slope;
+      d[e] = d[e] * value;
+    }
+  };
+  if (act == kActGelu) each(kActGelu);
+  else if (act == kActSilu) each(kActSilu);
+  else if (act == kActRelu) each(kActRelu);
+  else each(kActNone);
+}
+
 template <bool GATED>
 TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, unsigned slab) {
   __shared__ float sums[4][512];
@@ -980,40 +1008,52 @@ TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, un
   for (int e = 0; e < 8; ++e) db[e] = 0.0f;
   // dz's rows are whole eights: zeros past the last column
   const int pad = n < 8 && n > 0 && !GATED ? 8 : n;
-  for (int64_t m = first + wave; m < end && n > 0; m += 8) {
-    float d[2][8], z[2][8], u[2][8];
+  // Z: z's type; WHOLE: each lane has eight columns
+  auto rows = [&](auto z_type, auto whole) {
+    constexpr int Z = z_type();
+    constexpr bool WHOLE = whole();
+    const int have = WHOLE ? 8 : n;
+    for (int64_t m = first + wave; m < end; m += 8) {
+      float d[2][8], z[2][8], u[2][8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t row = m + 4 * i;
-      if (row >= end) break;
-      load8(a.dout.p, a.dout.dt, row * a.dout.ld + c, n, d[i]);
-      if (GATED || a.act != kActNone) load8(a.z.p, a.z.dt, row * a.z.ld + c, n, z[i]);
-      if (GATED) load8(a.z.p, a.z.dt, row * a.z.ld + a.N + c, n, u[i]);
-    }
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = m + 4 * i;
+        if (row >= end) break;
+        load8(a.dout.p, kBF16, row * a.dout.ld + c, have, d[i]);
+        if (GATED || a.act != kActNone) load8(a.z.p, Z, row * a.z.ld + c, have, z[i]);
+        if (GATED) load8(a.z.p, Z, row * a.z.ld + a.N + c, have, u[i]);
+      }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t row = m + 4 * i;
-      if (row >= end) break;
-      if constexpr (GATED) {
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = m + 4 * i;
+        if (row >= end) break;
+        if constexpr (GATED) {
+          act_back_gated(z[i], u[i], d[i], a.act);
+          store8(a.dz, kBF16, row * a.ld_dz + c, have, u[i]);
+          store8(a.dz, kBF16, row * a.ld_dz + a.N + c, have, d[i]);
+        } else {
+          if (a.act != kActNone) times_slope(z[i], d[i], a.act);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float value, slope;
-          act_both(z[i][e], a.act, &value, &slope);
-          u[i][e] = d[i][e] * u[i][e] * slope;
-          d[i][e] = d[i][e] * value;
+          for (int e = 0; e < 8; ++e) {
+            if (!WHOLE && e >= n) d[i][e] = 0.0f;
+            db[e] += d[i][e];
+          }
+          if (a.dz) store8(a.dz, kBF16, row * a.ld_dz + c, WHOLE ? 8 : pad, d[i]);
         }
-        store8(a.dz, kBF16, row * a.ld_dz + c, n, u[i]);
-        store8(a.dz, kBF16, row * a.ld_dz + a.N + c, n, d[i]);
-      } else {
-        if (a.act != kActNone) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[i][e] = e < n ? d[i][e] * act_slope(z[i][e], a.act) : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) db[e] += d[i][e];
-        if (a.dz) store8(a.dz, kBF16, row * a.ld_dz + c, pad, d[i]);
       }
     }
+  };
+  const std::integral_constant<int, kBF16> bf16;
+  const std::integral_constant<int, kF32> f32;
+  // (wave-uniform, so that a wave runs one of them)
+  const bool whole = a.N % 8 == 0 || ((int)slab + 1) * kWave * 8 <= a.N;
+  if (n <= 0) {
+  } else if (whole) {
+    if (a.z.dt == kBF16) rows(bf16, std::true_type());
+    else rows(f32, std::true_type());
+  } else {
+    if (a.z.dt == kBF16) rows(bf16, std::false_type());
+    else rows(f32, std::false_type());
   }
   if constexpr (GATED) {
     // zeros past the last column of the second half
