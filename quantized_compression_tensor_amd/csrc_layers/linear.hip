@@ -416,10 +416,9 @@ TACO_DEV void hand_over() {
 // Measured, random values: 8192^3 forward 737 us (1490 TFLOP/s), dx 763, dw
 // 798; 4096^3 96 (1425), 100 and 104. The matrix cores are busy 0.73 of the
 // time at 8192^3, at 1.6 GHz, and 0.67 and 0.62 in the gradients, at 2.1.
-// A small tile alone on its CU takes 0.55 us a step, of which LDS accesses are
-// 0.33; five stages of a and four of b instead of three and two changed none of
-// it, and two such workgroups on a CU were faster than one (1024 x 4096 x 4096
-// 50.7 us, with the deeper stages 60.3).
+// A small tile alone on its CU takes 0.55 us a step, two together 1.1 for both:
+// the LDS is what bounds them (96 KB a step), and five stages of a and four of
+// b instead of three and two, for one of them on a CU, were no faster.
 // `block`: of the product's a.whole + a.rest * a.parts.
 template <class TL, bool AK, bool BK_, bool GATED>
 TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
@@ -783,27 +782,32 @@ struct Plan {
   int64_t part;
 };
 
+constexpr int64_t kCus = 256;
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
 
-// `taken`: slots that another product fills at the same time.
-static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int64_t taken = 0) {
+// `other`: steps of the tiles of another product that run at the same time.
+static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int64_t other = 0) {
   const int64_t large = tiles_of(M, N, 256, gated ? 128 : 256), steps = (K + 63) / 64;
   const bool is_large = large >= 192;
   const int64_t tiles = is_large ? large : tiles_of(M, N, 128, gated ? 64 : 128);
-  // Tiles that run at once: one of 256 x 256 on a CU, or two of 128 x 128.
-  const int64_t slots = std::max<int64_t>((is_large ? 256 : 512) - taken, 1);
-  // The last round of tiles, if it fills less than half of them, has its K cut
-  // so that it does. A part keeps at least eight steps (with four, 128 x 4096 x
-  // 4096 took 23.4 us, with eight 18.8).
-  const int64_t rest = tiles % slots;
-  int64_t parts = rest > 0 ? std::min<int64_t>(std::min(slots / rest, steps / 8), 16) : 1;
-  // What that saves (a step of the last round takes 1.5 us, or 0.9 us) against
-  // the parts' way through memory, 30 us for a full round of large tiles and
-  // half of that for small ones, and the launch that joins them.
-  if (parts > 1) {
-    const double saved = (double)(steps - (steps + parts - 1) / parts) * (is_large ? 1.5 : 0.9);
-    const double cost = 5.0 + (is_large ? 30.0 : 15.0) * (double)(rest * parts) / (double)slots;
-    if (saved < cost) parts = 1;
+  // Tiles go to 256 CUs: one of 256 x 256 at a time, or two of 128 x 128, which
+  // take twice as long together. The last round of tiles, if it is not full,
+  // has its K cut where that shortens it by more than the parts' way through
+  // memory and the launch that joins them take: 1100 x 4000 x 4000 47.8 us, cut
+  // for two small tiles to a CU 64.1; gated 512 x 5120 x 5120 71.3 us, not cut
+  // 91.7. Times in us: a step, a round of parts, the launch. A part keeps at
+  // least eight steps (with four, 128 x 4096 x 4096 took 23.4 us, with eight
+  // 18.8).
+  const double step = is_large ? 1.45 : 0.56, round = is_large ? 30.0 : 6.0, launch = 3.0;
+  const int64_t rest = tiles % kCus, most = std::min<int64_t>(steps / 8, 16);
+  int64_t parts = 1;
+  double least = 0.0;
+  for (int64_t p = 1; rest > 0 && p <= std::max<int64_t>(most, 1); ++p) {
+    const int64_t per = (steps + p - 1) / p;
+    const double busy = other > 0 ? std::max((double)per, (double)(tiles * steps + other) / (double)kCus)
+                                  : (double)((rest * p + kCus - 1) / kCus * per);
+    const double t = busy * step + (p > 1 ? launch + round * (double)(rest * p) / (double)kCus : 0.0);
+    if (p == 1 || t < least) parts = p, least = t;
   }
   if (parts <= 1) return Plan{is_large, (unsigned)tiles, 0, 1, 0};
   const int64_t per = (steps + parts - 1) / parts;
@@ -826,7 +830,8 @@ struct PairPlan {
 };
 static PairPlan pair_plan_of(int64_t M, int64_t wide, int64_t K) {
   const int64_t dx_tiles = tiles_of(M, K, 128, 128), dw_tiles = tiles_of(wide, K, 128, 128);
-  PairPlan p = {false, plan_of(M, K, wide, false, dw_tiles), plan_of(wide, K, M, false, dx_tiles)};
+  PairPlan p = {false, plan_of(M, K, wide, false, dw_tiles * ((M + 63) / 64)),
+                plan_of(wide, K, M, false, dx_tiles * ((wide + 63) / 64))};
   p.together = M > 0 && !p.dx.large && !p.dw.large && dx_tiles + dw_tiles <= 512;
   return p;
 }

@@ -38,7 +38,7 @@ SIZES = [
     (127, 128, 64, 0, 0), (128, 128, 128, 0, 0), (129, 127, 129, 1, 1), (200, 520, 192, 24, 16), (255, 257, 320, 0, 0),
     (256, 256, 256, 0, 0), (257, 264, 328, 0, 8), (300, 1032, 1288, 0, 0), (512, 512, 4096, 0, 0),
     (511, 515, 1021, 3, 0), (768, 768, 512, 8, 0), (1001, 777, 1285, 3, 1), (2048, 2048, 256, 0, 0),
-    (3000, 1100, 136, 4, 4), (4100, 4104, 72, 0, 0), (70000, 24, 16, 0, 0), (130, 60008, 24, 0, 0),
+    (1500, 1480, 6000, 0, 0), (3000, 1100, 136, 4, 4), (4100, 4104, 72, 0, 0), (70000, 24, 16, 0, 0), (130, 60008, 24, 0, 0),
 ]
 
 
