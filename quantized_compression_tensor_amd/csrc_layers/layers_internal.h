@@ -71,14 +71,14 @@ struct Operand {
   bool by_k;
 };
 
-// Up to two matrices to be copied with rows on 16 bytes and zeros up to the
-// next multiple of eight elements.
+// Up to two matrices to be copied with zeros up to the next multiple of eight
+// elements.
 struct PackArgs {
   struct One {
     Mat src;
     int64_t rows, cols;
     uint16_t* dst;
-    int64_t ld;   // a multiple of 8, at least cols
+    int64_t ld;   // a multiple of 8
   } m[2];
   int count;
 };

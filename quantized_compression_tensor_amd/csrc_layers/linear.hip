@@ -935,7 +935,7 @@ hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, const ColumnSumArgs& sum, 
 // lane takes eight elements; `block` of `blocks` for matrix `which`.
 TACO_DEV void pack(const PackArgs& a, unsigned block, unsigned blocks, unsigned which) {
   const PackArgs::One m = a.m[which];
-  const int64_t octs = m.ld / 8, total = m.rows * octs;
+  const int64_t octs = (m.cols + 7) / 8, total = m.rows * octs;
   for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
     // (a division in 64 bits takes five times as long)
     const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)octs : i / octs;
@@ -950,7 +950,7 @@ __global__ __launch_bounds__(256) void k_pack(PackArgs a) { pack(a, blockIdx.x, 
 // Workgroups for each matrix.
 static unsigned pack_blocks(const PackArgs& a) {
   int64_t most = 0;
-  for (int i = 0; i < a.count; ++i) most = std::max(most, a.m[i].rows * (a.m[i].ld / 8));
+  for (int i = 0; i < a.count; ++i) most = std::max(most, a.m[i].rows * ((a.m[i].cols + 7) / 8));
   return (unsigned)std::min<int64_t>((most + 255) / 256, 4096);
 }
 
@@ -1011,7 +1011,7 @@ TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, un
   float db[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) db[e] = 0.0f;
-  // dz's rows are whole eights: zeros past the last column
+  // dz's rows hold whole eights: zeros past the last column
   const int pad = n < 8 && n > 0 && !GATED ? 8 : n;
   // Z: z's type; WHOLE: each lane has eight columns
   auto rows = [&](auto z_type, auto whole) {
@@ -1062,7 +1062,7 @@ TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, un
   }
   if constexpr (GATED) {
     // zeros past the last column of the second half
-    const int64_t rest = a.ld_dz - 2 * (int64_t)a.N;
+    const int64_t rest = -2 * (int64_t)a.N & 7;
     if (slab == 0 && threadIdx.x < rest)
       for (int64_t m = first; m < end; ++m) a.dz[m * a.ld_dz + 2 * (int64_t)a.N + threadIdx.x] = 0;
   } else {
