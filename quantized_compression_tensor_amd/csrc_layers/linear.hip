@@ -966,9 +966,9 @@ hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
 // Workgroup `group` of `groups` takes 512 columns (`slab`) of a range of rows,
 // a wave every fourth row of them, two at a time, a lane eight neighbouring
 // columns. Eight rows are a range; more where there would be over kActMaxGroups
-// ranges. Memory bounds it: gated 8192 x 5120, silu, 84 us (5.0 TB/s). With
+// ranges. Memory bounds it: gated 8192 x 5120, silu, 80 us (5.2 TB/s). With
 // gelu's slope the arithmetic takes about as long as the bytes, and the sums
-// of dbias add a tenth of them: 4096 x 4096 27 us (3.9 TB/s).
+// of dbias add a tenth of them: 4096 x 4096 26 us (4.2 TB/s).
 constexpr int kActRows = 8, kActMaxGroups = 1024;
 int act_back_groups(int64_t M) {
   const int64_t g = (M + kActRows - 1) / kActRows;
