@@ -351,8 +351,8 @@ int taco_layer_norm(taco_array x, int64_t rows, int64_t cols, taco_array weight,
  *   dx      = rstd * (g - sum(g) / cols - xhat * sum(g * xhat) / cols)
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
  * in float32, each rounded once. dx, dweight and dbias may each be absent (not
- * all); the workspace is needed for dweight or dbias. rows == 0 clears dweight
- * and dbias. */
+ * all, unless rows is 0); the workspace is needed for dweight or dbias.
+ * rows == 0 clears dweight and dbias. */
 int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t cols, taco_array weight,
                              const float* mean, const float* rstd, taco_array dx, taco_array dweight,
                              taco_array dbias, void* workspace, size_t ws_bytes, hipStream_t stream);
@@ -388,8 +388,8 @@ size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   dbias = sum over rows of dz
  * (the residual's gradient is dout itself). Where there is an activation, dz
  * is rounded to bf16 once, as an operand of the matrix cores; dbias sums it
- * unrounded. dx, dw and dbias may each be absent (not all). M == 0 clears dw
- * and dbias. */
+ * unrounded. dx, dw and dbias may each be absent (not all, unless M is 0).
+ * M == 0 clears dw and dbias. */
 int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
                          taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
                          size_t ws_bytes, hipStream_t stream);
@@ -408,7 +408,7 @@ size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
 /* Gradients of taco_gated_linear from dout [M, F] (bf16) and its preact:
  *   dz = [dout * z[:, F:] * act'(z[:, :F]), dout * act(z[:, :F])], rounded to
  *   bf16 once,  dx = dz W [M, K],  dw = dz^T x [2 F, K]
- * dx and dw may each be absent (not both). M == 0 clears dw. */
+ * dx and dw may each be absent (not both, unless M is 0). M == 0 clears dw. */
 int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
                                taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,
                                size_t ws_bytes, hipStream_t stream);

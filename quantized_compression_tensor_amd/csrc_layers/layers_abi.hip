@@ -303,7 +303,7 @@ int taco_layer_norm_backward(taco_array dy, taco_array x, int64_t rows, int64_t 
   if (st != TACO_OK) return st;
   if (rows > 0 && (mean == nullptr || rstd == nullptr)) return TACO_ERR_INVALID_ARG;
   const bool sums = dweight.data != nullptr || dbias.data != nullptr;
-  if (!sums && dx.data == nullptr) return TACO_ERR_INVALID_ARG;
+  if (rows > 0 && !sums && dx.data == nullptr) return TACO_ERR_INVALID_ARG;
   const Checked cws =
       check_workspace(workspace, ws_bytes, sums ? taco_layer_norm_backward_workspace_bytes(rows, cols) : 0);
   if (cws.status != TACO_OK) return cws.status;
@@ -370,11 +370,12 @@ int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t ac
   const Checked cdb = check_vector(dbias, N, kOptional);
   st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw, &cdb});
   if (st != TACO_OK) return st;
-  if (!dx.data && !dw.data && !dbias.data) return TACO_ERR_INVALID_ARG;
+  if (M > 0 && !dx.data && !dw.data && !dbias.data) return TACO_ERR_INVALID_ARG;
   const Backward b = {cd, cx, cw, cz, cdx, cdw, cdb, act, false, M, N, K};
   const Checked cws = check_workspace(workspace, ws_bytes, space_of(b, kSize));
   if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cdb, &cws})) return TACO_ERR_INVALID_ARG;
+  if (M == 0 && !dw.data && !dbias.data) return TACO_OK;
   return run(b, cws.m.p, stream);
 }
 
@@ -394,11 +395,12 @@ int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int3
   const Checked cdx = check_array(dx, M, K, kOptional), cdw = check_array(dw, 2 * F, K, kOptional);
   st = first_error({&cd, &cx, &cw, &cz, &cdx, &cdw});
   if (st != TACO_OK) return st;
-  if (!dx.data && !dw.data) return TACO_ERR_INVALID_ARG;
+  if (M > 0 && !dx.data && !dw.data) return TACO_ERR_INVALID_ARG;
   const Backward b = {cd, cx, cw, cz, cdx, cdw, {kAbsent, 0, TACO_OK, 0, 0}, act, true, M, F, K};
   const Checked cws = check_workspace(workspace, ws_bytes, space_of(b, kSize));
   if (cws.status != TACO_OK) return cws.status;
   if (any_overlap({&cd, &cx, &cw, &cz}, {&cdx, &cdw, &cws})) return TACO_ERR_INVALID_ARG;
+  if (M == 0 && !dw.data) return TACO_OK;
   return run(b, cws.m.p, stream);
 }
 
