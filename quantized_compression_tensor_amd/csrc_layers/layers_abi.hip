@@ -29,7 +29,7 @@ enum Need { kOptional, kRequired };
 enum Types { kAnyType, kBf16Only };
 
 Checked check_array(const taco_array& a, int64_t rows, int64_t cols, Need need, Types types = kAnyType) {
-  Checked c = {{a.data, a.stride, a.dtype}, 0, TACO_OK, 0, 0};
+  Checked c = {{a.data, rows > 1 ? a.stride : cols, a.dtype}, 0, TACO_OK, 0, 0};
   if (a.data == nullptr) {
     if (need == kRequired && rows > 0) c.status = TACO_ERR_INVALID_ARG;
     return c;
@@ -40,7 +40,6 @@ Checked check_array(const taco_array& a, int64_t rows, int64_t cols, Need need, 
   else if (rows > 1 && a.stride < cols) c.status = TACO_ERR_SHAPE;
   else if (rows > 1 && a.stride > kMaxElems / rows) c.status = TACO_ERR_INVALID_ARG;
   else if (reinterpret_cast<uintptr_t>(a.data) % (uintptr_t)elem_bytes(a.dtype) != 0) c.status = TACO_ERR_ALIGN;
-  if (rows <= 1) c.m.ld = cols;
   if (c.status == TACO_OK && rows > 0) {
     c.bytes = ((rows - 1) * c.m.ld + cols) * elem_bytes(a.dtype);
     c.row = cols * elem_bytes(a.dtype);

@@ -22,6 +22,19 @@ def test_backward_of_no_rows_for_the_inputs_gradient_alone(act):
                                         None) == T.TACO_OK
 
 
+@pytest.mark.parametrize("rows", [0, 1])
+def test_the_stride_of_fewer_than_two_rows_is_not_looked_at(rows):
+    """A slice of a very wide tensor keeps its stride when it has no rows. (One
+    row of a refused element type: the next check after the stride's.)"""
+    wide = T.TACO_LINEAR_MAX_STRIDE + 8
+    x = T.taco_array(None if rows == 0 else 1 << 30, wide, B, 0)
+    out = T.taco_array(None if rows == 0 else 1 << 31, 64, B if rows == 0 else 7, 0)
+    w = T.taco_array(1 << 32, 64, B, 0)
+    want = T.TACO_OK if rows == 0 else T.TACO_ERR_FORMAT
+    assert T.lib().taco_linear(x, w, NONE, 0, NONE, out, NONE, rows, 64, 64, None, 0, None) == want
+    assert T.lib().taco_gated_linear(x, w, 0, out, NONE, rows, 32, 64, None, 0, None) == want
+
+
 @pytest.mark.gpu
 def test_empty_tensors_for_the_inputs_gradient_alone():
     import torch
