@@ -101,10 +101,12 @@ int check_norm_sizes(int64_t rows, int64_t cols) {
   return TACO_OK;
 }
 
-// Sizes of a projection with `n` output columns and `wide` weight rows.
-int check_linear_sizes(int64_t m, int64_t n, int64_t wide, int64_t k) {
+// Sizes of a projection with `n` output columns, of as many weight rows or
+// (gated) twice as many.
+int check_linear_sizes(int64_t m, int64_t n, int64_t k, bool gated) {
   if (m < 0 || n <= 0 || k <= 0) return TACO_ERR_INVALID_ARG;
-  if (n > TACO_LINEAR_MAX_DIM || wide > TACO_LINEAR_MAX_DIM || k > TACO_LINEAR_MAX_DIM) return TACO_ERR_SHAPE;
+  if (n > TACO_LINEAR_MAX_DIM / (gated ? 2 : 1) || k > TACO_LINEAR_MAX_DIM) return TACO_ERR_SHAPE;
+  const int64_t wide = gated ? 2 * n : n;
   if (m > (int64_t(1) << 30) || wide * k > kMaxElems || m > kMaxElems / wide || m > kMaxElems / k)
     return TACO_ERR_INVALID_ARG;
   return TACO_OK;
@@ -251,13 +253,13 @@ int run(const Call& c, void* ws, hipStream_t stream) {
 }
 
 size_t forward_bytes(bool gated, int64_t m, int64_t n, int64_t k) {
-  if (check_linear_sizes(m, n, gated ? 2 * n : n, k) != TACO_OK) return 0;
+  if (check_linear_sizes(m, n, k, gated) != TACO_OK) return 0;
   Forward f = {};
   f.gated = gated; f.m = m; f.n = n; f.k = k;
   return space_of(f, kSizeOfAny);
 }
 size_t backward_bytes(bool gated, int64_t m, int64_t n, int64_t k) {
-  if (check_linear_sizes(m, n, gated ? 2 * n : n, k) != TACO_OK) return 0;
+  if (check_linear_sizes(m, n, k, gated) != TACO_OK) return 0;
   Backward b = {};
   b.gated = gated; b.m = m; b.n = n; b.k = k;
   return space_of(b, kSizeOfAny);
@@ -319,7 +321,7 @@ size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) { return for
 int taco_linear(taco_array x, taco_array w, taco_array bias, int32_t act, taco_array residual, taco_array out,
                 taco_array preact, int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
                 hipStream_t stream) {
-  int st = check_linear_sizes(M, N, N, K);
+  int st = check_linear_sizes(M, N, K, false);
   if (st != TACO_OK) return st;
   st = check_act(act);
   if (st != TACO_OK) return st;
@@ -339,7 +341,7 @@ size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K) { retu
 
 int taco_gated_linear(taco_array x, taco_array w, int32_t act, taco_array out, taco_array preact, int64_t M,
                       int64_t F, int64_t K, void* workspace, size_t ws_bytes, hipStream_t stream) {
-  int st = check_linear_sizes(M, F, 2 * F, K);
+  int st = check_linear_sizes(M, F, K, true);
   if (st != TACO_OK) return st;
   st = check_act(act);
   if (st != TACO_OK) return st;
@@ -359,7 +361,7 @@ size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) { r
 int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
                          taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
                          size_t ws_bytes, hipStream_t stream) {
-  int st = check_linear_sizes(M, N, N, K);
+  int st = check_linear_sizes(M, N, K, false);
   if (st != TACO_OK) return st;
   st = check_act(act);
   if (st != TACO_OK) return st;
@@ -385,7 +387,7 @@ size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t 
 int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
                                taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,
                                size_t ws_bytes, hipStream_t stream) {
-  int st = check_linear_sizes(M, F, 2 * F, K);
+  int st = check_linear_sizes(M, F, K, true);
   if (st != TACO_OK) return st;
   st = check_act(act);
   if (st != TACO_OK) return st;
