@@ -316,10 +316,10 @@ int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, cons
  * is not looked at.
  * Errors, for every function here: TACO_ERR_FORMAT for an element type or an
  * activation that it does not take; TACO_ERR_SHAPE for a stride below the
- * number of columns or a size beyond what the function says;
- * TACO_ERR_INVALID_ARG for sizes below zero, tensors above 2^35 elements, a
- * missing array or an output that overlaps an input or another output;
- * TACO_ERR_ALIGN; TACO_ERR_WORKSPACE for a workspace that is missing, smaller
+ * number of columns (of two rows or more) or a size beyond what the function
+ * says; TACO_ERR_INVALID_ARG for sizes below zero, no columns, tensors above
+ * 2^35 elements, a missing array or an output that overlaps an input or another
+ * output; TACO_ERR_ALIGN; TACO_ERR_WORKSPACE for a workspace that is missing, smaller
  * than the call needs or not 16-byte aligned. The function's *_workspace_bytes
  * is enough for arrays of any alignment and all outputs. Workspaces are
  * scratch: nothing is kept in them between calls, they need no clearing, and
@@ -339,7 +339,8 @@ typedef struct taco_array {
 
 /* y = (x - mean) * rstd * weight + bias for each row of x [rows, cols], with
  * mean = sum(x) / cols and rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps) in
- * float32, y rounded once. cols at most TACO_NORM_MAX_COLS.
+ * float32, y rounded once. cols at most TACO_NORM_MAX_COLS (TACO_ERR_SHAPE),
+ * rows below 2^31 (TACO_ERR_INVALID_ARG); rows may be 0 (nothing enqueued).
  *   weight, bias   [cols], each may be absent (1 and 0)
  *   mean, rstd     float32 [rows] for the backward pass, nullable */
 #define TACO_NORM_MAX_COLS 16384
@@ -369,8 +370,9 @@ size_t taco_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *   z = x W^T + bias,  out = act(z) + residual
  * x bf16 [M, K], w bf16 [N, K] (a linear layer's weight); products summed in
  * float32 on the matrix cores, the epilogue in float32, each output rounded
- * once. N, K at most TACO_LINEAR_MAX_DIM, M below 2^31 and strides of x and w
- * at most TACO_LINEAR_MAX_STRIDE.
+ * once. N, K at most TACO_LINEAR_MAX_DIM (TACO_ERR_SHAPE), M at most 2^30
+ * (TACO_ERR_INVALID_ARG) and strides of x, w and dout at most
+ * TACO_LINEAR_MAX_STRIDE.
  *   bias      [N], may be absent
  *   residual  [M, N], may be absent
  *   preact    [M, N] receives z for the backward pass, may be absent
