@@ -29,7 +29,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // Phi = erfc(x) / 2 with x = |z| / sqrt(2), and erfc(x) = t Q(t) exp(-x^2),
 // t = 1 / (1 + p x): Q is a polynomial of degree 8 fitted to
 // exp(x^2) erfc(x) / t over x in [0, 9.5] by iteratively reweighted least
-// squares, relative error below 1.2e-8; for z > 0 Phi = 1 - that. In float32
+// squares, relative error below 1.3e-8; for z > 0 Phi = 1 - that. In float32
 // Phi is within 2.1e-7, and within 2e-6 of its value for |z| < 6 (the rounding
 // of exp's argument). About 20 instructions; erff takes two to three times as
 // many, which showed in the epilogue and bound the backward pass.
