@@ -95,8 +95,10 @@ TACO_DEV void load8(const void* base, int dt, int64_t at, int n, float* f) {
 }
 TACO_DEV void load8(const void* base, int dt, int64_t at, float* f) { load8(base, dt, at, 8, f); }
 // NT: streamed past the caches, as a tensor that another kernel reads should
-// be where whole 128-byte lines are written (forward norm 8192 x 5120 45.5 us
-// cached, 43.1 us streamed; 4096 x 4096 x 512 product 24.0 and 21.3).
+// be (forward norm 8192 x 5120 46.0 us cached, 39.3 streamed). A norm's waves
+// write neighbouring columns of a row at about the same time, so that holds
+// for rows that do not start on a line too (rows 5123 apart 46.0 and 39.9, 8192
+// x 5121 55.0 and 44.0, 32768 x 1001 39.5 and 31.6; float32 rows about equal).
 template <bool NT>
 TACO_DEV void store16(void* p, u32x4 v) {
   typedef unsigned any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));

@@ -122,6 +122,22 @@ TACO_DEV void load_residual(const Epilogue& e, int64_t m, int n, int count, floa
   if (e.residual.p && count > 0) load8(e.residual.p, e.residual.dt, m * e.residual.ld + n, count, r);
 }
 
+// Whether an output is streamed past the caches: where a store instruction
+// writes whole 128-byte lines, so bf16 whose rows start on one (4096 x 4096 x
+// 512 23.2 us cached, 21.0 streamed). Otherwise the caches join the parts of a
+// line, which two tiles write far apart in time (rows 4099 apart 22.2 us
+// cached, 28.2 streamed; 8192 x 8192 x 64 with rows 8195 apart 45.2 and 62.4)
+// or, in float32, two instructions, each half of a lane's eight (4096 x 4096 x
+// 512 27.2 and 41.3). One loss: two outputs and a residual of rows 4099 apart,
+// 78.6 and 75.3. (Few rows: no difference.)
+TACO_DEV bool streamed(const Mat& t) {
+  return t.dt == kBF16 && reinterpret_cast<uintptr_t>(t.p) % 128 == 0 && t.ld % 64 == 0;
+}
+TACO_DEV void store_out(const Mat& t, int64_t at, int count, const float* z) {
+  if (streamed(t)) store8<true>(t.p, kBF16, at, count, z);
+  else store8<false>(t.p, t.dt, at, count, z);
+}
+
 // Eight neighbouring columns n ... of row m, of which `count` exist, with
 // their bias b and residual r.
 TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z, const float* b, const float* r) {
@@ -129,13 +145,13 @@ TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z, c
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += b[i];
   }
-  if (e.preact.p) store8(e.preact.p, e.preact.dt, m * e.preact.ld + n, count, z);
+  if (e.preact.p) store_out(e.preact, m * e.preact.ld + n, count, z);
   act_values(z, e.act);
   if (e.residual.p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += r[i];
   }
-  store8(e.out.p, e.out.dt, m * e.out.ld + n, count, z);
+  store_out(e.out, m * e.out.ld + n, count, z);
 }
 TACO_DEV void finish(const Epilogue& e, int64_t m, int n, int count, float* z) {
   float b[8], r[8];
@@ -173,15 +189,19 @@ TACO_DEV void load_rows(const Mat& t, int64_t m, int apart, int n, float (&z)[Q]
     for (int q = 0; q < Q; ++q) load8(t.p, kF32, at + q * apart * t.ld, z[q]);
   }
 }
-template <bool NT, int Q>
-TACO_DEV void store_rows(const Mat& t, int64_t m, int apart, int n, const float (&z)[Q][8]) {
+// `stream`: that of streamed(), or false.
+template <int Q>
+TACO_DEV void store_rows(const Mat& t, int64_t m, int apart, int n, const float (&z)[Q][8], bool stream) {
   const int64_t at = m * t.ld + n;
-  if (t.dt == kBF16) {
+  if (stream) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) store8<NT>(t.p, kBF16, at + q * apart * t.ld, 8, z[q]);
+    for (int q = 0; q < Q; ++q) store8<true>(t.p, kBF16, at + q * apart * t.ld, 8, z[q]);
+  } else if (t.dt == kBF16) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) store8<false>(t.p, kBF16, at + q * apart * t.ld, 8, z[q]);
   } else {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) store8<NT>(t.p, kF32, at + q * apart * t.ld, 8, z[q]);
+    for (int q = 0; q < Q; ++q) store8<false>(t.p, kF32, at + q * apart * t.ld, 8, z[q]);
   }
 }
 template <int Q>
@@ -209,7 +229,7 @@ TACO_DEV void finish_rows(const Epilogue& e, int64_t m, int apart, int n, float 
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[q][i] += b[i];
   }
-  if (e.preact.p) store_rows<true>(e.preact, m, apart, n, z);
+  if (e.preact.p) store_rows(e.preact, m, apart, n, z, streamed(e.preact));
   act_rows(z, e.act);
   if (e.residual.p) {
 #pragma unroll
@@ -217,21 +237,21 @@ TACO_DEV void finish_rows(const Epilogue& e, int64_t m, int apart, int n, float 
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[q][i] += r[q][i];
   }
-  store_rows<true>(e.out, m, apart, n, z);
+  store_rows(e.out, m, apart, n, z, streamed(e.out));
 }
 template <int Q>
 TACO_DEV void finish_gated_rows(const Epilogue& e, int width, int64_t m, int apart, int n, float (&z)[Q][8],
                                 const float (&u)[Q][8]) {
   if (e.preact.p) {
-    store_rows<false>(e.preact, m, apart, n, z);
-    store_rows<false>(e.preact, m, apart, width + n, u);
+    store_rows(e.preact, m, apart, n, z, false);
+    store_rows(e.preact, m, apart, width + n, u, false);
   }
   act_rows(z, e.act);
 #pragma unroll
   for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[q][i] *= u[q][i];
-  store_rows<false>(e.out, m, apart, n, z);
+  store_rows(e.out, m, apart, n, z, false);
 }
 
 // ------------------------------------------------------------------ tiles --
@@ -587,7 +607,7 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
       } else if constexpr (GATED) {
         finish_gated_rows(a.e, a.N, m, kPass, n, z, u);
       } else if constexpr (kPlain) {
-        store_rows<true>(a.e.out, m, kPass, n, z);
+        store_rows(a.e.out, m, kPass, n, z, streamed(a.e.out));
       } else {
         finish_rows(a.e, m, kPass, n, z, bias, r);
       }
@@ -604,7 +624,7 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
         if constexpr (GATED) {
           finish_gated(a.e, a.N, m + q * kPass, n, count, z, u);
         } else if constexpr (kPlain) {
-          store8(a.e.out.p, a.e.out.dt, (m + q * kPass) * a.e.out.ld + n, count, z);
+          store_out(a.e.out, (m + q * kPass) * a.e.out.ld + n, count, z);
         } else {
           load_residual(a.e, m + q * kPass, n, count, r);
           finish(a.e, m + q * kPass, n, count, z, bias, r);
