@@ -1,5 +1,6 @@
-// Host helpers shared by the files that implement the C ABI: argument checks
-// and the status of a launch.
+// Host helpers of the layers' part of the C ABI: argument checks and the status
+// of a launch. (The codecs' part, csrc/taco_abi.hip, has its own; both take
+// tensors of up to 2^35 elements.)
 #pragma once
 
 #include <hip/hip_runtime.h>
