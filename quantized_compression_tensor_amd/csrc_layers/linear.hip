@@ -802,7 +802,7 @@ struct Plan {
   int64_t part;
 };
 
-constexpr int64_t kCus = 256;
+constexpr int kCus = 256;   // of an MI355X; not asked of the device, so that sizes alone decide a workspace
 static int64_t tiles_of(int64_t M, int64_t N, int bm, int cols) { return ((M + bm - 1) / bm) * ((N + cols - 1) / cols); }
 
 // `other`: steps of the tiles of another product that run at the same time.
@@ -902,7 +902,7 @@ static void launch_few_rows(GemmArgs a, hipStream_t s) {
   // as many columns for a workgroup as give each CU the same number of them
   // (one row, 5120 x 20480: 41.9 us with 512 workgroups of 10 columns, 52.6
   // with 320 of 16); a few workgroups more than that run beside the others
-  const int most = a.gated ? 8 : 16, cus = device_cu_count();
+  const int most = a.gated ? 8 : 16, cus = kCus;
   const int groups = (a.N + most - 1) / most, rounds = std::max(1, (groups - cus / 8 + cus - 1) / cus);
   a.cols = std::min(most, (a.N + rounds * cus - 1) / (rounds * cus));
   const dim3 grid((unsigned)((a.N + a.cols - 1) / a.cols)), block(kFewWaves * kWave);
