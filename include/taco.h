@@ -389,8 +389,9 @@ size_t taco_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
  *   dz = dout * act'(preact),  dx = dz W [M, K],  dw = dz^T x [N, K],
  *   dbias = sum over rows of dz
  * (the residual's gradient is dout itself). Where there is an activation, dz
- * is rounded to bf16 once, as an operand of the matrix cores; dbias sums it
- * unrounded. dx, dw and dbias may each be absent (not all, unless M is 0).
+ * is rounded to bf16 once, as an operand of the matrix cores, and terms of dx
+ * and dw are off by up to 2^-8 for it, also where these are float32; dbias sums
+ * dz unrounded. dx, dw and dbias may each be absent (not all, unless M is 0).
  * M == 0 clears dw and dbias. */
 int taco_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact, taco_array dx,
                          taco_array dw, taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -409,7 +410,8 @@ size_t taco_gated_linear_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /* Gradients of taco_gated_linear from dout [M, F] (bf16) and its preact:
  *   dz = [dout * z[:, F:] * act'(z[:, :F]), dout * act(z[:, :F])], rounded to
- *   bf16 once,  dx = dz W [M, K],  dw = dz^T x [2 F, K]
+ *   bf16 once (as in taco_linear_backward),  dx = dz W [M, K],
+ *   dw = dz^T x [2 F, K]
  * dx and dw may each be absent (not both, unless M is 0). M == 0 clears dw. */
 int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
                                taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,

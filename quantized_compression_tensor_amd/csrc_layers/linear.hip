@@ -394,9 +394,10 @@ struct Loader : Chunks<BY_K, R, NT, GATED> {
   }
 };
 
-// Output tile of this workgroup: each XCD walks one contiguous range of tiles,
-// and inside it groups of kGroupM tile rows column by column, so the
-// workgroups resident on an XCD share rows of a and of b through its L2.
+// Output tile of this workgroup: each XCD walks one contiguous range of tiles
+// (xcd_ordered_block() for any index of any count), and inside it groups of
+// kGroupM tile rows column by column, so the workgroups resident on an XCD share
+// rows of a and of b through its L2.
 TACO_DEV unsigned xcd_ordered(unsigned b, unsigned G) {
   const unsigned x = b % kXcds, l = b / kXcds, q = G / kXcds, r = G % kXcds;
   return x * q + (x < r ? x : r) + l;
@@ -433,12 +434,17 @@ TACO_DEV void hand_over() {
 // or two steps' time. The 16 x 16 x 32 products were faster than 32 x 32 x 16
 // (8192^3: 750 against 815 us) although they leave more gaps: this size is
 // bound by power, and they move half as many sums through the registers.
-// Measured, random values: 8192^3 forward 737 us (1490 TFLOP/s), dx 763, dw
-// 798; 4096^3 96 (1425), 100 and 104. The matrix cores are busy 0.73 of the
-// time at 8192^3, at 1.6 GHz, and 0.67 and 0.62 in the gradients, at 2.1.
-// A small tile alone on its CU takes 0.55 us a step, two together 1.1 for both:
-// the LDS is what bounds them (96 KB a step), and five stages of a and four of
-// b instead of three and two, for one of them on a CU, were no faster.
+// Measured, random values, bf16 outputs, on one card 8192^3 forward 807 us
+// (1360 TFLOP/s), dx 833, dw 879, where the library's product took 725, and
+// 4096^3 104 (1320), 108 and 114 (112); on a faster one 737, 763, 798 and 96,
+// 100, 104. In profiled launches (8192^3 900 us, 4096^3 108 and 114) the matrix
+// cores are busy 0.73 of the time at 1.67 GHz, the gradients 0.68 and 0.62 at
+// 2.1; the LDS serves reads in 0.25 to 0.29 of the cycles.
+// A small tile takes 0.55 us a step on a CU of its own, and two together 1.1
+// for both. The counters show no unit that it fills: matrix cores 0.42 to 0.45
+// at 2.4 GHz, LDS 0.22 to 0.26, and L2 gives 14 to 19 TB/s where a loop of reads
+// gets 31 to 33. Five stages of a and four of b instead of three and two, for one
+// tile on a CU, were no faster, so a longer reach ahead is not what is missing.
 // `block`: of the product's a.whole + a.rest * a.parts.
 template <class TL, bool AK, bool BK_, bool GATED>
 TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
@@ -701,9 +707,12 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
 // a wave together. The waves' sums are joined in LDS. Rows may start anywhere.
 // One row, 8192 x 8192 weights: 27.6 us, 4.9 TB/s (eight waves with eight units
 // each 31.8 us); 4096 x 4096: 7.6 us. With 24 rows the reads of x, which every
-// workgroup makes, are as many as those of the weights: 24 x 5120 into 2 x 1728
-// gated 13.8 us (2.6 TB/s). Loading further ahead was slower everywhere (that
-// one 19.7 us and more), and x's lanes without a row left out no faster.
+// workgroup makes, are more than those of the weights: 24 x 5120 into 2 x 1728
+// gated 13.8 us (2.6 TB/s). Counters of that one: 37 MB from memory, 111 MB out
+// of L2 (7 TB/s), neither near its rate, and waves that wait 0.96 of their time,
+// for three rounds of loads one after the other. Loading further ahead was
+// slower everywhere (that one 19.7 us and more), and x's lanes without a row
+// left out no faster.
 constexpr int kFewRows = 32, kFewWaves = 16;
 
 template <int TM, bool GATED>
