@@ -329,11 +329,12 @@ int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, cons
  * the columns) that they enter. The launch cap does not apply. */
 #define TACO_F32 0
 #define TACO_BF16 1
+#define TACO_I8 2     /* codes, where a function says so */
 
 typedef struct taco_array {
   void* data;       /* device memory; inputs are never written */
   int64_t stride;   /* elements from one row to the next, at least the columns */
-  int32_t dtype;    /* TACO_F32 or TACO_BF16 */
+  int32_t dtype;    /* TACO_F32 or TACO_BF16 (TACO_I8: codes) */
   int32_t reserved; /* must be 0 */
 } taco_array;
 
@@ -417,6 +418,80 @@ int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int3
                                taco_array dx, taco_array dw, int64_t M, int64_t F, int64_t K, void* workspace,
                                size_t ws_bytes, hipStream_t stream);
 size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
+
+/* ---- projections in 8-bit integers -----------------------------------------
+ * Rows to symmetric codes of 8 bits with one scale each, as INT8_SYM makes them
+ * for its blocks: with A = max |x| of the row,
+ *   scale = A / 127,  q = x * (127 / A) to the nearest, ties to even
+ * in float32, each step rounded once (codes lie in [-127, 127]). A below
+ * 2^-100: codes 0 and scale 0. A row with an infinity or NaN: codes 0 and that
+ * as its scale, so products with it are NaN. Serves tokens and, row by row of a
+ * linear layer's weight, output channels.
+ *   x      [rows, cols], float32 or bf16
+ *   q      [rows, cols], TACO_I8
+ *   scale  float32 [rows]
+ * cols at most TACO_LINEAR_MAX_DIM (TACO_ERR_SHAPE); rows may be 0. */
+int taco_quantize_rows(taco_array x, int64_t rows, int64_t cols, taco_array q, float* scale, hipStream_t stream);
+
+/* taco_linear's forward pass with both operands in 8 bits:
+ *   z[m, n] = (sum over k of x[m, k] w[n, k]) * x_scale[m] * w_scale[n] + bias[n],
+ *   out = act(z) + residual
+ * x TACO_I8 [M, K], w TACO_I8 [N, K], any codes from -128 to 127. Sums of codes
+ * are exact (K at most TACO_INT8_MAX_K, else TACO_ERR_SHAPE); from there on in
+ * float32 as in taco_linear, whose limits and arguments these are otherwise.
+ * x and w whose rows start on 16 bytes and hold a multiple of 16 codes are read
+ * fastest.
+ *   x_scale   float32 [M], w_scale float32 [N] (gated: [2 F]) */
+#define TACO_INT8_MAX_K 131071
+int taco_linear_int8(taco_array x, const float* x_scale, taco_array w, const float* w_scale, taco_array bias, int32_t act,
+                     taco_array residual, taco_array out, int64_t M, int64_t N, int64_t K, void* workspace,
+                     size_t ws_bytes, hipStream_t stream);
+size_t taco_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* taco_gated_linear in the same way: w TACO_I8 [2 F, K]. */
+int taco_gated_linear_int8(taco_array x, const float* x_scale, taco_array w, const float* w_scale, int32_t act,
+                           taco_array out, int64_t M, int64_t F, int64_t K, void* workspace, size_t ws_bytes,
+                           hipStream_t stream);
+size_t taco_gated_linear_int8_workspace_bytes(int64_t M, int64_t F, int64_t K);
+
+/* ---- projections by group (experts) ----------------------------------------
+ * The projections above where groups of rows have weights of their own: rows
+ * offsets[g] ... offsets[g + 1] - 1 of x, out and their gradients belong to
+ * group g (tokens sorted by expert). `offsets` is device int32 [groups + 1],
+ * not decreasing, in [0, M]; the host does not read it, so calls need no
+ * synchronization and can be captured. Groups may be empty. Rows before
+ * offsets[0] and from offsets[groups] on belong to none: no output is written
+ * there and nothing there is looked at except by copies in the workspace. An
+ * offset outside of [0, M] counts as its nearer end; offsets that decrease give
+ * unspecified values, but no access outside the arrays.
+ * Weights, their gradients and biases lie group by group: w [groups * N, K]
+ * with the rows of group g from g * N on, bias and dbias [groups, N]. Otherwise
+ * the arguments, types and limits are those of the function without groups;
+ * groups is at most TACO_MAX_GROUPS (TACO_ERR_SHAPE), w at most 2^35 elements. */
+#define TACO_MAX_GROUPS 1024
+int taco_grouped_linear(taco_array x, taco_array w, taco_array bias, int32_t act, const int32_t* offsets, int32_t groups,
+                        taco_array out, taco_array preact, int64_t M, int64_t N, int64_t K, void* workspace,
+                        size_t ws_bytes, hipStream_t stream);
+size_t taco_grouped_linear_workspace_bytes(int32_t groups, int64_t M, int64_t N, int64_t K);
+
+/* Its gradients, each where its array is given: dx of the groups' rows, dw
+ * [groups * N, K] and dbias [groups, N] of every group (zeros for one without
+ * rows). dz is rounded to bf16 as in taco_linear_backward. */
+int taco_grouped_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
+                                 const int32_t* offsets, int32_t groups, taco_array dx, taco_array dw,
+                                 taco_array dbias, int64_t M, int64_t N, int64_t K, void* workspace, size_t ws_bytes,
+                                 hipStream_t stream);
+size_t taco_grouped_linear_backward_workspace_bytes(int32_t groups, int64_t M, int64_t N, int64_t K);
+
+/* Gated: w [groups * 2 F, K], of each group the gate's rows first. */
+int taco_grouped_gated_linear(taco_array x, taco_array w, int32_t act, const int32_t* offsets, int32_t groups,
+                              taco_array out, taco_array preact, int64_t M, int64_t F, int64_t K, void* workspace,
+                              size_t ws_bytes, hipStream_t stream);
+size_t taco_grouped_gated_linear_workspace_bytes(int32_t groups, int64_t M, int64_t F, int64_t K);
+int taco_grouped_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int32_t act, taco_array preact,
+                                       const int32_t* offsets, int32_t groups, taco_array dx, taco_array dw, int64_t M,
+                                       int64_t F, int64_t K, void* workspace, size_t ws_bytes, hipStream_t stream);
+size_t taco_grouped_gated_linear_backward_workspace_bytes(int32_t groups, int64_t M, int64_t F, int64_t K);
 
 /* Cap on the workgroups of every later launch made by the calling host
  * thread (0 = no cap, the default): lets the codec share the GPU with a

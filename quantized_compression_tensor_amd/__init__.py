@@ -36,6 +36,7 @@ TACO_WORKSPACE_BYTES = 32768
 
 TACO_F32 = 0
 TACO_BF16 = 1
+TACO_I8 = 2
 TACO_NORM_MAX_COLS = 16384
 TACO_ACT_NONE = 0
 TACO_ACT_GELU = 1
@@ -43,6 +44,8 @@ TACO_ACT_SILU = 2
 TACO_ACT_RELU = 3
 TACO_LINEAR_MAX_DIM = 1 << 20
 TACO_LINEAR_MAX_STRIDE = 1 << 21
+TACO_INT8_MAX_K = 131071
+TACO_MAX_GROUPS = 1024
 
 # Entry points declared in include/taco.h (checked by the ABI tests).
 EXPORTS = (
@@ -54,6 +57,12 @@ EXPORTS = (
     "taco_layer_norm_backward_workspace_bytes", "taco_linear", "taco_linear_workspace_bytes", "taco_linear_backward",
     "taco_linear_backward_workspace_bytes", "taco_gated_linear", "taco_gated_linear_workspace_bytes",
     "taco_gated_linear_backward", "taco_gated_linear_backward_workspace_bytes",
+    "taco_quantize_rows", "taco_linear_int8", "taco_linear_int8_workspace_bytes", "taco_gated_linear_int8",
+    "taco_gated_linear_int8_workspace_bytes",
+    "taco_grouped_linear", "taco_grouped_linear_workspace_bytes", "taco_grouped_linear_backward",
+    "taco_grouped_linear_backward_workspace_bytes", "taco_grouped_gated_linear",
+    "taco_grouped_gated_linear_workspace_bytes", "taco_grouped_gated_linear_backward",
+    "taco_grouped_gated_linear_backward_workspace_bytes",
 )
 
 
@@ -126,7 +135,17 @@ def _load():
         "taco_linear_backward": (ctypes.c_int, [A, A, A, I32, A, A, A, A, I64, I64, I64, P, SZ, P]),
         "taco_gated_linear": (ctypes.c_int, [A, A, I32, A, A, I64, I64, I64, P, SZ, P]),
         "taco_gated_linear_backward": (ctypes.c_int, [A, A, A, I32, A, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_quantize_rows": (ctypes.c_int, [A, I64, I64, A, P, P]),
+        "taco_linear_int8": (ctypes.c_int, [A, P, A, P, A, I32, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_gated_linear_int8": (ctypes.c_int, [A, P, A, P, I32, A, I64, I64, I64, P, SZ, P]),
+        "taco_grouped_linear": (ctypes.c_int, [A, A, A, I32, P, I32, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_grouped_linear_backward": (ctypes.c_int, [A, A, A, I32, A, P, I32, A, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_grouped_gated_linear": (ctypes.c_int, [A, A, I32, P, I32, A, A, I64, I64, I64, P, SZ, P]),
+        "taco_grouped_gated_linear_backward": (ctypes.c_int, [A, A, A, I32, A, P, I32, A, A, I64, I64, I64, P, SZ, P]),
         **{f"taco_{n}_workspace_bytes": (SZ, [I64, I64, I64])
+           for n in ("linear", "linear_backward", "gated_linear", "gated_linear_backward", "linear_int8",
+                     "gated_linear_int8")},
+        **{f"taco_grouped_{n}_workspace_bytes": (SZ, [I32, I64, I64, I64])
            for n in ("linear", "linear_backward", "gated_linear", "gated_linear_backward")},
     }
     for name, (res, args) in sig.items():
@@ -461,6 +480,151 @@ def taco_gated_linear_backward(dout, x, w, act=TACO_ACT_SILU, preact=None, dx=No
         _matrix(dout, M, F, "dout"), _matrix(x, M, K, "x"), _matrix(w, 2 * F, K, "w"), act,
         _matrix(preact, M, 2 * F, "preact"), _matrix(dx, M, K, "dx"), _matrix(dw, 2 * F, K, "dw"), M, F, K,
         *_workspace(workspace), _stream(stream)), "taco_gated_linear_backward")
+
+
+# ------------------------------------------------ projections in 8 bits --
+
+def _codes(t, rows, cols, what):
+    """An int8 matrix."""
+    if not t.is_cuda:
+        _on_gpu(t, what)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
+    import torch
+    if t.dtype != torch.int8:
+        raise TypeError(f"{what}: {t.dtype} is not int8")
+    return taco_array(t.data_ptr(), stride, TACO_I8, 0)
+
+
+def taco_quantize_rows(x, q, scale, stream=None):
+    """q (int8 [rows, cols]) and scale (float32 [rows]) of the rows of x: scale =
+    max |x| / 127, q = x * (127 / max |x|) to the nearest."""
+    rows, cols = x.shape
+    return _check(_lib.taco_quantize_rows(_matrix(x, rows, cols, "x"), rows, cols, _codes(q, rows, cols, "q"),
+                                          _floats(scale, rows, "scale"), _stream(stream)), "taco_quantize_rows")
+
+
+def taco_linear_int8_workspace_bytes(M, N, K):
+    return _lib.taco_linear_int8_workspace_bytes(M, N, K)
+
+
+def taco_linear_int8(x, x_scale, w, w_scale, out, bias=None, act=TACO_ACT_NONE, residual=None, workspace=None,
+                     stream=None):
+    """out = act((x w^T) x_scale w_scale + bias) + residual; x int8 [M, K], w int8
+    [N, K], x_scale float32 [M], w_scale float32 [N]."""
+    (M, K), N = x.shape, w.shape[0]
+    return _check(_lib.taco_linear_int8(
+        _codes(x, M, K, "x"), _floats(x_scale, M, "x_scale"), _codes(w, N, K, "w"), _floats(w_scale, N, "w_scale"),
+        _vector(bias, N, "bias"), act, _matrix(residual, M, N, "residual"), _matrix(out, M, N, "out"), M, N, K,
+        *_workspace(workspace), _stream(stream)), "taco_linear_int8")
+
+
+def taco_gated_linear_int8_workspace_bytes(M, F, K):
+    return _lib.taco_gated_linear_int8_workspace_bytes(M, F, K)
+
+
+def taco_gated_linear_int8(x, x_scale, w, w_scale, out, act=TACO_ACT_SILU, workspace=None, stream=None):
+    """out = act(z[:, :F]) * z[:, F:] with z = (x w^T) x_scale w_scale; w int8
+    [2 F, K], the gate's rows first, w_scale float32 [2 F]."""
+    (M, K), F = x.shape, w.shape[0] // 2
+    return _check(_lib.taco_gated_linear_int8(
+        _codes(x, M, K, "x"), _floats(x_scale, M, "x_scale"), _codes(w, 2 * F, K, "w"),
+        _floats(w_scale, 2 * F, "w_scale"), act, _matrix(out, M, F, "out"), M, F, K, *_workspace(workspace),
+        _stream(stream)), "taco_gated_linear_int8")
+
+
+# ------------------------------------------------- projections by group --
+# Weights are [groups, rows, K] tensors, a group's matrix right after another's
+# (any row stride); offsets int32 [groups + 1] on the GPU.
+
+def _groups_of(t, groups, rows, cols, what):
+    """A [groups, rows, cols] tensor as the matrix [groups * rows, cols]."""
+    if t is None:
+        return _ABSENT
+    if not t.is_cuda:
+        _on_gpu(t, what)
+    if t.shape != (groups, rows, cols):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(groups, rows, cols)}")
+    apart, stride, inner = t.stride()
+    if rows == 1:
+        stride = apart
+    if (inner != 1 and cols > 1) or (groups > 1 and apart != rows * stride):
+        raise ValueError(f"{what}: rows must be contiguous and evenly spaced over all groups (strides {t.stride()})")
+    dt = _DTYPES.get(t.dtype)
+    return taco_array(t.data_ptr(), stride, _dtype(t, what) if dt is None else dt, 0)
+
+
+def _offsets(t, groups):
+    import torch
+    if not t.is_cuda:
+        _on_gpu(t, "offsets")
+    if t.shape != (groups + 1,) or not t.is_contiguous():
+        raise ValueError(f"offsets: expected {groups + 1} contiguous values, got shape {tuple(t.shape)}")
+    if t.dtype != torch.int32:
+        raise TypeError(f"offsets: {t.dtype} is not int32")
+    return t.data_ptr()
+
+
+def taco_grouped_linear_workspace_bytes(groups, M, N, K):
+    return _lib.taco_grouped_linear_workspace_bytes(groups, M, N, K)
+
+
+def taco_grouped_linear(x, w, offsets, out, bias=None, act=TACO_ACT_NONE, preact=None, workspace=None, stream=None):
+    """out = act(x w[g]^T + bias[g]) for the rows offsets[g] ... offsets[g + 1] of
+    x [M, K]; w bf16 [groups, N, K], bias [groups, N]; preact receives what act is
+    taken of. Rows of no group stay as they are."""
+    (M, K), (G, N, _) = x.shape, w.shape
+    return _check(_lib.taco_grouped_linear(
+        _matrix(x, M, K, "x"), _groups_of(w, G, N, K, "w"), _matrix(bias, G, N, "bias"), act, _offsets(offsets, G), G,
+        _matrix(out, M, N, "out"), _matrix(preact, M, N, "preact"), M, N, K, *_workspace(workspace), _stream(stream)),
+        "taco_grouped_linear")
+
+
+def taco_grouped_linear_backward_workspace_bytes(groups, M, N, K):
+    return _lib.taco_grouped_linear_backward_workspace_bytes(groups, M, N, K)
+
+
+def taco_grouped_linear_backward(dout, x, w, offsets, act=TACO_ACT_NONE, preact=None, dx=None, dw=None, dbias=None,
+                                 workspace=None, stream=None):
+    """Gradients of taco_grouped_linear, each where its tensor is given."""
+    (M, K), (G, N, _) = x.shape, w.shape
+    return _check(_lib.taco_grouped_linear_backward(
+        _matrix(dout, M, N, "dout"), _matrix(x, M, K, "x"), _groups_of(w, G, N, K, "w"), act,
+        _matrix(preact, M, N, "preact"), _offsets(offsets, G), G, _matrix(dx, M, K, "dx"),
+        _groups_of(dw, G, N, K, "dw"), _matrix(dbias, G, N, "dbias"), M, N, K, *_workspace(workspace),
+        _stream(stream)), "taco_grouped_linear_backward")
+
+
+def taco_grouped_gated_linear_workspace_bytes(groups, M, F, K):
+    return _lib.taco_grouped_gated_linear_workspace_bytes(groups, M, F, K)
+
+
+def taco_grouped_gated_linear(x, w, offsets, out, act=TACO_ACT_SILU, preact=None, workspace=None, stream=None):
+    """out = act(z[:, :F]) * z[:, F:] with z = x w[g]^T for the rows of group g; w
+    bf16 [groups, 2 F, K], of each group the gate's rows first; preact receives z."""
+    (M, K), G, F = x.shape, w.shape[0], w.shape[1] // 2
+    return _check(_lib.taco_grouped_gated_linear(
+        _matrix(x, M, K, "x"), _groups_of(w, G, 2 * F, K, "w"), act, _offsets(offsets, G), G,
+        _matrix(out, M, F, "out"), _matrix(preact, M, 2 * F, "preact"), M, F, K, *_workspace(workspace),
+        _stream(stream)), "taco_grouped_gated_linear")
+
+
+def taco_grouped_gated_linear_backward_workspace_bytes(groups, M, F, K):
+    return _lib.taco_grouped_gated_linear_backward_workspace_bytes(groups, M, F, K)
+
+
+def taco_grouped_gated_linear_backward(dout, x, w, offsets, act=TACO_ACT_SILU, preact=None, dx=None, dw=None,
+                                       workspace=None, stream=None):
+    """Gradients of taco_grouped_gated_linear, each where its tensor is given."""
+    (M, K), G, F = x.shape, w.shape[0], w.shape[1] // 2
+    return _check(_lib.taco_grouped_gated_linear_backward(
+        _matrix(dout, M, F, "dout"), _matrix(x, M, K, "x"), _groups_of(w, G, 2 * F, K, "w"), act,
+        _matrix(preact, M, 2 * F, "preact"), _offsets(offsets, G), G, _matrix(dx, M, K, "dx"),
+        _groups_of(dw, G, 2 * F, K, "dw"), M, F, K, *_workspace(workspace), _stream(stream)),
+        "taco_grouped_gated_linear_backward")
 
 
 # ------------------------------------------------- buffer plumbing (torch) --

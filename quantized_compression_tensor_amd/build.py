@@ -22,7 +22,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtaco.so")
 
 SOURCES = ["taco_abi.hip", "fp8_hadamard.hip", "codecs.hip", "reorder.hip", "dequant_gemm.hip",
-           *(os.path.join(LAYERS, f) for f in ("layers_abi.hip", "norm.hip", "linear.hip"))]
+           *(os.path.join(LAYERS, f) for f in ("layers_abi.hip", "norm.hip", "linear.hip", "int8_abi.hip", "int8.hip",
+                                              "experts_abi.hip", "experts.hip"))]
 ARCH = "gfx950"
 
 # -ffp-contract=off: no fused multiply-adds except the explicit fmaf calls,

@@ -1,0 +1,219 @@
+// Projections in 8-bit integers: rows to codes, and the forward products of
+// codes with a scale for each row of x (a token) and of w (an output channel),
+//   z[m, n] = (sum over k of qx[m, k] qw[n, k]) sx[m] sw[n] + bias
+// with the epilogues of linear.hip. The sums are whole numbers, exact in 32
+// bits up to K = 131071 (2^31 / 2^14), so neither their order nor a cut of K
+// changes a bit; a sum becomes a float with one rounding, and each scale is one
+// more.
+//
+// The matrix cores take twice as many codes as bf16 elements at a time, in the
+// same 16 bytes of a lane, so a product of codes is one of 16-bit elements with
+// half the K to everything but the matrix instruction and the epilogue: tiles,
+// stages of LDS, waits and plans are those of linear.hip.
+#define TACO_DEVICE_CODE_ONLY
+#include "linear.hip"
+
+namespace taco {
+
+// --------------------------------------------------------------- products --
+
+template <class TL, bool GATED>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_int8(GemmArgs a) {
+  gemm<TL, false, false, GATED, Int8>(a, blockIdx.x);
+}
+
+template <class TL, bool GATED>
+static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_int8<TL, GATED>), dim3(a.whole + a.rest * a.parts), dim3(TL::kThreads), TL::kLdsBytes, s, a);
+  if (a.rest == 0) return;
+  const int octs = (GATED ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
+  hipLaunchKernelGGL((k_join<TL, GATED, Int8>), dim3(a.rest, (unsigned)(TL::BM / rows)), dim3(256), 0, s, a);
+}
+
+bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated) {
+  const int64_t weights = (gated ? 2 : 1) * N * K;
+  return M <= 4 || (M <= kFewRows && weights * M <= int64_t(1) << 30);
+}
+
+hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s) {
+  if (few_rows_int8(a.M, a.N, a.K, a.gated)) {
+    const dim3 grid(set_few_columns(&a)), block(kFewWaves * kWave);
+    if (a.M <= 16) {
+      if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true, Int8>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((k_few_rows<1, false, Int8>), grid, block, 0, s, a);
+    } else {
+      if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true, Int8>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((k_few_rows<2, false, Int8>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+  }
+  const bool large = set_gemm_plan(&a, partials);
+  if (a.gated) {
+    if (large) launch_tiles_int8<TilesLarge, true>(a, s);
+    else launch_tiles_int8<TilesSmall, true>(a, s);
+  } else {
+    if (large) launch_tiles_int8<TilesLarge, false>(a, s);
+    else launch_tiles_int8<TilesSmall, false>(a, s);
+  }
+  return hipGetLastError();
+}
+
+// ----------------------------------------------------------------- packing --
+
+// Copies matrices of bytes so that rows start on 16 bytes and hold a multiple
+// of 16, zeros past the last; a lane takes 16. Rows may start anywhere.
+__global__ __launch_bounds__(256) void k_pack_int8(PackArgs a) {
+  const PackArgs::One m = a.m[blockIdx.y];
+  const int64_t parts = (m.cols + 15) / 16, total = m.rows * parts;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)parts : i / parts;
+    const int64_t c = (i - row * parts) * 16, left = m.cols - c;
+    const u32x4 v = few_load<Int8>(static_cast<const char*>(m.src.p) + row * m.src.ld + c, left < 16 ? (int)left : 16);
+    *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(m.dst) + row * m.ld + c) = v;
+  }
+}
+
+hipError_t launch_pack_int8(const PackArgs& a, hipStream_t s) {
+  int64_t most = 0;
+  for (int i = 0; i < a.count; ++i) most = std::max(most, a.m[i].rows * ((a.m[i].cols + 15) / 16));
+  const unsigned blocks = (unsigned)std::min<int64_t>((most + 255) / 256, 4096);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_pack_int8, dim3(blocks, (unsigned)a.count), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ rows to codes --
+
+// The largest magnitude of a row, as the bits of its absolute value: these are
+// in the order of the values, with infinity and then NaN above all others.
+TACO_DEV unsigned magnitude(float f) { return __builtin_bit_cast(unsigned, f) & 0x7FFFFFFFu; }
+
+TACO_DEV unsigned lanes_max(unsigned v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const unsigned o = (unsigned)__shfl_xor((int)v, d, kWave);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// A row's scale A / 127 and what its elements are multiplied by, 127 / A: the
+// codec INT8_SYM's. Rows below kTiny are zeros; rows with an infinity or NaN
+// have that as their scale, and codes of zero.
+struct RowScale {
+  float scale, inv;
+  TACO_DEV explicit RowScale(unsigned bits) {
+    const float largest = __builtin_bit_cast(float, bits);
+    const bool finite = bits < 0x7F800000u, zero = finite && largest < kTiny;
+    scale = zero ? 0.0f : finite ? largest / 127.0f : largest;
+    inv = finite && !zero ? 127.0f / largest : 0.0f;
+  }
+  // |x inv| is below 127.5, so the codes need no clamp
+  TACO_DEV int code(float x) const { return inv == 0.0f ? 0 : rne_int(x * inv); }
+};
+TACO_DEV unsigned four_codes(const float* f, const RowScale& s) {
+  return (unsigned)(s.code(f[0]) & 255) | (unsigned)(s.code(f[1]) & 255) << 8 | (unsigned)(s.code(f[2]) & 255) << 16 |
+         (unsigned)s.code(f[3]) << 24;
+}
+
+constexpr int kQuantizeSteps = 4;   // eights of a row that a lane holds
+
+// A row is held by `waves` waves, four eights to a lane at most; where it is
+// longer (SECOND) its parts are read again for the codes. Bound by memory.
+template <int DT, bool SECOND>
+__global__ __launch_bounds__(1024) void k_quantize(QuantizeArgs a, int waves) {
+  __shared__ unsigned largest[2][16];   // used in turn, so that one barrier a row is enough
+  const int wave = wave_in_group(), size = waves * kWave, first_wave = wave / waves * waves;
+  const int lane = (int)threadIdx.x - first_wave * kWave, rows_at_once = (int)blockDim.x / size;
+  int turn = 0;
+  for (int64_t block = (int64_t)blockIdx.x * rows_at_once; block < a.rows; block += (int64_t)gridDim.x * rows_at_once) {
+    const int64_t row = block + wave / waves;
+    const bool live = row < a.rows;
+    const char* x = static_cast<const char*>(a.x.p) + (live ? row : 0) * a.x.ld * (DT == kBF16 ? 2 : 4);
+    char* q = static_cast<char*>(a.q.p) + (live ? row : 0) * a.q.ld;
+    const int64_t octs = live ? (a.cols + 7) / 8 : 0, per = (int64_t)kQuantizeSteps * size;
+    Oct<DT> o[kQuantizeSteps];
+    auto load = [&](int64_t from) {
+#pragma unroll
+      for (int i = 0; i < kQuantizeSteps; ++i) {
+        const int64_t c = from + lane + i * size, left = a.cols - 8 * c;
+        o[i].clear();
+        if (c < octs) o[i].load(x, 8 * c, left < 8 ? (int)left : 8);
+      }
+    };
+    unsigned m = 0;
+    auto look = [&] {
+#pragma unroll
+      for (int i = 0; i < kQuantizeSteps; ++i) {
+        float f[8];
+        o[i].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned b = magnitude(f[e]);
+          m = b > m ? b : m;
+        }
+      }
+    };
+    load(0);
+    look();
+    if constexpr (SECOND) {
+      for (int64_t from = per; from < octs; from += per) {
+        load(from);
+        look();
+      }
+    }
+    m = lanes_max(m);
+    if (waves > 1) {
+      if (lane % kWave == 0) largest[turn][wave] = m;
+      __syncthreads();
+      for (int w = 0; w < waves; ++w) m = largest[turn][first_wave + w] > m ? largest[turn][first_wave + w] : m;
+      turn ^= 1;
+    }
+    const RowScale s(m);
+    auto store = [&](int64_t from) {
+#pragma unroll
+      for (int i = 0; i < kQuantizeSteps; ++i) {
+        const int64_t c = from + lane + i * size, left = a.cols - 8 * c;
+        if (c >= octs) continue;
+        float f[8];
+        o[i].get(f);
+        const unsigned w[2] = {four_codes(f, s), four_codes(f + 4, s)};
+        if (left >= 8) {
+          __builtin_memcpy(q + 8 * c, w, 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < left) q[8 * c + e] = (char)(w[e / 4] >> (8 * (e % 4)));
+        }
+      }
+    };
+    if constexpr (SECOND) {
+      for (int64_t from = 0; from < octs; from += per) {
+        load(from);
+        store(from);
+      }
+    } else {
+      store(0);
+    }
+    if (live && lane == 0) a.scale[row] = s.scale;
+  }
+}
+
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
+  const int64_t octs = (a.cols + 7) / 8;
+  int waves = 1;
+  while (waves < 16 && (int64_t)waves * kWave * kQuantizeSteps < octs) waves *= 2;
+  const bool second = (int64_t)waves * kWave * kQuantizeSteps < octs;
+  const int per = std::max(1, 4 / waves);
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 16)), block((unsigned)(per * waves * kWave));
+  if (a.x.dt == kBF16) {
+    if (second) hipLaunchKernelGGL((k_quantize<kBF16, true>), grid, block, 0, s, a, waves);
+    else hipLaunchKernelGGL((k_quantize<kBF16, false>), grid, block, 0, s, a, waves);
+  } else {
+    if (second) hipLaunchKernelGGL((k_quantize<kF32, true>), grid, block, 0, s, a, waves);
+    else hipLaunchKernelGGL((k_quantize<kF32, false>), grid, block, 0, s, a, waves);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace taco

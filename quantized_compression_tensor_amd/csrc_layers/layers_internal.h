@@ -7,7 +7,7 @@
 
 namespace taco {
 
-enum Dtype : int { kF32 = 0, kBF16 = 1 };
+enum Dtype : int { kF32 = 0, kBF16 = 1, kI8 = 2 };
 
 // A row-major matrix or a vector; p null: absent.
 struct Mat {
@@ -59,6 +59,7 @@ struct Epilogue {
   Mat preact;     // receives z (+ bias), may be absent
   Mat out;
   int act;
+  const float *row_scale, *col_scale;   // [M], [weight rows]: for products of 8-bit codes
 };
 
 // One operand of a matrix product, bf16: element (i, k) of its [rows, K] view
@@ -125,6 +126,10 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
+// Fills in the plan of a product; whether its tiles are the large ones.
+bool set_gemm_plan(GemmArgs* a, void* partials);
+// Fills in the columns of a workgroup of the kernel for few rows; its grid.
+unsigned set_few_columns(GemmArgs* a);
 // Both gradients of a projection, dx [M, K] and dw [wide, K], and a column
 // sum, as one launch where they are small; gemm_pair_partial_bytes: for these,
 // else 0.
@@ -132,5 +137,39 @@ size_t gemm_pair_partial_bytes(int64_t M, int64_t wide, int64_t K);
 hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, const ColumnSumArgs& sum, void* partials, hipStream_t s);
 hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s);   // and launch_pack's work
 void launch_column_sum(const ColumnSumArgs& a, hipStream_t s);
+
+// Rows to codes of 8 bits, q[r, c] = x[r, c] / scale[r] rounded.
+struct QuantizeArgs {
+  Mat x, q;
+  int64_t rows, cols;
+  float* scale;
+};
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
+
+// Forward products of codes of 8 bits: in GemmArgs, ld and K in elements for
+// few rows, else in pairs of them (lines of whole 16 bytes, zeros past the
+// last k). launch_pack_int8: copies of such lines; here all sizes in elements.
+bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated);
+hipError_t launch_pack_int8(const PackArgs& a, hipStream_t s);
+hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s);
+
+// Rows offsets[g] ... offsets[g + 1] of a matrix of `rows` rows are group g's;
+// `count` groups. An offset outside of [0, rows] counts as its nearer end.
+struct Groups {
+  const int32_t* offsets;
+  int count;
+  int rows;
+};
+// Products by group. launch_experts: rows of a with the group's part of b
+// (`b_rows` rows of it), a.M not looked at; a.K and a.N as ever.
+// launch_experts_dw: for each group out [a.M, a.N] = the product over its rows.
+hipError_t launch_experts(const GemmArgs& a, const Groups& g, int64_t b_rows, hipStream_t s);
+hipError_t launch_experts_dw(const GemmArgs& a, const Groups& g, hipStream_t s);
+// Whether the forward product takes the kernel for few rows.
+bool few_rows_experts(const Groups& g, int64_t N, int64_t K, bool gated);
+// dz of the groups' rows with the sums over each group's rows, dbias
+// [groups, N]; partials [experts_back_ranges][N].
+int64_t experts_back_ranges(const Groups& g);
+hipError_t launch_experts_act_back(const ActBackArgs& a, const Mat& dbias, const Groups& g, hipStream_t s);
 
 }  // namespace taco

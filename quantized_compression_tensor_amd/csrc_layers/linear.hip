@@ -122,6 +122,16 @@ TACO_DEV void load_residual(const Epilogue& e, int64_t m, int n, int count, floa
   if (e.residual.p && count > 0) load8(e.residual.p, e.residual.dt, m * e.residual.ld + n, count, r);
 }
 
+// Products of 8-bit codes: their sums, whole numbers, become the values that
+// they stand for, sum * scale of the row * scale of the column.
+TACO_DEV void load_scale(const Epilogue& e, int n, int count, float* s) {
+  if (count > 0) load8(e.col_scale, kF32, n, count, s);
+}
+TACO_DEV void to_values(float* z, float row_scale, const float* col_scale) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = (float)__builtin_bit_cast(int, z[i]) * row_scale * col_scale[i];
+}
+
 // Whether an output is streamed past the caches: where a store instruction
 // writes whole 128-byte lines, so bf16 whose rows start on one (4096 x 4096 x
 // 512 23.2 us cached, 21.0 streamed). Otherwise the caches join the parts of a
@@ -266,7 +276,7 @@ struct Tiles {
   // After how many of a slice's rows of MFMA tiles a stage is handed back: b's
   // in the first slice, a's in the second
   static constexpr int kFreeB = TM / 2, kFreeA = TM / 4;
-  static constexpr int kTurnLd = TN * 16 + 4, kTurnMost = 32;    // the epilogue's turn: floats of a row, rows at most
+  static constexpr int kTurnLd = TN * 16 + 4, kTurnMost = TM < 2 ? 16 : 32;   // the epilogue's turn: floats of a row, rows at most
   static constexpr int kLdsBytes = (kStagesA * kA + kStagesB * kB) * 2;
   static_assert(WGM * WGN * kTurnMost * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
@@ -346,6 +356,25 @@ struct Chunks {
   // lie within 32).
   static TACO_DEV bool second(int wave, int i) {
     return GATED && ((wave * (kWave / Tile::kPerLine) + i * kLines) / 32 & 1) != 0;
+  }
+};
+
+// Operand types of the matrix cores. Either takes 16 bytes of each operand per
+// lane; the k that these are need only be the same in both.
+struct Bf16 {
+  static constexpr bool kScaled = false;   // sums are those of the values
+  typedef f32x4 Sums;
+  static TACO_DEV Sums product(bf16x8 a, bf16x8 b, Sums c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+// Whole numbers of 8 bits, two to each 16 of the operands' k: the sums are exact
+// in 32 bits, and become floats in the epilogue.
+struct Int8 {
+  static constexpr bool kScaled = true;   // sums are of codes, in whole numbers
+  typedef int Sums __attribute__((ext_vector_type(4)));
+  static TACO_DEV Sums product(bf16x8 a, bf16x8 b, Sums c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(Sums, a), __builtin_bit_cast(Sums, b), c, 0, 0, 0);
   }
 };
 
@@ -445,9 +474,18 @@ TACO_DEV void hand_over() {
 // at 2.4 GHz, LDS 0.22 to 0.26, and L2 gives 14 to 19 TB/s where a loop of reads
 // gets 31 to 33. Five stages of a and four of b instead of three and two, for one
 // tile on a CU, were no faster, so a longer reach ahead is not what is missing.
-// `block`: of the product's a.whole + a.rest * a.parts.
-template <class TL, bool AK, bool BK_, bool GATED>
-TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
+struct Tile {
+  const uint16_t *a, *b, *b2;   // the operands' first elements (b2: the other projection's)
+  int64_t lda, ldb;
+  int64_t K;                    // of this part
+  int64_t m0;                   // first row and column of the output
+  int n0;
+  int rows, cols;               // of the output that exist from there on, at most the tile's
+  int N;                        // columns of the whole output
+  float* part;                  // receives the sums, null: the epilogue does
+};
+template <class TL, bool AK, bool BK_, bool GATED, class OP>
+TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
   static_assert(!GATED || TN == 4, "a wave holds the two projections of its columns");
@@ -455,54 +493,42 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
   const int wm = wave / TL::WGN, wn = wave % TL::WGN;
-  const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
-  // the tiles with all of K, then the parts of the others, each in its own order
-  const bool whole = block < a.whole;
-  const unsigned index = whole ? xcd_ordered(block, a.whole) : xcd_ordered(block - a.whole, a.rest * a.parts);
-  const unsigned part = whole ? 0 : index / a.rest;
-  unsigned tm, tn;
-  tile_of(whole ? index : a.whole + index % a.rest, ntm, ntn, &tm, &tn);
-  const int64_t m0 = (int64_t)tm * BM, k0 = part * a.part;
-  const int n0 = (int)tn * kCols;
-  const int64_t K = whole || a.K - k0 < a.part ? a.K - k0 : a.part;   // of this part
-  const int rows_a = (int)(a.M - m0 < BM ? a.M - m0 : BM), rows_b = a.N - n0 < kCols ? a.N - n0 : kCols;
-  const uint16_t* pa = a.a.p + (AK ? m0 + k0 * a.a.ld : m0 * a.a.ld + k0);
-  const uint16_t* pb = a.b.p + (BK_ ? n0 + k0 * a.b.ld : n0 * a.b.ld + k0);
-  const uint16_t* pb2 = GATED ? pb + (int64_t)a.N * a.b.ld : pb;
+  const bool whole = t.part == nullptr;
+  const int64_t m0 = t.m0, K = t.K;
+  const int n0 = t.n0;
   using LA = Loader<AK, BM, NT, false>;
   using LB = Loader<BK_, BN, NT, GATED>;
   LA la;
   LB lb;
-  la.init(pa, pa, a.a.ld, rows_a, K, tid);
-  lb.init(pb, pb2, a.b.ld, rows_b, K, tid);
-  f32x4 acc[TM][TN];
+  la.init(t.a, t.a, t.lda, t.rows, K, tid);
+  lb.init(t.b, t.b2, t.ldb, t.cols, K, tid);
+  typename OP::Sums acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
 
   const int steps = (int)((K + BK - 1) / BK);
   uint16_t *const lds_a = lds, *const lds_b = lds + TL::kStagesA * TL::kA;
   bf16x8 fa[TM], fb[2][TN];
-  auto read_a = [&](const uint16_t* t, int kk, int i) { fa[i] = LdsTile<AK, BM>::operand(t, (wm * TM + i) * 16, kk, lane); };
-  auto read_b = [&](const uint16_t* t, int kk) {
+  auto read_a = [&](const uint16_t* s, int kk, int i) { fa[i] = LdsTile<AK, BM>::operand(s, (wm * TM + i) * 16, kk, lane); };
+  auto read_b = [&](const uint16_t* s, int kk) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[kk][j] = LdsTile<BK_, BN>::operand(t, (wn * TN + j) * 16, kk, lane);
+    for (int j = 0; j < TN; ++j) fb[kk][j] = LdsTile<BK_, BN>::operand(s, (wn * TN + j) * 16, kk, lane);
   };
   auto multiply = [&](int kk, int i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[kk][j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < TN; ++j) acc[i][j] = OP::product(fa[i], fb[kk][j], acc[i][j]);
   };
-  // Part `part` of `parts` of the loads of step ks into stage t.
-  auto load = [&](auto& l, int ks, uint16_t* t, int part, int parts) {
+  // Part `part` of `parts` of the loads of step ks into stage s.
+  auto load = [&](auto& l, int ks, uint16_t* s, int part, int parts) {
     constexpr int kPer = std::remove_reference_t<decltype(l)>::kPer;
     const int each = (kPer + parts - 1) / parts;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (i / each == part) l.issue(t, wave, K - (int64_t)ks * BK, i);
+      if (i / each == part) l.issue(s, wave, K - (int64_t)ks * BK, i);
   };
   if (steps > 0) {
     uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
@@ -516,7 +542,7 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
     read_b(b0, 0);
-    constexpr int kFreeA = TL::kFreeA, kFreeB = TL::kFreeB;
+    constexpr int kFreeA = TL::kFreeA, kFreeB = TL::kFreeB, kNextB = kFreeA + 1 < TM ? kFreeA + 1 : kFreeA;
 #pragma unroll 1
     for (int ks = 0; ks < steps; ++ks) {
       read_b(b0, 1);
@@ -542,21 +568,21 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
         if (i >= kFreeA) load(la, ks + 3, a0, i - kFreeA, TM - kFreeA);
         multiply(1, i);
         if (i >= kFreeA) read_a(a1, 0, i);
-        if (i == kFreeA + 1) read_b(b1, 0);
+        if (i == kNextB) read_b(b1, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      uint16_t* t = a0;
+      uint16_t* s = a0;
       a0 = a1;
       a1 = a2;
-      a2 = t;
-      t = b0;
+      a2 = s;
+      s = b0;
       b0 = b1;
-      b1 = t;
+      b1 = s;
     }
   }
   hand_over<0, 0>();
 
-  // Accumulator e of lane l holds row 4 (l / 16) + e, column l % 16 of its
+  // Accumulator q of lane l holds row 4 (l / 16) + q, column l % 16 of its
   // tile. Each wave turns kTurnRows rows at a time round through its own part
   // of LDS, so that a lane has eight neighbouring columns of a row, and has the
   // residuals of all of its rows under way together. A turn's code is there
@@ -571,10 +597,13 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   constexpr int kWaveCols = GATED ? TN * 8 : TN * 16, kLanes = kWaveCols / 8;
   constexpr int kPass = kWave / kLanes, kRound = kTurnRows / kPass;   // rows of a pass, passes
   float* turn = reinterpret_cast<float*>(lds) + wave * kTurnRows * kLd;
-  const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c, count = a.N - n;
-  const bool full = rows_a == BM && rows_b == kCols;
-  float bias[8];
-  if (!GATED && !kPlain) load_bias(a.e, n, whole ? count : 0, bias);
+  const int c = (lane % kLanes) * 8, n = n0 + wn * kWaveCols + c, count = t.N - n;
+  const int64_t m_end = m0 + t.rows;
+  const bool full = t.rows == BM && t.cols == kCols;
+  float bias[8], scale[8], scale_u[8];
+  if (!GATED && !kPlain) load_bias(e, n, whole ? count : 0, bias);
+  if (OP::kScaled) load_scale(e, n, whole ? count : 0, scale);
+  if (OP::kScaled && GATED) load_scale(e, t.N + n, whole ? count : 0, scale_u);
 #pragma unroll 1
   for (int i0 = 0; i0 < TM; i0 += kTurn) {
 #pragma unroll
@@ -582,8 +611,10 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          turn[(16 * h + 4 * (lane >> 4) + e) * kLd + j * 16 + (lane & 15)] = acc[h][j][e];
+        for (int q = 0; q < 4; ++q) {
+          const auto sum = acc[h][j][q];   // (a bit cast of a vector's element itself takes the first one)
+          turn[(16 * h + 4 * (lane >> 4) + q) * kLd + j * 16 + (lane & 15)] = __builtin_bit_cast(float, sum);
+        }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     int rows_done = i0 * 16;
     asm volatile("" : "+s"(rows_done));   // addresses are not carried from turn to turn: they would take 40 registers
@@ -592,7 +623,7 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
     if (!whole || full) {
       float z[kRound][8], u[GATED ? kRound : 1][8], r[kPlain || GATED ? 1 : kRound][8];
       if constexpr (!GATED && !kPlain) {
-        if (whole && a.e.residual.p) load_rows(a.e.residual, m, kPass, n, r);
+        if (whole && e.residual.p) load_rows(e.residual, m, kPass, n, r);
       }
 #pragma unroll
       for (int q = 0; q < kRound; ++q)
@@ -602,38 +633,53 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
           if constexpr (GATED)
             *reinterpret_cast<f32x4*>(u[q] + h) = *reinterpret_cast<const f32x4*>(row + q * kPass * kLd + kWaveCols + h);
         }
+      if constexpr (OP::kScaled) {
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < kRound; ++q) {
+            const float row_scale = e.row_scale[m + q * kPass];
+            to_values(z[q], row_scale, scale);
+            if constexpr (GATED) to_values(u[q], row_scale, scale_u);
+          }
+        }
+      }
       if (!whole) {
-        float* part_row = a.partials + ((int64_t)index * BM + (m - m0)) * BN + (n - n0);
+        float* part_row = t.part + (m - m0) * BN + (n - n0);
 #pragma unroll
         for (int q = 0; q < kRound; ++q) {
-          if (m + q * kPass >= a.M || count <= 0) continue;
+          if (m + q * kPass >= m_end || count <= 0) continue;
           keep8(part_row + q * kPass * BN, z[q]);   // eights past the last column too: the tile has room
           if constexpr (GATED) keep8(part_row + q * kPass * BN + kCols, u[q]);
         }
       } else if constexpr (GATED) {
-        finish_gated_rows(a.e, a.N, m, kPass, n, z, u);
+        finish_gated_rows(e, t.N, m, kPass, n, z, u);
       } else if constexpr (kPlain) {
-        store_rows(a.e.out, m, kPass, n, z, streamed(a.e.out));
+        store_rows(e.out, m, kPass, n, z, streamed(e.out));
       } else {
-        finish_rows(a.e, m, kPass, n, z, bias, r);
+        finish_rows(e, m, kPass, n, z, bias, r);
       }
     } else {
 #pragma unroll 1
       for (int q = 0; q < kRound; ++q) {
-        if (m + q * kPass >= a.M || count <= 0) continue;
+        if (m + q * kPass >= m_end || count <= 0) continue;
         float z[8], u[8], r[8];
 #pragma unroll
         for (int h = 0; h < 8; h += 4) {
           *reinterpret_cast<f32x4*>(z + h) = *reinterpret_cast<const f32x4*>(row + q * kPass * kLd + h);
           if (GATED) *reinterpret_cast<f32x4*>(u + h) = *reinterpret_cast<const f32x4*>(row + q * kPass * kLd + kWaveCols + h);
         }
+        if constexpr (OP::kScaled) {
+          const float row_scale = e.row_scale[m + q * kPass];
+          to_values(z, row_scale, scale);
+          if constexpr (GATED) to_values(u, row_scale, scale_u);
+        }
         if constexpr (GATED) {
-          finish_gated(a.e, a.N, m + q * kPass, n, count, z, u);
+          finish_gated(e, t.N, m + q * kPass, n, count, z, u);
         } else if constexpr (kPlain) {
-          store_out(a.e.out, (m + q * kPass) * a.e.out.ld + n, count, z);
+          store_out(e.out, (m + q * kPass) * e.out.ld + n, count, z);
         } else {
-          load_residual(a.e, m + q * kPass, n, count, r);
-          finish(a.e, m + q * kPass, n, count, z, bias, r);
+          load_residual(e, m + q * kPass, n, count, r);
+          finish(e, m + q * kPass, n, count, z, bias, r);
         }
       }
     }
@@ -645,9 +691,39 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   }
 }
 
+
+// `block` of the product's a.whole + a.rest * a.parts.
+template <class TL, bool AK, bool BK_, bool GATED, class OP>
+TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
+  constexpr int BM = TL::BM, BN = TL::BN;
+  constexpr int kCols = GATED ? BN / 2 : BN;
+  const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
+  // the tiles with all of K, then the parts of the others, each in its own order
+  const bool whole = block < a.whole;
+  const unsigned index = whole ? xcd_ordered(block, a.whole) : xcd_ordered(block - a.whole, a.rest * a.parts);
+  const unsigned part = whole ? 0 : index / a.rest;
+  unsigned tm, tn;
+  tile_of(whole ? index : a.whole + index % a.rest, ntm, ntn, &tm, &tn);
+  Tile t;
+  t.m0 = (int64_t)tm * BM;
+  t.n0 = (int)tn * kCols;
+  t.N = a.N;
+  t.rows = (int)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
+  t.cols = a.N - t.n0 < kCols ? a.N - t.n0 : kCols;
+  const int64_t k0 = part * a.part;
+  t.K = whole || a.K - k0 < a.part ? a.K - k0 : a.part;
+  t.a = a.a.p + (AK ? t.m0 + k0 * a.a.ld : t.m0 * a.a.ld + k0);
+  t.b = a.b.p + (BK_ ? t.n0 + k0 * a.b.ld : t.n0 * a.b.ld + k0);
+  t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
+  t.lda = a.a.ld;
+  t.ldb = a.b.ld;
+  t.part = whole ? nullptr : a.partials + (int64_t)index * BM * BN;
+  sum_tile<TL, AK, BK_, GATED, OP>(a.e, t);
+}
+
 template <class TL, bool AK, bool BK_, bool GATED>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm(GemmArgs a) {
-  gemm<TL, AK, BK_, GATED>(a, blockIdx.x);
+  gemm<TL, AK, BK_, GATED, Bf16>(a, blockIdx.x);
 }
 // All gradients at once, where the products do not fill the device: dx = dz W
 // in the first `count_dx` workgroups, dw = dz^T x in the next `count_dw`, and
@@ -658,8 +734,8 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm_pair(GemmArgs dx, Gemm
                                                                unsigned count_dx, unsigned count_dw) {
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   const unsigned b = blockIdx.x;
-  if (b < count_dx) gemm<TL, false, true, false>(dx, b);
-  else if (b < count_dx + count_dw) gemm<TL, true, true, false>(dw, b - count_dx);
+  if (b < count_dx) gemm<TL, false, true, false, Bf16>(dx, b);
+  else if (b < count_dx + count_dw) gemm<TL, true, true, false, Bf16>(dw, b - count_dx);
   else column_sum<TL::kThreads / kWave>(sum, b - count_dx - count_dw, 0, reinterpret_cast<float*>(lds));
 }
 
@@ -667,7 +743,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_gemm_pair(GemmArgs dx, Gemm
 // workgroup takes some rows of a tile (blockIdx.x), a lane eight columns. Bound
 // by the parts' bytes, mostly out of the Infinity Cache: 15 us for 128 gated
 // tiles in two parts with both projections kept (92 MB, 6 TB/s).
-template <class TL, bool GATED>
+template <class TL, bool GATED, class OP>
 __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
   constexpr int BM = TL::BM, BN = TL::BN, kCols = GATED ? BN / 2 : BN, kOcts = kCols / 8, kRows = 256 / kOcts;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
@@ -679,17 +755,34 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
   if (m >= a.M || n >= a.N) return;
   float z[8], u[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = 0.0f, u[e] = 0.0f;
+  for (int i = 0; i < 8; ++i) z[i] = 0.0f, u[i] = 0.0f;
+  // (of codes: whole numbers, kept in the floats' bits)
+  auto add = [](float* sum, const float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (OP::kScaled)
+        sum[i] = __builtin_bit_cast(float, __builtin_bit_cast(int, sum[i]) + __builtin_bit_cast(int, f[i]));
+      else
+        sum[i] += f[i];
+    }
+  };
   for (unsigned p = 0; p < a.parts; ++p) {
     const float* at = a.partials + (((int64_t)p * a.rest + blockIdx.x) * BM + row) * BN + col;
     float f[8];
     load8(at, kF32, 0, f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] += f[e];
+    add(z, f);
     if (GATED) {
       load8(at, kF32, kCols, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] += f[e];
+      add(u, f);
+    }
+  }
+  if constexpr (OP::kScaled) {
+    float scale[8];
+    load_scale(a.e, n, a.N - n, scale);
+    to_values(z, a.e.row_scale[m], scale);
+    if (GATED) {
+      load_scale(a.e, a.N + n, a.N - n, scale);
+      to_values(u, a.e.row_scale[m], scale);
     }
   }
   if (GATED) finish_gated(a.e, a.N, m, n, a.N - n, z, u);
@@ -715,44 +808,73 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
 // left out no faster.
 constexpr int kFewRows = 32, kFewWaves = 16;
 
-template <int TM, bool GATED>
-__global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
-  constexpr int kUnits = 2;   // of a wave, loaded together
+// One workgroup's share of a product of few rows: `cols` output columns from n0
+// on, of N; addresses, strides and K in bytes.
+struct FewRows {
+  const char *a, *b;   // the first row, the first weight row of column 0
+  int64_t lda, ldb, K;
+  int64_t m0;          // first row and number of rows of the output
+  int rows, n0, cols, N;
+};
+
+// 16 bytes of a row of 16-bit elements or bytes, of which `n` exist (zeros past them).
+template <class OP>
+TACO_DEV u32x4 few_load(const char* p, int n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if constexpr (OP::kScaled) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (2 * i < n) v[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+  }
+  return v;
+}
+
+template <int TM, bool GATED, class OP>
+TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
+  constexpr int kUnits = 2;    // of a wave, loaded together
+  constexpr int kUnit = 128;   // bytes of a row
   __shared__ float parts[kFewWaves][TM][4 * kWave];
   __shared__ float sums[16 * TM][16];
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1), wave = wave_in_group();
-  const int n0 = (int)blockIdx.x * a.cols, r = lane & 15;
-  const int cols = a.N - n0 < a.cols ? a.N - n0 : a.cols;   // of this workgroup; lanes past them repeat the last
-  int n = GATED ? r & 7 : r;
-  n = n0 + (n < cols ? n : cols - 1);
-  const uint16_t* pw = a.b.p + (GATED && r >= 8 ? n + (int64_t)a.N : n) * a.b.ld + 8 * (lane >> 4);
-  const uint16_t* px[TM];
+  const int r = lane & 15;
+  int n = GATED ? r & 7 : r;   // lanes past the last column repeat it
+  n = f.n0 + (n < f.cols ? n : f.cols - 1);
+  const char* pw = f.b + (GATED && r >= 8 ? n + (int64_t)f.N : n) * f.ldb + 16 * (lane >> 4);
+  const char* px[TM];
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
-    const int64_t m = 16 * t + r;
-    px[t] = a.a.p + (m < a.M ? m : a.M - 1) * a.a.ld + 8 * (lane >> 4);
+    const int m = 16 * t + r;
+    px[t] = f.a + (m < f.rows ? m : f.rows - 1) * f.lda + 16 * (lane >> 4);
   }
-  f32x4 acc[TM];
+  typename OP::Sums acc[TM];
 #pragma unroll
-  for (int t = 0; t < TM; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto product = [&](const Oct<kBF16>& w, const Oct<kBF16>& x, int t) {
-    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v), __builtin_bit_cast(bf16x8, x.v),
-                                                     acc[t], 0, 0, 0);
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = 0;
+  auto product = [&](u32x4 w, u32x4 x, int t) {
+    acc[t] = OP::product(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc[t]);
   };
-  const int units = (int)(a.K / 64);
+  const int units = (int)(f.K / kUnit);
   for (int first = wave; first < units; first += kFewWaves * kUnits) {
-    Oct<kBF16> w[kUnits][2], x[kUnits][TM][2];
+    u32x4 w[kUnits][2], x[kUnits][TM][2];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int unit = first + u * kFewWaves;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        w[u][h].clear();
-        if (unit < units) w[u][h].load(pw, 64 * (int64_t)unit + 32 * h);
+        const int64_t at = kUnit * (int64_t)unit + kUnit / 2 * h;
+        w[u][h] = u32x4{0u, 0u, 0u, 0u};
+        if (unit < units) __builtin_memcpy(&w[u][h], pw + at, 16);
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
-          x[u][t][h].clear();
-          if (unit < units) x[u][t][h].load(px[t], 64 * (int64_t)unit + 32 * h);
+          x[u][t][h] = u32x4{0u, 0u, 0u, 0u};
+          if (unit < units) __builtin_memcpy(&x[u][t][h], px[t] + at, 16);
         }
       }
     }
@@ -764,42 +886,221 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
         for (int t = 0; t < TM; ++t) product(w[u][h], x[u][t][h], t);
   }
   if (wave == units % kFewWaves) {
-    // the last k, fewer than 64
-    for (int64_t k = 64 * (int64_t)units; k < a.K; k += 32) {
-      const int64_t left = a.K - k - 8 * (lane >> 4);
-      const int count = left > 8 ? 8 : left > 0 ? (int)left : 0;
-      Oct<kBF16> w, x;
-      w.load(pw, k, count);
+    // the last k, less than a unit
+    for (int64_t k = kUnit * (int64_t)units; k < f.K; k += kUnit / 2) {
+      const int64_t left = f.K - k - 16 * (lane >> 4);
+      const int count = left > 16 ? 16 : left > 0 ? (int)left : 0;
+      const u32x4 w = few_load<OP>(pw + k, count);
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        x.load(px[t], k, count);
-        product(w, x, t);
-      }
+      for (int t = 0; t < TM; ++t) product(w, few_load<OP>(px[t] + k, count), t);
     }
   }
-  // accumulator e of lane l holds weight row 4 (l / 16) + e, row l % 16 of x
+  // accumulator q of lane l holds weight row 4 (l / 16) + q, row l % 16 of x
 #pragma unroll
-  for (int t = 0; t < TM; ++t) *reinterpret_cast<f32x4*>(&parts[wave][t][4 * lane]) = acc[t];
+  for (int t = 0; t < TM; ++t)
+    *reinterpret_cast<f32x4*>(&parts[wave][t][4 * lane]) = __builtin_bit_cast(f32x4, acc[t]);
   __syncthreads();
   for (int i = tid; i < TM * 4 * kWave; i += kFewWaves * kWave) {
     const int t = i / (4 * kWave), q = i % (4 * kWave), l = q / 4;
-    float z = 0.0f;
+    float z;
+    if constexpr (OP::kScaled) {
+      int whole = 0;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) z += parts[w][t][q];
+      for (int w = 0; w < kFewWaves; ++w) whole += __builtin_bit_cast(int, parts[w][t][q]);
+      z = __builtin_bit_cast(float, whole);
+    } else {
+      z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) z += parts[w][t][q];
+    }
     sums[16 * t + l % 16][4 * (l / 16) + q % 4] = z;
   }
   __syncthreads();
-  const int m = GATED ? tid : tid / 2, c = GATED ? 0 : tid % 2 * 8;
-  if (m >= a.M || m >= 16 * TM || c >= cols) return;
+  const int m = GATED ? tid : tid / 2, c = GATED ? 0 : tid % 2 * 8, count = f.cols - c;
+  if (m >= f.rows || m >= 16 * TM || count <= 0) return;
   float z[8], u[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    z[e] = sums[m][c + e];
-    u[e] = sums[m][(c + 8 + e) % 16];
+  for (int i = 0; i < 8; ++i) {
+    z[i] = sums[m][c + i];
+    u[i] = sums[m][(c + 8 + i) % 16];
   }
-  if (GATED) finish_gated(a.e, a.N, m, n0, cols, z, u);
-  else finish(a.e, m, n0 + c, cols - c, z);
+  if constexpr (OP::kScaled) {
+    float scale[8];
+    const float row_scale = e.row_scale[f.m0 + m];
+    load_scale(e, f.n0 + c, count, scale);
+    to_values(z, row_scale, scale);
+    if constexpr (GATED) {
+      load_scale(e, f.N + f.n0, count, scale);
+      to_values(u, row_scale, scale);
+    }
+  }
+  if (GATED) finish_gated(e, f.N, f.m0 + m, f.n0, count, z, u);
+  else finish(e, f.m0 + m, f.n0 + c, count, z);
 }
+
+template <int TM, bool GATED, class OP>
+__global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
+  constexpr int kBytes = OP::kScaled ? 1 : 2;   // of an element
+  FewRows f;
+  f.a = reinterpret_cast<const char*>(a.a.p);
+  f.b = reinterpret_cast<const char*>(a.b.p);
+  f.lda = a.a.ld * kBytes;
+  f.ldb = a.b.ld * kBytes;
+  f.K = a.K * kBytes;
+  f.m0 = 0;
+  f.rows = (int)a.M;
+  f.n0 = (int)blockIdx.x * a.cols;
+  f.cols = a.N - f.n0 < a.cols ? a.N - f.n0 : a.cols;
+  f.N = a.N;
+  few_rows_product<TM, GATED, OP>(a.e, f);
+}
+
+// ----------------------------------------------------------------- packing --
+
+// Copies bf16 matrices so that rows start on 16 bytes and hold a multiple of
+// eight elements, zeros past the last: the tiles' loads into LDS want that,
+// and a copy at memory's speed costs less than loads that do not (4096 x 4096
+// x 4097 forward: 190 us with tiles staged through registers, 135 packed). A
+// lane takes eight elements; `block` of `blocks` for matrix `which`.
+TACO_DEV void pack(const PackArgs& a, unsigned block, unsigned blocks, unsigned which) {
+  const PackArgs::One m = a.m[which];
+  const int64_t octs = (m.cols + 7) / 8, total = m.rows * octs;
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
+    // (a division in 64 bits takes five times as long)
+    const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)octs : i / octs;
+    const int64_t c = (i - row * octs) * 8, left = m.cols - c;
+    Oct<kBF16> o;
+    o.load(m.src.p, row * m.src.ld + c, left < 8 ? (int)left : 8);
+    *reinterpret_cast<u32x4*>(m.dst + row * m.ld + c) = o.v;
+  }
+}
+
+// ------------------------------------------------- backward of activations --
+
+// A workgroup takes 512 columns (`slab`) of the rows from `first` to `end`,
+// a wave every fourth row of them, two at a time, a lane eight neighbouring
+// columns. Eight rows are a range; more where there would be over kActMaxGroups
+// ranges. Memory bounds it: gated 8192 x 5120, silu, 80 us (5.2 TB/s). With
+// gelu's slope the arithmetic takes about as long as the bytes, and the sums
+// of dbias add a tenth of them: 4096 x 4096 26 us (4.2 TB/s).
+constexpr int kActRows = 8, kActMaxGroups = 1024;
+
+// d = d act'(z), and of the gated layer u = d u act'(z), d = d act(z).
+TACO_DEV void times_slope(const float* z, float* d, int act) {
+  auto each = [&](int which) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], which);
+  };
+  if (act == kActGelu) each(kActGelu);
+  else if (act == kActSilu) each(kActSilu);
+  else each(kActRelu);
+}
+TACO_DEV void act_back_gated(const float* z, float* u, float* d, int act) {
+  auto each = [&](int which) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float value, slope;
+      act_both(z[e], which, &value, &slope);
+      u[e] = d[e] * u[e] * slope;
+      d[e] = d[e] * value;
+    }
+  };
+  if (act == kActGelu) each(kActGelu);
+  else if (act == kActSilu) each(kActSilu);
+  else if (act == kActRelu) each(kActRelu);
+  else each(kActNone);
+}
+
+template <bool GATED>
+TACO_DEV void act_back(const ActBackArgs& a, int64_t first, int64_t end, unsigned group, unsigned slab) {
+  __shared__ float sums[4][512];
+  const int lane = (int)threadIdx.x % kWave, wave = wave_in_group();
+  const int c = ((int)slab * kWave + lane) * 8, n = a.N - c;
+  float db[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) db[e] = 0.0f;
+  // dz's rows hold whole eights: zeros past the last column
+  const int pad = n < 8 && n > 0 && !GATED ? 8 : n;
+  // Z: z's type; WHOLE: each lane has eight columns
+  auto rows = [&](auto z_type, auto whole) {
+    constexpr int Z = z_type();
+    constexpr bool WHOLE = whole();
+    const int have = WHOLE ? 8 : n;
+    for (int64_t m = first + wave; m < end; m += 8) {
+      float d[2][8], z[2][8], u[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = m + 4 * i;
+        if (row >= end) break;
+        load8(a.dout.p, kBF16, row * a.dout.ld + c, have, d[i]);
+        if (GATED || a.act != kActNone) load8(a.z.p, Z, row * a.z.ld + c, have, z[i]);
+        if (GATED) load8(a.z.p, Z, row * a.z.ld + a.N + c, have, u[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = m + 4 * i;
+        if (row >= end) break;
+        if constexpr (GATED) {
+          act_back_gated(z[i], u[i], d[i], a.act);
+          store8(a.dz, kBF16, row * a.ld_dz + c, have, u[i]);
+          store8(a.dz, kBF16, row * a.ld_dz + a.N + c, have, d[i]);
+        } else {
+          if (a.act != kActNone) times_slope(z[i], d[i], a.act);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (!WHOLE && e >= n) d[i][e] = 0.0f;
+            db[e] += d[i][e];
+          }
+          if (a.dz) store8(a.dz, kBF16, row * a.ld_dz + c, WHOLE ? 8 : pad, d[i]);
+        }
+      }
+    }
+  };
+  const std::integral_constant<int, kBF16> bf16;
+  const std::integral_constant<int, kF32> f32;
+  // (wave-uniform, so that a wave runs one of them)
+  const bool whole = a.N % 8 == 0 || ((int)slab + 1) * kWave * 8 <= a.N;
+  if (n <= 0) {
+  } else if (whole) {
+    if (a.z.dt == kBF16) rows(bf16, std::true_type());
+    else rows(f32, std::true_type());
+  } else {
+    if (a.z.dt == kBF16) rows(bf16, std::false_type());
+    else rows(f32, std::false_type());
+  }
+  if constexpr (GATED) {
+    // zeros past the last column of the second half
+    const int64_t rest = -2 * (int64_t)a.N & 7;
+    if (slab == 0 && threadIdx.x < rest)
+      for (int64_t m = first; m < end; ++m) a.dz[m * a.ld_dz + 2 * (int64_t)a.N + threadIdx.x] = 0;
+  } else {
+    if (a.partials == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = db[e];
+    __syncthreads();
+    for (int i = (int)threadIdx.x; i < 512; i += 256) {
+      const int col = (int)slab * 512 + i;
+      if (col < a.N)
+        a.partials[(int64_t)group * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+    }
+  }
+}
+
+// dz, and in the workgroups after its `blocks` the copies that the products
+// need beside it.
+template <bool GATED>
+__global__ __launch_bounds__(256) void k_act_back(ActBackArgs a, PackArgs p, unsigned groups, unsigned blocks,
+                                                  unsigned packing) {
+  if (blockIdx.x < blocks) {
+    const unsigned group = blockIdx.x % groups;
+    const int64_t per = (a.M + groups - 1) / groups, first = group * per;
+    act_back<GATED>(a, first, first + per < a.M ? first + per : a.M, group, blockIdx.x / groups);
+  } else pack(p, (blockIdx.x - blocks) % packing, packing, (blockIdx.x - blocks) / packing);
+}
+
+// The products by expert and of 8-bit codes (experts.hip, int8.hip) are made of
+// the device code above.
+#ifndef TACO_DEVICE_CODE_ONLY
 
 // ----------------------------------------------------------------- launch --
 
@@ -882,8 +1183,8 @@ static void launch_join(const GemmArgs& a, hipStream_t s) {
   if (a.rest == 0) return;
   const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
   const dim3 join(a.rest, (unsigned)(TL::BM / rows));
-  if (a.gated) hipLaunchKernelGGL((k_join<TL, true>), join, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_join<TL, false>), join, dim3(256), 0, s, a);
+  if (a.gated) hipLaunchKernelGGL((k_join<TL, true, Bf16>), join, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_join<TL, false, Bf16>), join, dim3(256), 0, s, a);
 }
 
 template <class TL>
@@ -907,21 +1208,31 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated) {
   return M <= 4 || (M <= kFewRows && weights * M <= int64_t(1) << 29);
 }
 
+// As many columns for a workgroup as give each CU the same number of them
+// (one row, 5120 x 20480: 41.9 us with 512 workgroups of 10 columns, 52.6
+// with 320 of 16); a few workgroups more than that run beside the others.
+unsigned set_few_columns(GemmArgs* a) {
+  const int most = a->gated ? 8 : 16, cus = kCus;
+  const int groups = (a->N + most - 1) / most, rounds = std::max(1, (groups - cus / 8 + cus - 1) / cus);
+  a->cols = std::min(most, (a->N + rounds * cus - 1) / (rounds * cus));
+  return (unsigned)((a->N + a->cols - 1) / a->cols);
+}
+
 static void launch_few_rows(GemmArgs a, hipStream_t s) {
-  // as many columns for a workgroup as give each CU the same number of them
-  // (one row, 5120 x 20480: 41.9 us with 512 workgroups of 10 columns, 52.6
-  // with 320 of 16); a few workgroups more than that run beside the others
-  const int most = a.gated ? 8 : 16, cus = kCus;
-  const int groups = (a.N + most - 1) / most, rounds = std::max(1, (groups - cus / 8 + cus - 1) / cus);
-  a.cols = std::min(most, (a.N + rounds * cus - 1) / (rounds * cus));
-  const dim3 grid((unsigned)((a.N + a.cols - 1) / a.cols)), block(kFewWaves * kWave);
+  const dim3 grid(set_few_columns(&a)), block(kFewWaves * kWave);
   if (a.M <= 16) {
-    if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_few_rows<1, false>), grid, block, 0, s, a);
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true, Bf16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_few_rows<1, false, Bf16>), grid, block, 0, s, a);
   } else {
-    if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_few_rows<2, false>), grid, block, 0, s, a);
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true, Bf16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_few_rows<2, false, Bf16>), grid, block, 0, s, a);
   }
+}
+
+bool set_gemm_plan(GemmArgs* a, void* partials) {
+  const Plan p = plan_of(a->M, a->N, a->K, a->gated);
+  set_plan(a, p, partials);
+  return p.large;
 }
 
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
@@ -930,9 +1241,7 @@ hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s) {
     launch_few_rows(a, s);
     return hipGetLastError();
   }
-  const Plan p = plan_of(a.M, a.N, a.K, a.gated);
-  set_plan(&a, p, partials);
-  if (p.large) launch_tiles<TilesLarge>(a, s);
+  if (set_gemm_plan(&a, partials)) launch_tiles<TilesLarge>(a, s);
   else launch_tiles<TilesSmall>(a, s);
   return hipGetLastError();
 }
@@ -955,25 +1264,6 @@ hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, const ColumnSumArgs& sum, 
   return hipGetLastError();
 }
 
-// ----------------------------------------------------------------- packing --
-
-// Copies bf16 matrices so that rows start on 16 bytes and hold a multiple of
-// eight elements, zeros past the last: the tiles' loads into LDS want that,
-// and a copy at memory's speed costs less than loads that do not (4096 x 4096
-// x 4097 forward: 190 us with tiles staged through registers, 135 packed). A
-// lane takes eight elements; `block` of `blocks` for matrix `which`.
-TACO_DEV void pack(const PackArgs& a, unsigned block, unsigned blocks, unsigned which) {
-  const PackArgs::One m = a.m[which];
-  const int64_t octs = (m.cols + 7) / 8, total = m.rows * octs;
-  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
-    // (a division in 64 bits takes five times as long)
-    const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)octs : i / octs;
-    const int64_t c = (i - row * octs) * 8, left = m.cols - c;
-    Oct<kBF16> o;
-    o.load(m.src.p, row * m.src.ld + c, left < 8 ? (int)left : 8);
-    *reinterpret_cast<u32x4*>(m.dst + row * m.ld + c) = o.v;
-  }
-}
 __global__ __launch_bounds__(256) void k_pack(PackArgs a) { pack(a, blockIdx.x, gridDim.x, blockIdx.y); }
 
 // Workgroups for each matrix.
@@ -990,130 +1280,9 @@ hipError_t launch_pack(const PackArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// ------------------------------------------------- backward of activations --
-
-// Workgroup `group` of `groups` takes 512 columns (`slab`) of a range of rows,
-// a wave every fourth row of them, two at a time, a lane eight neighbouring
-// columns. Eight rows are a range; more where there would be over kActMaxGroups
-// ranges. Memory bounds it: gated 8192 x 5120, silu, 80 us (5.2 TB/s). With
-// gelu's slope the arithmetic takes about as long as the bytes, and the sums
-// of dbias add a tenth of them: 4096 x 4096 26 us (4.2 TB/s).
-constexpr int kActRows = 8, kActMaxGroups = 1024;
 int act_back_groups(int64_t M) {
   const int64_t g = (M + kActRows - 1) / kActRows;
   return (int)(g < kActMaxGroups ? g : kActMaxGroups);
-}
-
-// d = d act'(z), and of the gated layer u = d u act'(z), d = d act(z).
-TACO_DEV void times_slope(const float* z, float* d, int act) {
-  auto each = [&](int which) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], which);
-  };
-  if (act == kActGelu) each(kActGelu);
-  else if (act == kActSilu) each(kActSilu);
-  else each(kActRelu);
-}
-TACO_DEV void act_back_gated(const float* z, float* u, float* d, int act) {
-  auto each = [&](int which) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float value, slope;
-      act_both(z[e], which, &value, &slope);
-      u[e] = d[e] * u[e] * slope;
-      d[e] = d[e] * value;
-    }
-  };
-  if (act == kActGelu) each(kActGelu);
-  else if (act == kActSilu) each(kActSilu);
-  else if (act == kActRelu) each(kActRelu);
-  else each(kActNone);
-}
-
-template <bool GATED>
-TACO_DEV void act_back(const ActBackArgs& a, unsigned group, unsigned groups, unsigned slab) {
-  __shared__ float sums[4][512];
-  const int lane = (int)threadIdx.x % kWave, wave = wave_in_group();
-  const int c = ((int)slab * kWave + lane) * 8, n = a.N - c;
-  const int64_t per = (a.M + groups - 1) / groups, first = group * per;
-  const int64_t end = first + per < a.M ? first + per : a.M;
-  float db[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) db[e] = 0.0f;
-  // dz's rows hold whole eights: zeros past the last column
-  const int pad = n < 8 && n > 0 && !GATED ? 8 : n;
-  // Z: z's type; WHOLE: each lane has eight columns
-  auto rows = [&](auto z_type, auto whole) {
-    constexpr int Z = z_type();
-    constexpr bool WHOLE = whole();
-    const int have = WHOLE ? 8 : n;
-    for (int64_t m = first + wave; m < end; m += 8) {
-      float d[2][8], z[2][8], u[2][8];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t row = m + 4 * i;
-        if (row >= end) break;
-        load8(a.dout.p, kBF16, row * a.dout.ld + c, have, d[i]);
-        if (GATED || a.act != kActNone) load8(a.z.p, Z, row * a.z.ld + c, have, z[i]);
-        if (GATED) load8(a.z.p, Z, row * a.z.ld + a.N + c, have, u[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t row = m + 4 * i;
-        if (row >= end) break;
-        if constexpr (GATED) {
-          act_back_gated(z[i], u[i], d[i], a.act);
-          store8(a.dz, kBF16, row * a.ld_dz + c, have, u[i]);
-          store8(a.dz, kBF16, row * a.ld_dz + a.N + c, have, d[i]);
-        } else {
-          if (a.act != kActNone) times_slope(z[i], d[i], a.act);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!WHOLE && e >= n) d[i][e] = 0.0f;
-            db[e] += d[i][e];
-          }
-          if (a.dz) store8(a.dz, kBF16, row * a.ld_dz + c, WHOLE ? 8 : pad, d[i]);
-        }
-      }
-    }
-  };
-  const std::integral_constant<int, kBF16> bf16;
-  const std::integral_constant<int, kF32> f32;
-  // (wave-uniform, so that a wave runs one of them)
-  const bool whole = a.N % 8 == 0 || ((int)slab + 1) * kWave * 8 <= a.N;
-  if (n <= 0) {
-  } else if (whole) {
-    if (a.z.dt == kBF16) rows(bf16, std::true_type());
-    else rows(f32, std::true_type());
-  } else {
-    if (a.z.dt == kBF16) rows(bf16, std::false_type());
-    else rows(f32, std::false_type());
-  }
-  if constexpr (GATED) {
-    // zeros past the last column of the second half
-    const int64_t rest = -2 * (int64_t)a.N & 7;
-    if (slab == 0 && threadIdx.x < rest)
-      for (int64_t m = first; m < end; ++m) a.dz[m * a.ld_dz + 2 * (int64_t)a.N + threadIdx.x] = 0;
-  } else {
-    if (a.partials == nullptr) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = db[e];
-    __syncthreads();
-    for (int i = (int)threadIdx.x; i < 512; i += 256) {
-      const int col = (int)slab * 512 + i;
-      if (col < a.N)
-        a.partials[(int64_t)group * a.N + col] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
-    }
-  }
-}
-
-// dz, and in the workgroups after its `blocks` the copies that the products
-// need beside it.
-template <bool GATED>
-__global__ __launch_bounds__(256) void k_act_back(ActBackArgs a, PackArgs p, unsigned groups, unsigned blocks,
-                                                  unsigned packing) {
-  if (blockIdx.x < blocks) act_back<GATED>(a, blockIdx.x % groups, groups, blockIdx.x / groups);
-  else pack(p, (blockIdx.x - blocks) % packing, packing, (blockIdx.x - blocks) / packing);
 }
 
 hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s) {
@@ -1126,5 +1295,7 @@ hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t 
   }
   return hipGetLastError();
 }
+
+#endif  // TACO_DEVICE_CODE_ONLY
 
 }  // namespace taco
