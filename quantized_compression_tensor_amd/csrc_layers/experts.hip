@@ -34,16 +34,26 @@ TACO_DEV unsigned lanes_scan(unsigned v) {
 }
 TACO_DEV unsigned lane_value(unsigned v, int lane) { return (unsigned)__builtin_amdgcn_readlane((int)v, lane); }
 
-// Tiles of 2^log rows in which the groups lie, each group beginning a new one.
+// Which tiles of 2^log rows are counted of a group, whose first row begins a
+// new one: all, those that it fills, or, for the rows left, ones of 2^rest_log.
+enum Count { kAllTiles, kFullTiles, kRestTiles };
+TACO_DEV unsigned tiles_of_rows(Count what, int rows, int log, int rest_log) {
+  if (rows <= 0) return 0;
+  const unsigned full = (unsigned)rows >> log, left = (unsigned)rows - (full << log);
+  if (what == kAllTiles) return full + (left != 0);
+  return what == kFullTiles ? full : left == 0 ? 0 : ((left - 1) >> rest_log) + 1;
+}
+
+// The groups' tiles, counted: each lane has some groups.
+template <Count WHAT>
 struct GroupTiles {
   const Groups& gr;
-  int log, per;               // groups of a lane
+  int log, rest_log, per;     // groups of a lane
   unsigned mine, upto;        // tiles of this lane's groups, and of them and all before
   int lo, hi;                 // rows of this lane's group, if each has one
-  TACO_DEV unsigned tiles(int first, int end) const {
-    return end > first ? ((unsigned)(end - first - 1) >> log) + 1 : 0;
-  }
-  TACO_DEV GroupTiles(const Groups& groups, int log_rows) : gr(groups), log(log_rows) {
+  TACO_DEV unsigned tiles(int first, int end) const { return tiles_of_rows(WHAT, end - first, log, rest_log); }
+  TACO_DEV GroupTiles(const Groups& groups, int log_rows, int log_rest = 0)
+      : gr(groups), log(log_rows), rest_log(log_rest) {
     const int lane = (int)threadIdx.x % kWave;
     per = (gr.count + kWave - 1) / kWave;
     mine = 0;
@@ -60,13 +70,14 @@ struct GroupTiles {
   TACO_DEV unsigned all() const { return lane_value(upto, kWave - 1); }
 };
 
-// A group and where its tiles lie among all.
+// A group and where its counted tiles lie among all.
 struct Group {
   int g, lo, hi;
   unsigned before, tiles;
 };
 // The group of tile t; false if there is none.
-TACO_DEV bool group_of_tile(const GroupTiles& gt, unsigned t, Group* out) {
+template <Count WHAT>
+TACO_DEV bool group_of_tile(const GroupTiles<WHAT>& gt, unsigned t, Group* out) {
   const unsigned long long after = __builtin_amdgcn_ballot_w64(gt.upto > t);
   if (after == 0) return false;
   const int lane = __builtin_ctzll(after);
@@ -96,31 +107,36 @@ constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 
 // --------------------------------------------------------------- products --
 
+using TilesHalf = Tiles<128, 256, 2, 4>;
 using TilesTall = Tiles<64, 128, 2, 2>;    // few rows to a group: the weights' bytes bound it
 using TilesFlat = Tiles<32, 128, 2, 2>;
+// What takes the rows that do not fill a tile.
+template <class TL>
+struct RestOf;
+template <>
+struct RestOf<TilesLarge> { using Type = TilesHalf; };
+template <>
+struct RestOf<TilesSmall> { using Type = TilesTall; };
+template <>
+struct RestOf<TilesTall> { using Type = TilesFlat; };
+template <>
+struct RestOf<TilesFlat> { using Type = TilesFlat; };
 
 // Forward products (w's k contiguous), and dx = dz w (BK_). Only as many
-// workgroups as the groups have tiles do anything.
-template <class TL, bool BK_, bool GATED>
-__global__ __launch_bounds__(TL::kThreads, 2) void k_experts(GemmArgs a, Groups gr, int64_t b_rows) {
+// workgroups as the groups have tiles do anything: first the tiles that are
+// full, in one contiguous range for each XCD, then those of the rows left, half
+// as high, which waste less and even out the last round.
+template <class TL, bool BK_, bool GATED, bool RAGGED>
+TACO_DEV void experts_tile(const GemmArgs& a, const Group& g, int64_t b_rows, int m0, unsigned tn) {
   constexpr int BM = TL::BM, kCols = GATED ? TL::BN / 2 : TL::BN;
-  const unsigned ntn = (unsigned)(a.N + kCols - 1) / kCols;
-  const GroupTiles gt(gr, log2_of(BM));
-  const unsigned count = gt.all() * ntn;
-  if (blockIdx.x >= count) return;
-  const unsigned index = xcd_ordered(blockIdx.x, count);
-  Group g;
-  if (!group_of_tile(gt, index / ntn, &g)) return;
-  unsigned tm, tn;
-  tile_of(index - g.before * ntn, g.tiles, ntn, &tm, &tn);
   Tile t;
-  t.m0 = g.lo + (int64_t)tm * BM;
+  t.m0 = m0;
   t.n0 = (int)tn * kCols;
   t.N = a.N;
-  t.rows = g.hi - (int)t.m0 < BM ? g.hi - (int)t.m0 : BM;
+  t.rows = g.hi - m0 < BM ? g.hi - m0 : BM;
   t.cols = a.N - t.n0 < kCols ? a.N - t.n0 : kCols;
   t.K = a.K;
-  t.a = a.a.p + t.m0 * a.a.ld;
+  t.a = a.a.p + m0 * a.a.ld;
   t.b = a.b.p + g.g * b_rows * a.b.ld + (BK_ ? t.n0 : t.n0 * a.b.ld);
   t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
   t.lda = a.a.ld;
@@ -129,18 +145,79 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_experts(GemmArgs a, Groups 
   Epilogue e = a.e;
   if (!BK_ && !GATED && e.bias.p)
     e.bias.p = static_cast<char*>(e.bias.p) + g.g * e.bias.ld * (e.bias.dt == kBF16 ? 2 : 4);
-  sum_tile<TL, false, BK_, GATED, Bf16>(e, t);
+  sum_tile<TL, false, BK_, GATED, Bf16, RAGGED>(e, t);
+}
+template <class TL, bool BK_, bool GATED>
+TACO_DEV void experts(const GemmArgs& a, const Groups& gr, int64_t b_rows, unsigned block) {
+  using TR = typename RestOf<TL>::Type;
+  static_assert(TL::kThreads == TR::kThreads && TL::BN == TR::BN && TR::kLdsBytes <= TL::kLdsBytes, "one launch");
+  constexpr int kCols = GATED ? TL::BN / 2 : TL::BN, kLog = log2_of(TL::BM), kRestLog = log2_of(TR::BM);
+  const unsigned ntn = (unsigned)(a.N + kCols - 1) / kCols;
+  const GroupTiles<kFullTiles> full(gr, kLog, kRestLog);
+  const GroupTiles<kRestTiles> rest(gr, kLog, kRestLog);
+  const unsigned count = full.all() * ntn;
+  Group g;
+  unsigned tm, tn;
+  if (block < count) {
+    const unsigned index = xcd_ordered(block, count);
+    if (!group_of_tile(full, index / ntn, &g)) return;
+    tile_of(index - g.before * ntn, g.tiles, ntn, &tm, &tn);
+    experts_tile<TL, BK_, GATED, false>(a, g, b_rows, g.lo + (int)(tm << kLog), tn);
+  } else {
+    const unsigned more = rest.all() * ntn;
+    if (block - count >= more) return;
+    const unsigned index = xcd_ordered(block - count, more);
+    if (!group_of_tile(rest, index / ntn, &g)) return;
+    tile_of(index - g.before * ntn, g.tiles, ntn, &tm, &tn);
+    const int first = g.lo + ((g.hi - g.lo) >> kLog << kLog);   // of the rows left
+    experts_tile<TR, BK_, GATED, true>(a, g, b_rows, first + (int)(tm << kRestLog), tn);
+  }
+}
+template <class TL, bool BK_, bool GATED>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_experts(GemmArgs a, Groups gr, int64_t b_rows) {
+  experts<TL, BK_, GATED>(a, gr, b_rows, blockIdx.x);
 }
 
+// The place-th largest group (the first of equals first), so that the longest
+// sums begin first; the place-th group if there are more than a wave's lanes.
+struct OneGroup {
+  int g, lo, hi;
+  TACO_DEV OneGroup(const Groups& gr, int place) {
+    if (gr.count > kWave) {
+      g = place;
+      lo = offset_at(gr, g);
+      hi = offset_at(gr, g + 1);
+      return;
+    }
+    const int lane = (int)threadIdx.x % kWave;
+    const int first = lane < gr.count ? offset_at(gr, lane) : 0, end = lane < gr.count ? offset_at(gr, lane + 1) : 0;
+    const int rows = end - first;
+    int before = 0;
+    for (int i = 0; i < gr.count; ++i) {
+      const int other = __builtin_amdgcn_readlane(rows, i);
+      before += other > rows || (other == rows && i < lane);
+    }
+    g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < gr.count && before == place));
+    lo = (int)lane_value((unsigned)first, g);
+    hi = (int)lane_value((unsigned)end, g);
+  }
+};
+
 // dw[g] = the product of dz and x over the group's rows; zeros if it has none.
+// A group's tiles take as long as it has rows, so each XCD has an eighth of
+// every group's (a range of its own, where there are enough of them).
+TACO_DEV unsigned dw_blocks(unsigned per) { return per < 2 * kXcds ? per : (per + kXcds - 1) / kXcds * kXcds; }
 template <class TL>
-__global__ __launch_bounds__(TL::kThreads, 2) void k_experts_dw(GemmArgs a, Groups gr) {
+TACO_DEV void experts_dw(const GemmArgs& a, const Groups& gr, unsigned block) {
   constexpr int BM = TL::BM, BN = TL::BN;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)((a.N + BN - 1) / BN);
-  const unsigned index = xcd_ordered(blockIdx.x, gridDim.x), per = ntm * ntn;
-  const int g = (int)(index / per), lo = offset_at(gr, g), hi = offset_at(gr, g + 1);
+  const unsigned per = ntm * ntn, blocks = dw_blocks(per), in_group = block % blocks;
+  const unsigned index = blocks == per ? in_group : in_group % kXcds * (blocks / kXcds) + in_group / kXcds;
+  if (index >= per) return;
+  const OneGroup group(gr, (int)(block / blocks));
+  const int g = group.g, lo = group.lo, hi = group.hi;
   unsigned tm, tn;
-  tile_of(index % per, ntm, ntn, &tm, &tn);
+  tile_of(index, ntm, ntn, &tm, &tn);
   Tile t;
   t.m0 = (int64_t)tm * BM;
   t.n0 = (int)tn * BN;
@@ -157,12 +234,16 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_experts_dw(GemmArgs a, Grou
   e.out.p = static_cast<char*>(e.out.p) + g * a.M * e.out.ld * (e.out.dt == kBF16 ? 2 : 4);
   sum_tile<TL, true, true, false, Bf16>(e, t);
 }
+template <class TL>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_experts_dw(GemmArgs a, Groups gr) {
+  experts_dw<TL>(a, gr, blockIdx.x);
+}
 
 // Few rows: of each group that has any, 16 * TM at a time.
 template <int TM, bool GATED>
 __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, Groups gr, int64_t b_rows) {
   const unsigned ntn = (unsigned)(a.N + a.cols - 1) / (unsigned)a.cols;
-  const GroupTiles gt(gr, 31);   // one tile to a group
+  const GroupTiles<kAllTiles> gt(gr, 31);   // one tile to a group
   const unsigned count = gt.all() * ntn;
   if (blockIdx.x >= count) return;
   const unsigned index = xcd_ordered(blockIdx.x, count);
@@ -188,11 +269,11 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, G
 
 // ------------------------------------------- backward of activations, dbias --
 
-// dz, and the sums over ranges of 32 rows of one group each.
-constexpr int kRangeLog = 5;
+// dz, and the sums over ranges of 8 rows of one group each.
+constexpr int kRangeLog = 3;
 template <bool GATED>
 __global__ __launch_bounds__(256) void k_experts_act_back(ActBackArgs a, Groups gr, unsigned slabs, unsigned bound) {
-  const GroupTiles gt(gr, kRangeLog);
+  const GroupTiles<kAllTiles> gt(gr, kRangeLog);
   const unsigned range = blockIdx.x / slabs;
   Group g;
   if (range >= bound || !group_of_tile(gt, range, &g)) return;
@@ -200,24 +281,54 @@ __global__ __launch_bounds__(256) void k_experts_act_back(ActBackArgs a, Groups 
   act_back<GATED>(a, first, end < g.hi ? end : g.hi, range, blockIdx.x % slabs);
 }
 
-// A group's sums of those, in order; zeros for a group without rows.
-__global__ __launch_bounds__(256) void k_experts_dbias(const float* partials, int N, Mat dbias, Groups gr, unsigned bound) {
-  __shared__ float sums[kSumParts * kWave];
-  const int g = (int)blockIdx.y;
-  const GroupTiles gt(gr, kRangeLog);
-  // tiles before the lane that has the group, and before it in that lane
+// Group g's sums of those, in order; zeros for a group without rows. `block`
+// takes 64 columns; `sums`: kSumParts * kWave floats of LDS.
+struct DbiasArgs {
+  const float* partials;
+  int N;
+  Mat dbias;        // p null: not wanted
+  unsigned bound;   // ranges that there is room for
+};
+template <int WAVES>
+TACO_DEV void experts_dbias(const DbiasArgs& a, const Groups& gr, unsigned block, int g, float* sums) {
+  const GroupTiles<kAllTiles> gt(gr, kRangeLog);
+  // ranges before the lane that has the group, and before it in that lane
   const int lane = g / gt.per;
   unsigned before = lane_value(gt.upto - gt.mine, lane);
   for (int i = lane * gt.per; i < g; ++i) before += gt.tiles(offset_at(gr, i), offset_at(gr, i + 1));
   const unsigned tiles = gt.tiles(offset_at(gr, g), offset_at(gr, g + 1));
   ColumnSumArgs s;
-  s.in = partials + (int64_t)before * N;
-  s.ld = N;
+  s.in = a.partials + (int64_t)before * a.N;
+  s.ld = a.N;
   s.second = 0;
-  s.count = before <= bound && tiles <= bound - before ? (int)tiles : 0;
-  s.cols = N;
-  s.out[0] = {static_cast<char*>(dbias.p) + g * dbias.ld * (dbias.dt == kBF16 ? 2 : 4), N, dbias.dt};
-  column_sum<4>(s, blockIdx.x, 0, sums);
+  s.count = before <= a.bound && tiles <= a.bound - before ? (int)tiles : 0;
+  s.cols = a.N;
+  s.out[0] = {static_cast<char*>(a.dbias.p) + g * a.dbias.ld * (a.dbias.dt == kBF16 ? 2 : 4), a.N, a.dbias.dt};
+  column_sum<WAVES>(s, block, 0, sums);
+}
+__global__ __launch_bounds__(256) void k_experts_dbias(DbiasArgs a, Groups gr) {
+  __shared__ float sums[kSumParts * kWave];
+  experts_dbias<4>(a, gr, blockIdx.x, (int)blockIdx.y, sums);
+}
+
+// All gradients in one launch: dx's `count_dx` workgroups, dw's `count_dw`, and
+// the biases'. dx's sums are the longer ones as a rule, so dw's tiles fill
+// what dx leaves of the device at its end.
+template <class TLX, class TLW>
+__global__ __launch_bounds__(TLW::kThreads, 2) void k_experts_back(GemmArgs dx, GemmArgs dw, DbiasArgs db, Groups gr,
+                                                                   int64_t b_rows, unsigned count_dx, unsigned count_dw) {
+  static_assert(TLX::kThreads == TLW::kThreads, "one launch");
+  extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
+  unsigned b = blockIdx.x;
+  if (b < count_dx) {
+    experts<TLX, true, false>(dx, gr, b_rows, b);
+  } else if ((b -= count_dx) < count_dw) {
+    experts_dw<TLW>(dw, gr, b);
+  } else {
+    b -= count_dw;
+    const unsigned slabs = (unsigned)(db.N + kWave - 1) / kWave;
+    experts_dbias<TLW::kThreads / kWave>(db, gr, b % slabs, (int)(b / slabs), reinterpret_cast<float*>(lds));
+  }
 }
 
 // ----------------------------------------------------------------- launch --
@@ -230,14 +341,31 @@ static int64_t most_tiles(const Groups& g, int log) {
 
 bool few_rows_experts(const Groups& g, int64_t, int64_t, bool) { return g.rows <= kFewRows; }
 
+// Row tiles of k_experts at most: full ones, and those of the rows left.
+template <class TL>
+static int64_t most_row_tiles(const Groups& g) {
+  using TR = typename RestOf<TL>::Type;
+  const int64_t used = std::min(g.count, g.rows);
+  return g.rows / TL::BM + std::min<int64_t>(TL::BM / TR::BM * used, most_tiles(g, log2_of(TR::BM)));
+}
+
 template <class TL>
 static void launch_experts_tiles(const GemmArgs& a, const Groups& g, int64_t b_rows, hipStream_t s) {
   const int cols = a.gated ? TL::BN / 2 : TL::BN;
-  const dim3 grid((unsigned)(most_tiles(g, log2_of(TL::BM)) * ((a.N + cols - 1) / cols))), block(TL::kThreads);
+  const dim3 grid((unsigned)(most_row_tiles<TL>(g) * ((a.N + cols - 1) / cols))), block(TL::kThreads);
   constexpr size_t lds = TL::kLdsBytes;
   if (a.b.by_k) hipLaunchKernelGGL((k_experts<TL, true, false>), grid, block, lds, s, a, g, b_rows);
   else if (a.gated) hipLaunchKernelGGL((k_experts<TL, false, true>), grid, block, lds, s, a, g, b_rows);
   else hipLaunchKernelGGL((k_experts<TL, false, false>), grid, block, lds, s, a, g, b_rows);
+}
+
+// Which tiles the rows of groups take (dx, and forward products that are not of few rows).
+enum Shape { kFlat, kTall, kSmall, kLarge };
+static Shape shape_of(const Groups& g, int64_t wide) {
+  const int64_t rows = g.rows / g.count;
+  if (rows <= 32) return kFlat;
+  if (rows <= 64) return kTall;
+  return rows >= 256 && g.rows * wide >= int64_t(192) << 16 ? kLarge : kSmall;
 }
 
 hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows, hipStream_t s) {
@@ -251,34 +379,67 @@ hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows,
     else hipLaunchKernelGGL((k_experts_few<1, false>), grid, block, 0, s, a, g, b_rows);
     return hipGetLastError();
   }
-  const int64_t rows = g.rows / g.count, cols = a.gated ? 2 * (int64_t)a.N : a.N;
-  if (rows <= 32) launch_experts_tiles<TilesFlat>(a, g, b_rows, s);
-  else if (rows <= 64) launch_experts_tiles<TilesTall>(a, g, b_rows, s);
-  else if (rows >= 256 && (int64_t)g.rows * cols >= int64_t(192) << 16) launch_experts_tiles<TilesLarge>(a, g, b_rows, s);
-  else launch_experts_tiles<TilesSmall>(a, g, b_rows, s);
+  switch (shape_of(g, a.gated ? 2 * (int64_t)a.N : a.N)) {
+    case kFlat: launch_experts_tiles<TilesFlat>(a, g, b_rows, s); break;
+    case kTall: launch_experts_tiles<TilesTall>(a, g, b_rows, s); break;
+    case kSmall: launch_experts_tiles<TilesSmall>(a, g, b_rows, s); break;
+    case kLarge: launch_experts_tiles<TilesLarge>(a, g, b_rows, s); break;
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_experts_dw(const GemmArgs& a, const Groups& g, hipStream_t s) {
-  auto launch = [&](auto tiles) {
-    using TL = decltype(tiles);
-    const int64_t per = ((a.M + TL::BM - 1) / TL::BM) * ((a.N + TL::BN - 1) / TL::BN);
-    hipLaunchKernelGGL((k_experts_dw<TL>), dim3((unsigned)(per * g.count)), dim3(TL::kThreads), TL::kLdsBytes, s, a, g);
-  };
-  const int64_t large = ((a.M + 255) / 256) * ((a.N + 255) / 256) * g.count;
-  if (large >= 192) launch(TilesLarge());
-  else launch(TilesSmall());
-  return hipGetLastError();
+// Whether dw takes large tiles: there are enough of them, and the sums are long.
+static bool dw_large(const GemmArgs& a, const Groups& g) {
+  return ((a.M + 255) / 256) * ((a.N + 255) / 256) * g.count >= 192 && g.rows / g.count >= 256;
+}
+template <class TL>
+static unsigned dw_grid(const GemmArgs& a, const Groups& g) {
+  const unsigned per = (unsigned)(((a.M + TL::BM - 1) / TL::BM) * ((a.N + TL::BN - 1) / TL::BN));
+  return (per < 2 * kXcds ? per : (per + kXcds - 1) / kXcds * kXcds) * (unsigned)g.count;   // as dw_blocks()
+}
+template <class TL>
+static void launch_dw_tiles(const GemmArgs& a, const Groups& g, hipStream_t s) {
+  hipLaunchKernelGGL((k_experts_dw<TL>), dim3(dw_grid<TL>(a, g)), dim3(TL::kThreads), TL::kLdsBytes, s, a, g);
+}
+static void launch_dbias(const DbiasArgs& a, const Groups& g, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + kWave - 1) / kWave), (unsigned)g.count);
+  hipLaunchKernelGGL(k_experts_dbias, grid, dim3(256), 0, s, a, g);
 }
 
 int64_t experts_back_ranges(const Groups& g) { return most_tiles(g, kRangeLog); }
 
-hipError_t launch_experts_act_back(const ActBackArgs& a, const Mat& dbias, const Groups& g, hipStream_t s) {
+hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStream_t s) {
   const unsigned bound = (unsigned)experts_back_ranges(g), slabs = (unsigned)((a.N + 511) / 512);
   if (bound > 0) hipLaunchKernelGGL((k_experts_act_back<false>), dim3(bound * slabs), dim3(256), 0, s, a, g, slabs, bound);
-  const dim3 grid((unsigned)((a.N + kWave - 1) / kWave), (unsigned)g.count);
-  hipLaunchKernelGGL(k_experts_dbias, grid, dim3(256), 0, s, a.partials, a.N, dbias, g, bound);
   return hipGetLastError();
+}
+
+hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* partials, int64_t N, const Mat& dbias,
+                               const Groups& g, int64_t b_rows, hipStream_t s) {
+  const DbiasArgs db = {partials, (int)N, dbias, (unsigned)experts_back_ranges(g)};
+  const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
+  if (dx && dw && (shape == kLarge) == dw_large(*dw, g)) {
+    auto launch = [&](auto tiles_dx, auto tiles_dw) {
+      using TLX = decltype(tiles_dx);
+      using TLW = decltype(tiles_dw);
+      const unsigned count_dw = dw_grid<TLW>(*dw, g);
+      const unsigned count_dx = (unsigned)(most_row_tiles<TLX>(g) * ((dx->N + TLX::BN - 1) / TLX::BN));
+      const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
+      hipLaunchKernelGGL((k_experts_back<TLX, TLW>), dim3(count_dx + count_dw + count_db), dim3(TLW::kThreads),
+                         TLW::kLdsBytes, s, *dx, *dw, db, g, b_rows, count_dx, count_dw);
+    };
+    if (shape == kFlat) launch(TilesFlat(), TilesSmall());
+    else if (shape == kTall) launch(TilesTall(), TilesSmall());
+    else if (shape == kSmall) launch(TilesSmall(), TilesSmall());
+    else launch(TilesLarge(), TilesLarge());
+    return hipGetLastError();
+  }
+  if (dbias.p) launch_dbias(db, g, s);
+  if (dw) {
+    if (dw_large(*dw, g)) launch_dw_tiles<TilesLarge>(*dw, g, s);
+    else launch_dw_tiles<TilesSmall>(*dw, g, s);
+  }
+  return dx ? launch_experts(*dx, g, b_rows, s) : hipGetLastError();
 }
 
 }  // namespace taco

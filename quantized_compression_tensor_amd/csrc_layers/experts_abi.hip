@@ -78,7 +78,7 @@ struct GroupedBackward {
     if (what != kRun) return hipSuccess;
     hipError_t err = hipSuccess;
     if (want_db) {
-      err = launch_experts_act_back(b, db.m, groups, stream);
+      err = launch_experts_act_back(b, groups, stream);
       if (err == hipSuccess && pack.count > 0) err = launch_pack(pack, stream);
     } else if (own_dz) {
       err = launch_act_back(b, pack, stream);
@@ -90,9 +90,8 @@ struct GroupedBackward {
     gx.a = dz; gx.b = ow; gx.M = m; gx.N = (int)k; gx.K = wide; gx.e.out = dx.m;
     dz.by_k = true;
     gw.a = dz; gw.b = ox; gw.M = wide; gw.N = (int)k; gw.K = m; gw.e.out = dw.m;
-    if (want_dx) err = launch_experts(gx, groups, wide, stream);
-    if (want_dw && err == hipSuccess) err = launch_experts_dw(gw, groups, stream);
-    return err;
+    return launch_experts_back(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, b.partials, n, want_db ? db.m : kAbsent,
+                               groups, wide, stream);
   }
 };
 

@@ -160,16 +160,19 @@ struct Groups {
   int count;
   int rows;
 };
-// Products by group. launch_experts: rows of a with the group's part of b
-// (`b_rows` rows of it), a.M not looked at; a.K and a.N as ever.
-// launch_experts_dw: for each group out [a.M, a.N] = the product over its rows.
+// Products by group: rows of a with the group's part of b (`b_rows` rows of it);
+// a.M is not looked at.
 hipError_t launch_experts(const GemmArgs& a, const Groups& g, int64_t b_rows, hipStream_t s);
-hipError_t launch_experts_dw(const GemmArgs& a, const Groups& g, hipStream_t s);
 // Whether the forward product takes the kernel for few rows.
 bool few_rows_experts(const Groups& g, int64_t N, int64_t K, bool gated);
-// dz of the groups' rows with the sums over each group's rows, dbias
-// [groups, N]; partials [experts_back_ranges][N].
+// dz of the groups' rows, and the sums over ranges of each group's rows:
+// partials [experts_back_ranges][N].
 int64_t experts_back_ranges(const Groups& g);
-hipError_t launch_experts_act_back(const ActBackArgs& a, const Mat& dbias, const Groups& g, hipStream_t s);
+hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStream_t s);
+// The gradients, each where it is given: dx, a product by group; dw, for each
+// group out [dw.M, dw.N] = the product over its rows; dbias [groups, N] from
+// the partials.
+hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* partials, int64_t N, const Mat& dbias,
+                               const Groups& g, int64_t b_rows, hipStream_t s);
 
 }  // namespace taco

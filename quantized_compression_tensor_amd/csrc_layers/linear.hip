@@ -484,7 +484,10 @@ struct Tile {
   int N;                        // columns of the whole output
   float* part;                  // receives the sums, null: the epilogue does
 };
-template <class TL, bool AK, bool BK_, bool GATED, class OP>
+// RAGGED: tiles that are partly empty are common, and a wave without rows or
+// columns of the output takes part in the loads alone; its SIMD's other wave
+// then has the matrix core to itself.
+template <class TL, bool AK, bool BK_, bool GATED, class OP, bool RAGGED = false>
 TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
@@ -511,6 +514,7 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
       for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
 
   const int steps = (int)((K + BK - 1) / BK);
+  const bool idle = wm * TM * 16 >= t.rows || wn * (GATED ? TN * 8 : TN * 16) >= t.cols;
   uint16_t *const lds_a = lds, *const lds_b = lds + TL::kStagesA * TL::kA;
   bf16x8 fa[TM], fb[2][TN];
   auto read_a = [&](const uint16_t* s, int kk, int i) { fa[i] = LdsTile<AK, BM>::operand(s, (wm * TM + i) * 16, kk, lane); };
@@ -539,6 +543,27 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
     load(lb, 1, b1, 0, 1);
     load(la, 2, a2, 0, 1);
     hand_over<0, 2 * LA::kPer + LB::kPer>();
+    auto next_step = [&] {
+      uint16_t* s = a0;
+      a0 = a1;
+      a1 = a2;
+      a2 = s;
+      s = b0;
+      b0 = b1;
+      b1 = s;
+    };
+    if (RAGGED && idle) {
+#pragma unroll 1
+      for (int ks = 0; ks < steps; ++ks) {
+        hand_over<0, -1>();
+        load(lb, ks + 2, b0, 0, 1);
+        hand_over<0, LA::kPer + LB::kPer>();
+        load(la, ks + 3, a0, 0, 1);
+        next_step();
+      }
+      hand_over<0, 0>();
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
     read_b(b0, 0);
@@ -571,13 +596,7 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
         if (i == kNextB) read_b(b1, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      uint16_t* s = a0;
-      a0 = a1;
-      a1 = a2;
-      a2 = s;
-      s = b0;
-      b0 = b1;
-      b1 = s;
+      next_step();
     }
   }
   hand_over<0, 0>();

@@ -14,6 +14,10 @@ def assembly(request, tmp_path_factory):
     return request.param, compiled(request.param, tmp_path_factory.mktemp("asm"))
 
 
+# Rows of a tile: the tile for the rows left by it.
+REST = {256: [128, 256, 2, 4], 128: [64, 128, 2, 2], 64: [32, 128, 2, 2], 32: [32, 128, 2, 2]}
+
+
 def check_loop(loop, tile, a_by_k, b_by_k):
     bm, bn, wgm, wgn = tile
     threads, rows, cols = 64 * wgm * wgn, bm // wgm // 16, bn // wgn // 16
@@ -50,15 +54,24 @@ def check_loop(loop, tile, a_by_k, b_by_k):
 def test_products_hand_over_what_they_count(assembly):
     source, text = assembly
     seen = 0
-    for name in ("k_int8", "k_experts", "k_experts_dw"):
+    for name in ("k_int8", "k_experts", "k_experts_dw", "k_experts_back"):
         for symbol, _ in kernels(text, name):
-            tile = [int(v) for v in re.search(r"TilesILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", symbol).groups()]
+            tiles = [[int(v) for v in t] for t in re.findall(r"ILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", symbol)]
             flags = [f == "1" for f in re.findall(r"Lb([01])E", symbol)]
-            a_by_k, b_by_k = (True, True) if name == "k_experts_dw" else (False, name == "k_experts" and flags[0])
             body = text[text.index(symbol + ":"):]
             loops = list(main_loops(body[:body.index(".Lfunc_end")].splitlines()))
-            assert len(loops) == 1, symbol
-            check_loop(loops[0], tile, a_by_k, b_by_k)
+            # dw reads both operands transposed; forward products neither
+            gradient = name == "k_experts" and flags[0]
+            dw = [name != "k_experts" and not any(i.startswith("ds_read_b128") for i in l) for l in loops]
+            rest = [REST[t[0]] if name in ("k_experts", "k_experts_back") else None for t in tiles[:1]]
+            expect = {"k_int8": 1, "k_experts_dw": 1, "k_experts": 2, "k_experts_back": 3}[name]
+            assert len(loops) == expect and sum(dw) == (name in ("k_experts_dw", "k_experts_back")), symbol
+            for loop, is_dw in zip(loops, dw):
+                # which tile it is of: full ones, those of the rows left (half as high), or dw's
+                products = sum(i.startswith("v_mfma") for i in loop)
+                choice = [tiles[-1]] if is_dw else [t for t in [tiles[0], *rest] if t and t[0] * t[1] // (t[2] * t[3]) // 128 == products]
+                assert choice, symbol
+                check_loop(loop, choice[0], is_dw, is_dw or gradient or name == "k_experts_back")
             seen += 1
     assert seen >= 4
 
