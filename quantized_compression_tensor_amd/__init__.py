@@ -156,6 +156,7 @@ def _load():
 
 
 _lib = _load()
+import torch  # noqa: E402  (loaded there)
 
 
 def lib():
@@ -493,8 +494,7 @@ def _codes(t, rows, cols, what):
     stride, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
-    import torch
-    if t.dtype != torch.int8:
+    if t.dtype is not torch.int8:
         raise TypeError(f"{what}: {t.dtype} is not int8")
     return taco_array(t.data_ptr(), stride, TACO_I8, 0)
 
@@ -558,12 +558,11 @@ def _groups_of(t, groups, rows, cols, what):
 
 
 def _offsets(t, groups):
-    import torch
     if not t.is_cuda:
         _on_gpu(t, "offsets")
     if t.shape != (groups + 1,) or not t.is_contiguous():
         raise ValueError(f"offsets: expected {groups + 1} contiguous values, got shape {tuple(t.shape)}")
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"offsets: {t.dtype} is not int32")
     return t.data_ptr()
 

@@ -108,8 +108,6 @@ constexpr int log2_of(int v) { return v <= 1 ? 0 : 1 + log2_of(v / 2); }
 // --------------------------------------------------------------- products --
 
 using TilesHalf = Tiles<128, 256, 2, 4>;
-using TilesTall = Tiles<64, 128, 2, 2>;    // few rows to a group: the weights' bytes bound it
-using TilesFlat = Tiles<32, 128, 2, 2>;
 // What takes the rows that do not fill a tile.
 template <class TL>
 struct RestOf;
@@ -122,60 +120,133 @@ struct RestOf<TilesTall> { using Type = TilesFlat; };
 template <>
 struct RestOf<TilesFlat> { using Type = TilesFlat; };
 
-// Forward products (w's k contiguous), and dx = dz w (BK_). Only as many
-// workgroups as the groups have tiles do anything: first the tiles that are
-// full, in one contiguous range for each XCD, then those of the rows left, half
-// as high, which waste less and even out the last round.
-template <class TL, bool BK_, bool GATED, bool RAGGED>
-TACO_DEV void experts_tile(const GemmArgs& a, const Group& g, int64_t b_rows, int m0, unsigned tn) {
-  constexpr int BM = TL::BM, kCols = GATED ? TL::BN / 2 : TL::BN;
-  Tile t;
-  t.m0 = m0;
-  t.n0 = (int)tn * kCols;
-  t.N = a.N;
-  t.rows = g.hi - m0 < BM ? g.hi - m0 : BM;
-  t.cols = a.N - t.n0 < kCols ? a.N - t.n0 : kCols;
-  t.K = a.K;
-  t.a = a.a.p + m0 * a.a.ld;
-  t.b = a.b.p + g.g * b_rows * a.b.ld + (BK_ ? t.n0 : t.n0 * a.b.ld);
-  t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
-  t.lda = a.a.ld;
-  t.ldb = a.b.ld;
-  t.part = nullptr;
-  Epilogue e = a.e;
-  if (!BK_ && !GATED && e.bias.p)
-    e.bias.p = static_cast<char*>(e.bias.p) + g.g * e.bias.ld * (e.bias.dt == kBF16 ? 2 : 4);
-  sum_tile<TL, false, BK_, GATED, Bf16, RAGGED>(e, t);
+// A tile of the groups' output rows: those that are full come first, then those
+// of the rows left, half as high, which waste less and even out the last round.
+struct RowTile {
+  Group g;
+  int m0;
+  unsigned tn;
+  bool full;
+};
+// Where tile `index` lies, of `full` and `rest`; false if there is none. Full
+// tiles are in one contiguous range for each XCD (index from xcd_ordered()).
+TACO_DEV bool locate(const GroupTiles<kFullTiles>& full, const GroupTiles<kRestTiles>& rest, unsigned ntn,
+                     unsigned index, RowTile* t) {
+  const unsigned count = full.all() * ntn;
+  unsigned tm;
+  t->full = index < count;
+  if (t->full) {
+    if (!group_of_tile(full, index / ntn, &t->g)) return false;
+    tile_of(index - t->g.before * ntn, t->g.tiles, ntn, &tm, &t->tn);
+    t->m0 = t->g.lo + (int)(tm << full.log);
+  } else {
+    index -= count;
+    if (!group_of_tile(rest, index / ntn, &t->g)) return false;
+    tile_of(index - t->g.before * ntn, t->g.tiles, ntn, &tm, &t->tn);
+    const int rows = t->g.hi - t->g.lo;
+    t->m0 = t->g.lo + (rows >> rest.log << rest.log) + (int)(tm << rest.rest_log);
+  }
+  return true;
 }
-template <class TL, bool BK_, bool GATED>
+
+TACO_DEV Epilogue of_group(const Epilogue& all, int g) {
+  Epilogue e = all;
+  if (e.bias.p) e.bias.p = static_cast<char*>(e.bias.p) + g * e.bias.ld * (e.bias.dt == kBF16 ? 2 : 4);
+  return e;
+}
+
+// Forward products (w's k contiguous), and dx = dz w (BK_). Only as many
+// workgroups as the groups have tiles do anything. Where tiles are few, K is
+// cut into a.parts parts of a.part, whose sums go to a.partials
+// [parts][a.rest tiles] for k_experts_join.
+template <class TL, bool BK_, bool GATED, bool RAGGED, bool DIRECT>
+TACO_DEV void experts_tile(const GemmArgs& a, const RowTile& r, int64_t b_rows, unsigned part, float* sums) {
+  constexpr int BM = TL::BM, kCols = GATED ? TL::BN / 2 : TL::BN;
+  const int64_t k0 = part * a.part;
+  Tile t;
+  t.m0 = r.m0;
+  t.n0 = (int)r.tn * kCols;
+  t.N = a.N;
+  t.rows = r.g.hi - r.m0 < BM ? r.g.hi - r.m0 : BM;
+  t.cols = a.N - t.n0 < kCols ? a.N - t.n0 : kCols;
+  t.K = a.parts > 1 && a.K - k0 > a.part ? a.part : a.K - k0;
+  t.a = a.a.p + r.m0 * a.a.ld + k0;
+  t.b = a.b.p + r.g.g * b_rows * a.b.ld + (BK_ ? t.n0 + k0 * a.b.ld : t.n0 * a.b.ld + k0);
+  t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
+  t.lda = a.a.ld * (DIRECT ? 2 : 1);
+  t.ldb = a.b.ld * (DIRECT ? 2 : 1);
+  t.part = sums;
+  sum_tile<TL, false, BK_, GATED, Bf16, RAGGED, DIRECT>(of_group(a.e, r.g.g), t);
+}
+template <class TL, bool BK_, bool GATED, bool DIRECT>
 TACO_DEV void experts(const GemmArgs& a, const Groups& gr, int64_t b_rows, unsigned block) {
   using TR = typename RestOf<TL>::Type;
   static_assert(TL::kThreads == TR::kThreads && TL::BN == TR::BN && TR::kLdsBytes <= TL::kLdsBytes, "one launch");
-  constexpr int kCols = GATED ? TL::BN / 2 : TL::BN, kLog = log2_of(TL::BM), kRestLog = log2_of(TR::BM);
+  constexpr int kCols = GATED ? TL::BN / 2 : TL::BN;
   const unsigned ntn = (unsigned)(a.N + kCols - 1) / kCols;
-  const GroupTiles<kFullTiles> full(gr, kLog, kRestLog);
-  const GroupTiles<kRestTiles> rest(gr, kLog, kRestLog);
-  const unsigned count = full.all() * ntn;
-  Group g;
-  unsigned tm, tn;
-  if (block < count) {
-    const unsigned index = xcd_ordered(block, count);
-    if (!group_of_tile(full, index / ntn, &g)) return;
-    tile_of(index - g.before * ntn, g.tiles, ntn, &tm, &tn);
-    experts_tile<TL, BK_, GATED, false>(a, g, b_rows, g.lo + (int)(tm << kLog), tn);
+  const GroupTiles<kFullTiles> full(gr, log2_of(TL::BM), log2_of(TR::BM));
+  const GroupTiles<kRestTiles> rest(gr, log2_of(TL::BM), log2_of(TR::BM));
+  // the full tiles' parts, then the others'
+  const unsigned count = full.all() * ntn, more = rest.all() * ntn;
+  unsigned tile, part = 0;
+  if (block < count * a.parts) {
+    tile = xcd_ordered(block, count * a.parts);
+    if (a.parts > 1) part = tile / count, tile %= count;
   } else {
-    const unsigned more = rest.all() * ntn;
-    if (block - count >= more) return;
-    const unsigned index = xcd_ordered(block - count, more);
-    if (!group_of_tile(rest, index / ntn, &g)) return;
-    tile_of(index - g.before * ntn, g.tiles, ntn, &tm, &tn);
-    const int first = g.lo + ((g.hi - g.lo) >> kLog << kLog);   // of the rows left
-    experts_tile<TR, BK_, GATED, true>(a, g, b_rows, first + (int)(tm << kRestLog), tn);
+    block -= count * a.parts;
+    if (block >= more * a.parts) return;
+    tile = xcd_ordered(block, more * a.parts);
+    if (a.parts > 1) part = tile / more, tile %= more;
+    tile += count;
   }
+  RowTile r;
+  if (!locate(full, rest, ntn, tile, &r)) return;
+  float* sums = nullptr;
+  if (a.parts > 1) {
+    if (tile >= a.rest) return;
+    sums = a.partials + ((int64_t)part * a.rest + tile) * (TL::BM * TL::BN);
+  }
+  if (r.full) experts_tile<TL, BK_, GATED, false, DIRECT>(a, r, b_rows, part, sums);
+  else experts_tile<TR, BK_, GATED, true, DIRECT>(a, r, b_rows, part, sums);
 }
-template <class TL, bool BK_, bool GATED>
+// DIRECT: x and w of any alignment.
+template <class TL, bool BK_, bool GATED, bool DIRECT>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_experts(GemmArgs a, Groups gr, int64_t b_rows) {
-  experts<TL, BK_, GATED>(a, gr, b_rows, blockIdx.x);
+  experts<TL, BK_, GATED, DIRECT>(a, gr, b_rows, blockIdx.x);
+}
+
+// Joins the parts of a tile's sums, in order, and finishes: a workgroup takes
+// some rows of a tile, a lane eight columns.
+template <class TL, bool GATED>
+__global__ __launch_bounds__(256) void k_experts_join(GemmArgs a, Groups gr) {
+  using TR = typename RestOf<TL>::Type;
+  constexpr int BN = TL::BN, kCols = GATED ? BN / 2 : BN, kOcts = kCols / 8, kRows = 256 / kOcts;
+  const unsigned ntn = (unsigned)(a.N + kCols - 1) / kCols;
+  const GroupTiles<kFullTiles> full(gr, log2_of(TL::BM), log2_of(TR::BM));
+  const GroupTiles<kRestTiles> rest(gr, log2_of(TL::BM), log2_of(TR::BM));
+  RowTile r;
+  if (!locate(full, rest, ntn, blockIdx.x, &r)) return;
+  const int row = (int)blockIdx.y * kRows + (int)threadIdx.x / kOcts, col = (int)threadIdx.x % kOcts * 8;
+  const int m = r.m0 + row, n = (int)r.tn * kCols + col;
+  if (row >= (r.full ? TL::BM : TR::BM) || m >= r.g.hi || n >= a.N) return;
+  float z[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = 0.0f, u[i] = 0.0f;
+  for (unsigned p = 0; p < a.parts; ++p) {
+    const float* at = a.partials + (((int64_t)p * a.rest + blockIdx.x) * TL::BM + row) * BN + col;
+    float f[8];
+    load8(at, kF32, 0, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += f[i];
+    if (GATED) {
+      load8(at, kF32, kCols, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] += f[i];
+    }
+  }
+  const Epilogue e = of_group(a.e, r.g.g);
+  if (GATED) finish_gated(e, a.N, m, n, a.N - n, z, u);
+  else finish(e, m, n, a.N - n, z);
 }
 
 // The place-th largest group (the first of equals first), so that the longest
@@ -257,8 +328,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, G
   f.cols = a.N - f.n0 < a.cols ? a.N - f.n0 : a.cols;
   f.N = a.N;
   f.b = reinterpret_cast<const char*>(a.b.p + g.g * b_rows * a.b.ld);
-  Epilogue e = a.e;
-  if (!GATED && e.bias.p) e.bias.p = static_cast<char*>(e.bias.p) + g.g * e.bias.ld * (e.bias.dt == kBF16 ? 2 : 4);
+  const Epilogue e = of_group(a.e, g.g);
   for (int m = g.lo; m < g.hi; m += 16 * TM) {
     f.m0 = m;
     f.rows = g.hi - m < 16 * TM ? g.hi - m : 16 * TM;
@@ -314,14 +384,14 @@ __global__ __launch_bounds__(256) void k_experts_dbias(DbiasArgs a, Groups gr) {
 // All gradients in one launch: dx's `count_dx` workgroups, dw's `count_dw`, and
 // the biases'. dx's sums are the longer ones as a rule, so dw's tiles fill
 // what dx leaves of the device at its end.
-template <class TLX, class TLW>
+template <class TLX, class TLW, bool DIRECT>
 __global__ __launch_bounds__(TLW::kThreads, 2) void k_experts_back(GemmArgs dx, GemmArgs dw, DbiasArgs db, Groups gr,
                                                                    int64_t b_rows, unsigned count_dx, unsigned count_dw) {
   static_assert(TLX::kThreads == TLW::kThreads, "one launch");
   extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
   unsigned b = blockIdx.x;
   if (b < count_dx) {
-    experts<TLX, true, false>(dx, gr, b_rows, b);
+    experts<TLX, true, false, DIRECT>(dx, gr, b_rows, b);
   } else if ((b -= count_dx) < count_dw) {
     experts_dw<TLW>(dw, gr, b);
   } else {
@@ -349,17 +419,8 @@ static int64_t most_row_tiles(const Groups& g) {
   return g.rows / TL::BM + std::min<int64_t>(TL::BM / TR::BM * used, most_tiles(g, log2_of(TR::BM)));
 }
 
-template <class TL>
-static void launch_experts_tiles(const GemmArgs& a, const Groups& g, int64_t b_rows, hipStream_t s) {
-  const int cols = a.gated ? TL::BN / 2 : TL::BN;
-  const dim3 grid((unsigned)(most_row_tiles<TL>(g) * ((a.N + cols - 1) / cols))), block(TL::kThreads);
-  constexpr size_t lds = TL::kLdsBytes;
-  if (a.b.by_k) hipLaunchKernelGGL((k_experts<TL, true, false>), grid, block, lds, s, a, g, b_rows);
-  else if (a.gated) hipLaunchKernelGGL((k_experts<TL, false, true>), grid, block, lds, s, a, g, b_rows);
-  else hipLaunchKernelGGL((k_experts<TL, false, false>), grid, block, lds, s, a, g, b_rows);
-}
-
 // Which tiles the rows of groups take (dx, and forward products that are not of few rows).
+constexpr int kDirectRows = 512;
 enum Shape { kFlat, kTall, kSmall, kLarge };
 static Shape shape_of(const Groups& g, int64_t wide) {
   const int64_t rows = g.rows / g.count;
@@ -368,23 +429,118 @@ static Shape shape_of(const Groups& g, int64_t wide) {
   return rows >= 256 && g.rows * wide >= int64_t(192) << 16 ? kLarge : kSmall;
 }
 
-hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows, hipStream_t s) {
+// Whether weights of another alignment are taken as they are, not copied: they
+// are read about as often as the groups' rows fill tiles.
+// (Lines below 16 bytes are not taken.)
+bool direct_experts(const Groups& g, int64_t wide) {
+  return wide >= 8 && shape_of(g, wide) != kLarge && g.rows / g.count <= kDirectRows;
+}
+
+// Calls f(tiles) with the tiles of a shape.
+template <class F>
+static void with_tiles(Shape shape, F f) {
+  switch (shape) {
+    case kFlat: f(TilesFlat()); break;
+    case kTall: f(TilesTall()); break;
+    case kSmall: f(TilesSmall()); break;
+    case kLarge: f(TilesLarge()); break;
+  }
+}
+
+// How a product by group is cut; decided by the sizes alone, so that the
+// workspace is known before the call.
+struct ExpertsPlan {
+  Shape shape;
+  int64_t tiles;        // at most
+  unsigned parts;       // of K
+  int64_t part;
+  size_t bytes;         // of partial sums
+};
+// `other`: us of the tiles of another product that run at the same time.
+static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gated, double other = 0.0) {
+  ExpertsPlan p = {shape_of(g, gated ? 2 * N : N), 0, 1, K, 0};
+  with_tiles(p.shape, [&](auto tiles) {
+    using TL = decltype(tiles);
+    const int64_t cols = gated ? TL::BN / 2 : TL::BN, ntn = (N + cols - 1) / cols, steps = (K + 63) / 64;
+    p.tiles = most_row_tiles<TL>(g) * ntn;
+    if (p.shape == kLarge) return;
+    // about as many tiles as there will be: every group with rows has some left
+    const double tiles_now = (double)((g.rows / TL::BM + std::min(g.count, g.rows)) * ntn);
+    // two tiles to a CU, a step of either 0.6 us; the parts' way through memory at 4 TB/s, and a launch
+    const double tile_us = 2.0 * TL::BM * TL::BN * sizeof(float) / 4e6, step = 0.6, launch = 4.0;
+    double least = 0.0;
+    for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
+      const int64_t per = (steps + parts - 1) / parts;
+      const double all = (tiles_now * (double)steps * step + other) / (2 * 256.0);
+      const double t = std::max(all, (double)per * step) + (parts > 1 ? launch + tiles_now * (double)parts * tile_us : 0.0);
+      if (parts == 1 || t < least) {
+        least = t;
+        p.parts = (unsigned)((steps + per - 1) / per);
+        p.part = per * 64;
+      }
+    }
+    if (p.parts > 1) p.bytes = (size_t)p.tiles * p.parts * TL::BM * TL::BN * sizeof(float);
+  });
+  return p;
+}
+static void set_experts_plan(GemmArgs* a, const ExpertsPlan& p, void* partials) {
+  a->parts = p.parts;
+  a->part = p.part;
+  a->rest = (unsigned)p.tiles;
+  a->partials = static_cast<float*>(partials);
+}
+size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated) {
+  return g.rows == 0 ? 0 : experts_plan(g, N, K, gated).bytes;
+}
+
+// dx beside dw [wide, N] of every group, whose small tiles take about 5 us
+// besides their steps.
+static ExpertsPlan dx_plan(const Groups& g, int64_t N, int64_t wide) {
+  const double steps = (double)(g.rows / g.count) / 64.0;
+  return experts_plan(g, N, wide, false,
+                      (double)(((wide + 127) / 128) * ((N + 127) / 128) * g.count) * (5.0 + 0.6 * steps));
+}
+size_t experts_back_bytes(const Groups& g, int64_t N, int64_t wide) {
+  return g.rows == 0 ? 0 : std::max(experts_plan(g, N, wide, false).bytes, dx_plan(g, N, wide).bytes);
+}
+
+template <class TL>
+static void launch_experts_join(const GemmArgs& a, const Groups& g, hipStream_t s) {
+  if (a.parts <= 1) return;
+  const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
+  const dim3 grid(a.rest, (unsigned)((TL::BM + rows - 1) / rows));
+  if (a.gated) hipLaunchKernelGGL((k_experts_join<TL, true>), grid, dim3(256), 0, s, a, g);
+  else hipLaunchKernelGGL((k_experts_join<TL, false>), grid, dim3(256), 0, s, a, g);
+}
+
+hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows, void* partials, hipStream_t s) {
   if (g.rows == 0) return hipSuccess;
   GemmArgs a = args;
   if (!a.b.by_k && few_rows_experts(g, a.N, a.K, a.gated)) {
     a.cols = a.gated ? 8 : 16;
     const dim3 grid((unsigned)((a.N + a.cols - 1) / a.cols) * (unsigned)std::min(g.count, g.rows));
     const dim3 block(kFewWaves * kWave);
-    if (a.gated) hipLaunchKernelGGL((k_experts_few<1, true>), grid, block, 0, s, a, g, b_rows);
-    else hipLaunchKernelGGL((k_experts_few<1, false>), grid, block, 0, s, a, g, b_rows);
+    if (a.gated) hipLaunchKernelGGL((k_experts_few<1, true>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
+    else hipLaunchKernelGGL((k_experts_few<1, false>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
     return hipGetLastError();
   }
-  switch (shape_of(g, a.gated ? 2 * (int64_t)a.N : a.N)) {
-    case kFlat: launch_experts_tiles<TilesFlat>(a, g, b_rows, s); break;
-    case kTall: launch_experts_tiles<TilesTall>(a, g, b_rows, s); break;
-    case kSmall: launch_experts_tiles<TilesSmall>(a, g, b_rows, s); break;
-    case kLarge: launch_experts_tiles<TilesLarge>(a, g, b_rows, s); break;
-  }
+  const ExpertsPlan p = experts_plan(g, a.N, a.K, a.gated);
+  set_experts_plan(&a, p, partials);
+  with_tiles(p.shape, [&](auto tiles) {
+    using TL = decltype(tiles);
+    auto launch = [&](auto direct) {
+      const dim3 grid((unsigned)p.tiles * p.parts), block(TL::kThreads);
+      constexpr size_t lds = direct() ? TL::kDirectLdsBytes : TL::kLdsBytes;
+      if (a.b.by_k) hipLaunchKernelGGL((k_experts<TL, true, false, direct()>), grid, block, lds, s, a, g, b_rows);
+      else if (a.gated) hipLaunchKernelGGL((k_experts<TL, false, true, direct()>), grid, block, lds, s, a, g, b_rows);
+      else hipLaunchKernelGGL((k_experts<TL, false, false, direct()>), grid, block, lds, s, a, g, b_rows);
+    };
+    if constexpr (TL::BM < TilesLarge::BM) {
+      if (a.direct) return launch(std::true_type()), launch_experts_join<TL>(a, g, s);
+    }
+    launch(std::false_type());
+    launch_experts_join<TL>(a, g, s);
+  });
   return hipGetLastError();
 }
 
@@ -414,32 +570,38 @@ hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* partials, int64_t N, const Mat& dbias,
-                               const Groups& g, int64_t b_rows, hipStream_t s) {
-  const DbiasArgs db = {partials, (int)N, dbias, (unsigned)experts_back_ranges(g)};
+hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* sums, int64_t N, const Mat& dbias,
+                               const Groups& g, int64_t b_rows, void* partials, hipStream_t s) {
+  const DbiasArgs db = {sums, (int)N, dbias, (unsigned)experts_back_ranges(g)};
+  const bool large_dw = dw && dw_large(*dw, g);
   const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
-  if (dx && dw && (shape == kLarge) == dw_large(*dw, g)) {
-    auto launch = [&](auto tiles_dx, auto tiles_dw) {
-      using TLX = decltype(tiles_dx);
-      using TLW = decltype(tiles_dw);
-      const unsigned count_dw = dw_grid<TLW>(*dw, g);
-      const unsigned count_dx = (unsigned)(most_row_tiles<TLX>(g) * ((dx->N + TLX::BN - 1) / TLX::BN));
-      const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
-      hipLaunchKernelGGL((k_experts_back<TLX, TLW>), dim3(count_dx + count_dw + count_db), dim3(TLW::kThreads),
-                         TLW::kLdsBytes, s, *dx, *dw, db, g, b_rows, count_dx, count_dw);
-    };
-    if (shape == kFlat) launch(TilesFlat(), TilesSmall());
-    else if (shape == kTall) launch(TilesTall(), TilesSmall());
-    else if (shape == kSmall) launch(TilesSmall(), TilesSmall());
-    else launch(TilesLarge(), TilesLarge());
+  if (dx && dw && (shape == kLarge) == large_dw) {
+    GemmArgs x = *dx;
+    const ExpertsPlan p = dx_plan(g, x.N, x.K);
+    set_experts_plan(&x, p, partials);
+    with_tiles(shape, [&](auto tiles) {
+      using TLX = decltype(tiles);
+      using TLW = std::conditional_t<TLX::BM == TilesLarge::BM, TilesLarge, TilesSmall>;
+      auto launch = [&](auto direct) {
+        const unsigned count_dw = dw_grid<TLW>(*dw, g), count_dx = (unsigned)p.tiles * p.parts;
+        const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
+        hipLaunchKernelGGL((k_experts_back<TLX, TLW, direct()>), dim3(count_dx + count_dw + count_db),
+                           dim3(TLW::kThreads), TLW::kLdsBytes, s, x, *dw, db, g, b_rows, count_dx, count_dw);
+      };
+      if constexpr (TLX::BM < TilesLarge::BM) {
+        if (x.direct) return launch(std::true_type()), launch_experts_join<TLX>(x, g, s);
+      }
+      launch(std::false_type());
+      launch_experts_join<TLX>(x, g, s);
+    });
     return hipGetLastError();
   }
   if (dbias.p) launch_dbias(db, g, s);
   if (dw) {
-    if (dw_large(*dw, g)) launch_dw_tiles<TilesLarge>(*dw, g, s);
+    if (large_dw) launch_dw_tiles<TilesLarge>(*dw, g, s);
     else launch_dw_tiles<TilesSmall>(*dw, g, s);
   }
-  return dx ? launch_experts(*dx, g, b_rows, s) : hipGetLastError();
+  return dx ? launch_experts(*dx, g, b_rows, partials, s) : hipGetLastError();
 }
 
 }  // namespace taco

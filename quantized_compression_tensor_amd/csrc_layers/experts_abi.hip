@@ -35,18 +35,20 @@ struct GroupedForward {
   hipError_t pass(Pass what, Space* space, hipStream_t stream) const {
     const bool worst = what == kSizeOfAny;
     const int64_t wide = gated ? 2 * n : n;
-    const bool few = few_rows_experts(groups, n, k, gated);
+    const bool any = few_rows_experts(groups, n, k, gated) || direct_experts(groups, wide);   // as they are
     PackArgs pack = {};
     GemmArgs g = {};
-    g.a = packed(x.m, m, k, false, few || (!worst && in_place(x.m, k)), space, &pack);
-    g.b = packed(w.m, groups.count * wide, k, false, few || (!worst && in_place(w.m, k)), space, &pack);
+    g.a = packed(x.m, m, k, false, any || (!worst && in_place(x.m, k)), space, &pack);
+    g.b = packed(w.m, groups.count * wide, k, false, any || (!worst && in_place(w.m, k)), space, &pack);
+    g.direct = any && !(in_place(x.m, k) && in_place(w.m, k));
     g.M = m; g.N = (int)n; g.K = k; g.gated = gated; g.e = e;
+    void* partials = space->take(few_rows_experts(groups, n, k, gated) ? 0 : experts_partial_bytes(groups, n, k, gated));
     if (what != kRun) return hipSuccess;
     if (pack.count > 0) {
       const hipError_t err = launch_pack(pack, stream);
       if (err != hipSuccess) return err;
     }
-    return launch_experts(g, groups, wide, stream);
+    return launch_experts(g, groups, wide, partials, stream);
   }
 };
 
@@ -73,8 +75,10 @@ struct GroupedBackward {
     }
     Operand ox = {}, ow = {};
     if (want_dw) ox = packed(x.m, m, k, true, !worst && in_place(x.m, k), space, &pack);
-    if (want_dx) ow = packed(w.m, groups.count * wide, k, true, !worst && in_place(w.m, k), space, &pack);
+    const bool direct = direct_experts(groups, k);
+    if (want_dx) ow = packed(w.m, groups.count * wide, k, true, direct || (!worst && in_place(w.m, k)), space, &pack);
     if (want_db) b.partials = static_cast<float*>(space->take((size_t)(experts_back_ranges(groups) * n) * sizeof(float)));
+    void* partials = space->take(want_dx ? experts_back_bytes(groups, k, wide) : 0);
     if (what != kRun) return hipSuccess;
     hipError_t err = hipSuccess;
     if (want_db) {
@@ -88,10 +92,11 @@ struct GroupedBackward {
     if (err != hipSuccess) return err;
     GemmArgs gx = {}, gw = {};
     gx.a = dz; gx.b = ow; gx.M = m; gx.N = (int)k; gx.K = wide; gx.e.out = dx.m;
+    gx.direct = direct && !in_place(w.m, k);
     dz.by_k = true;
     gw.a = dz; gw.b = ox; gw.M = wide; gw.N = (int)k; gw.K = m; gw.e.out = dw.m;
     return launch_experts_back(want_dx ? &gx : nullptr, want_dw ? &gw : nullptr, b.partials, n, want_db ? db.m : kAbsent,
-                               groups, wide, stream);
+                               groups, wide, partials, stream);
   }
 };
 

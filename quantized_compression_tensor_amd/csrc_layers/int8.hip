@@ -17,43 +17,83 @@ namespace taco {
 
 // --------------------------------------------------------------- products --
 
-template <class TL, bool GATED>
+// DIRECT: x and w of any alignment.
+template <class TL, bool GATED, bool DIRECT>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_int8(GemmArgs a) {
-  gemm<TL, false, false, GATED, Int8>(a, blockIdx.x);
+  gemm<TL, false, false, GATED, Int8, DIRECT>(a, blockIdx.x);
 }
 
-template <class TL, bool GATED>
+template <class TL, bool GATED, bool DIRECT>
 static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_int8<TL, GATED>), dim3(a.whole + a.rest * a.parts), dim3(TL::kThreads), TL::kLdsBytes, s, a);
+  constexpr size_t lds = DIRECT ? TL::kDirectLdsBytes : TL::kLdsBytes;
+  hipLaunchKernelGGL((k_int8<TL, GATED, DIRECT>), dim3(a.whole + a.rest * a.parts), dim3(TL::kThreads), lds, s, a);
   if (a.rest == 0) return;
   const int octs = (GATED ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
   hipLaunchKernelGGL((k_join<TL, GATED, Int8>), dim3(a.rest, (unsigned)(TL::BM / rows)), dim3(256), 0, s, a);
 }
 
+// Products of up to kDirectRows rows: read every weight once or twice, from where
+// it lies.
+constexpr int kDirectRows = 256;
+bool direct_int8(int64_t M) { return M <= kDirectRows; }
+
+struct Int8Plan {
+  int height;               // of a tile
+  unsigned tiles, parts;    // parts of K
+  int64_t part;             // pairs of codes
+};
+static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
+  Int8Plan p;
+  p.height = M <= TilesFlat::BM ? TilesFlat::BM : M <= TilesTall::BM ? TilesTall::BM : TilesSmall::BM;
+  const int64_t cols = gated ? 64 : 128, steps = (K + 127) / 128;
+  p.tiles = (unsigned)((M + p.height - 1) / p.height * ((N + cols - 1) / cols));
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps / 4, 16})), per = (steps + parts - 1) / parts;
+  p.parts = (unsigned)((steps + per - 1) / per);
+  p.part = per * 64;
+  return p;
+}
+size_t direct_int8_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  const Int8Plan p = int8_plan(M, N, K, gated);
+  return p.parts == 1 ? 0 : (size_t)p.tiles * p.parts * p.height * 128 * sizeof(float);
+}
+
 bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated) {
   const int64_t weights = (gated ? 2 : 1) * N * K;
-  return M <= 4 || (M <= kFewRows && weights * M <= int64_t(1) << 30);
+  return M <= 4 || (M <= 64 && weights * M <= int64_t(1) << 30);
 }
 
 hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s) {
   if (few_rows_int8(a.M, a.N, a.K, a.gated)) {
     const dim3 grid(set_few_columns(&a)), block(kFewWaves * kWave);
-    if (a.M <= 16) {
-      if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true, Int8>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((k_few_rows<1, false, Int8>), grid, block, 0, s, a);
-    } else {
-      if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true, Int8>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((k_few_rows<2, false, Int8>), grid, block, 0, s, a);
-    }
+    auto few = [&](auto tiles) {
+      constexpr int TM = tiles();
+      if (a.gated) hipLaunchKernelGGL((k_few_rows<TM, true, Int8>), grid, block, few_lds_bytes<TM>(), s, a);
+      else hipLaunchKernelGGL((k_few_rows<TM, false, Int8>), grid, block, few_lds_bytes<TM>(), s, a);
+    };
+    if (a.M <= 16) few(std::integral_constant<int, 1>());
+    else if (a.M <= 32) few(std::integral_constant<int, 2>());
+    else few(std::integral_constant<int, 4>());
     return hipGetLastError();
   }
-  const bool large = set_gemm_plan(&a, partials);
-  if (a.gated) {
-    if (large) launch_tiles_int8<TilesLarge, true>(a, s);
-    else launch_tiles_int8<TilesSmall, true>(a, s);
+  auto launch = [&](auto tiles, auto direct) {
+    using TL = decltype(tiles);
+    if (a.gated) launch_tiles_int8<TL, true, direct()>(a, s);
+    else launch_tiles_int8<TL, false, direct()>(a, s);
+  };
+  if (a.direct) {
+    const Int8Plan p = int8_plan(a.M, a.N, a.K, a.gated);
+    a.whole = p.parts == 1 ? p.tiles : 0;
+    a.rest = p.tiles - a.whole;
+    a.parts = p.parts;
+    a.part = p.part;
+    a.partials = static_cast<float*>(partials);
+    if (p.height == TilesFlat::BM) launch(TilesFlat(), std::true_type());
+    else if (p.height == TilesTall::BM) launch(TilesTall(), std::true_type());
+    else launch(TilesSmall(), std::true_type());
+  } else if (set_gemm_plan(&a, partials)) {
+    launch(TilesLarge(), std::false_type());
   } else {
-    if (large) launch_tiles_int8<TilesLarge, false>(a, s);
-    else launch_tiles_int8<TilesSmall, false>(a, s);
+    launch(TilesSmall(), std::false_type());
   }
   return hipGetLastError();
 }
@@ -68,7 +108,7 @@ __global__ __launch_bounds__(256) void k_pack_int8(PackArgs a) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t row = total <= UINT32_MAX ? (uint32_t)i / (uint32_t)parts : i / parts;
     const int64_t c = (i - row * parts) * 16, left = m.cols - c;
-    const u32x4 v = few_load<Int8>(static_cast<const char*>(m.src.p) + row * m.src.ld + c, left < 16 ? (int)left : 16);
+    const u32x4 v = load_part<Int8>(static_cast<const char*>(m.src.p) + row * m.src.ld + c, left < 16 ? (int)left : 16);
     *reinterpret_cast<u32x4*>(reinterpret_cast<char*>(m.dst) + row * m.ld + c) = v;
   }
 }

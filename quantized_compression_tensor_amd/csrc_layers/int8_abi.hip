@@ -34,11 +34,14 @@ struct Int8Call {
     const bool worst = what == kSizeOfAny;
     GemmArgs g = {};
     g.M = m; g.N = (int)n; g.gated = gated; g.e = e;
-    if (few_rows_int8(m, n, k, gated)) {
+    const bool few = few_rows_int8(m, n, k, gated);
+    if (few || direct_int8(m)) {
       g.K = k;
       g.a = Operand{static_cast<const uint16_t*>(x.m.p), x.m.ld, false};
       g.b = Operand{static_cast<const uint16_t*>(w.m.p), w.m.ld, false};
-      return what == kRun ? launch_gemm_int8(g, nullptr, stream) : hipSuccess;
+      g.direct = !few;
+      void* partials = space->take(few ? 0 : direct_int8_bytes(m, n, k, gated));
+      return what == kRun ? launch_gemm_int8(g, partials, stream) : hipSuccess;
     }
     PackArgs pack = {};
     g.K = up(k, 16) / 2;

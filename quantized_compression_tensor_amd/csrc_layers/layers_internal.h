@@ -102,6 +102,7 @@ struct GemmArgs {
   int64_t part;
   float* partials;
   int cols;   // output columns of a workgroup, for few rows
+  bool direct;   // a and b may start and end anywhere (by group and of codes only)
 };
 
 // dz = dout * act'(z) (gated: both halves), and the column sums of dz.
@@ -150,6 +151,10 @@ hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
 // few rows, else in pairs of them (lines of whole 16 bytes, zeros past the
 // last k). launch_pack_int8: copies of such lines; here all sizes in elements.
 bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated);
+// Whether operands are taken as they are (GemmArgs::direct, ld and K in
+// elements), and the bytes of partial sums that it needs then.
+bool direct_int8(int64_t M);
+size_t direct_int8_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_pack_int8(const PackArgs& a, hipStream_t s);
 hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s);
 
@@ -161,18 +166,23 @@ struct Groups {
   int rows;
 };
 // Products by group: rows of a with the group's part of b (`b_rows` rows of it);
-// a.M is not looked at.
-hipError_t launch_experts(const GemmArgs& a, const Groups& g, int64_t b_rows, hipStream_t s);
+// a.M is not looked at. partials: experts_partial_bytes.
+size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated);
+hipError_t launch_experts(const GemmArgs& a, const Groups& g, int64_t b_rows, void* partials, hipStream_t s);
 // Whether the forward product takes the kernel for few rows.
 bool few_rows_experts(const Groups& g, int64_t N, int64_t K, bool gated);
+// Whether a product by group with `wide` rows of weights or columns of dx takes
+// operands as they are (GemmArgs::direct), where they are not aligned.
+bool direct_experts(const Groups& g, int64_t wide);
 // dz of the groups' rows, and the sums over ranges of each group's rows:
 // partials [experts_back_ranges][N].
 int64_t experts_back_ranges(const Groups& g);
 hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStream_t s);
 // The gradients, each where it is given: dx, a product by group; dw, for each
 // group out [dw.M, dw.N] = the product over its rows; dbias [groups, N] from
-// the partials.
-hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* partials, int64_t N, const Mat& dbias,
-                               const Groups& g, int64_t b_rows, hipStream_t s);
+// the ranges' sums. partials: experts_back_bytes, where dx is given.
+size_t experts_back_bytes(const Groups& g, int64_t N, int64_t wide);
+hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* sums, int64_t N, const Mat& dbias,
+                               const Groups& g, int64_t b_rows, void* partials, hipStream_t s);
 
 }  // namespace taco

@@ -278,10 +278,13 @@ struct Tiles {
   static constexpr int kFreeB = TM / 2, kFreeA = TM / 4;
   static constexpr int kTurnLd = TN * 16 + 4, kTurnMost = TM < 2 ? 16 : 32;   // the epilogue's turn: floats of a row, rows at most
   static constexpr int kLdsBytes = (kStagesA * kA + kStagesB * kB) * 2;
-  static_assert(WGM * WGN * kTurnMost * kTurnLd * 4 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
+  static constexpr int kDirectLdsBytes = 2 * (kA + kB) * 2;      // two stages of either
+  static_assert(WGM * WGN * kTurnMost * kTurnLd * 4 <= kDirectLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
 using TilesLarge = Tiles<256, 256, 2, 4>;
 using TilesSmall = Tiles<128, 128, 2, 2>;
+using TilesTall = Tiles<64, 128, 2, 2>;    // few rows to a group: the weights' bytes bound it
+using TilesFlat = Tiles<32, 128, 2, 2>;
 constexpr int kGroupM = 8;   // tile rows walked together (their b rows are shared through L2)
 
 // An LDS read that transposes (see LdsTile::operand). The pointer is marked
@@ -423,6 +426,79 @@ struct Loader : Chunks<BY_K, R, NT, GATED> {
   }
 };
 
+// 16 bytes of a row of 16-bit elements or bytes, of which `n` exist (zeros past them).
+template <class OP>
+TACO_DEV u32x4 load_part(const char* p, int n) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if constexpr (OP::kScaled) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (2 * i < n) v[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
+  }
+  return v;
+}
+
+// Moves an operand's tiles by way of the registers, from rows that may start
+// anywhere. For weights that a product reads once or twice, which a copy to
+// aligned rows would read and write once more. Lines that do not exist repeat
+// the last one, columns that do not exist are whatever follows (their sums are
+// not stored); what lies past the last k is zero. `ld` in bytes, at least 16
+// (BY_K).
+// A step that has all of its k loads without a condition, so that the compiler
+// can count what is under way; the last one may need load_last.
+template <bool BY_K, int R, int NT, bool GATED, class OP>
+struct DirectLoader : Chunks<BY_K, R, NT, GATED> {
+  using C = Chunks<BY_K, R, NT, GATED>;
+  static constexpr int kBytes = OP::kScaled ? 1 : 2;   // of an element
+  static_assert(!BY_K || kBytes == 2, "only 16-bit elements can be transposed");
+  const char *p, *p2;
+  int64_t step;       // bytes from one step to the next
+  int64_t end;        // bytes of K (k contiguous), of the whole tile (BY_K)
+  int off[C::kPer];
+  int have;           // bytes of a line (BY_K)
+  // Steps that load() can take, of K in elements.
+  static TACO_DEV int full_steps(int64_t K) { return (int)(BY_K ? (K - 1) / 64 : K * kBytes / 128); }
+  TACO_DEV void init(const uint16_t* base, const uint16_t* base2, int64_t ld, int rows, int64_t K, int tid) {
+    p = reinterpret_cast<const char*>(base);
+    p2 = reinterpret_cast<const char*>(base2);
+    step = BY_K ? 64 * ld : 128;
+    have = 2 * rows;
+    end = BY_K ? (K - 1) * ld + have : K * kBytes;
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) {
+      const int l = C::line(tid, i), c = 16 * C::chunk(tid, i);
+      if (BY_K) off[i] = l * (int)ld + (c < have ? c : 0);
+      else off[i] = (C::row(l) < rows ? C::row(l) : rows - 1) * (int)ld + c;
+    }
+  }
+  TACO_DEV void load(int ks, int wave, u32x4 (&r)[C::kPer]) const {
+    const int64_t at = ks * step;
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) __builtin_memcpy(&r[i], (C::second(wave, i) ? p2 : p) + at + off[i], 16);
+  }
+  TACO_DEV void load_last(int ks, int64_t K, int tid, int wave, u32x4 (&r)[C::kPer]) const {
+    const int64_t at = ks * step;
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) {
+      const int c = 16 * C::chunk(tid, i);
+      int64_t n;   // bytes that may be read, and are not past the last k
+      if (BY_K) n = ks * 64 + C::line(tid, i) >= K ? 0 : at + off[i] + 16 <= end ? 16 : have - c;
+      else n = end - at - c;
+      r[i] = load_part<OP>((C::second(wave, i) ? p2 : p) + at + off[i], n >= 16 ? 16 : n > 0 ? (int)n : 0);
+    }
+  }
+  static TACO_DEV void store(uint16_t* t, int tid, const u32x4 (&r)[C::kPer]) {
+#pragma unroll
+    for (int i = 0; i < C::kPer; ++i) *reinterpret_cast<u32x4*>(t + (i * NT + tid) * 8) = r[i];
+  }
+};
+
 // Output tile of this workgroup: each XCD walks one contiguous range of tiles
 // (xcd_ordered_block() for any index of any count), and inside it groups of
 // kGroupM tile rows column by column, so the workgroups resident on an XCD share
@@ -476,7 +552,7 @@ TACO_DEV void hand_over() {
 // tile on a CU, were no faster, so a longer reach ahead is not what is missing.
 struct Tile {
   const uint16_t *a, *b, *b2;   // the operands' first elements (b2: the other projection's)
-  int64_t lda, ldb;
+  int64_t lda, ldb;             // in 16-bit elements, as K (DIRECT: lda and ldb in bytes, K in elements)
   int64_t K;                    // of this part
   int64_t m0;                   // first row and column of the output
   int n0;
@@ -487,7 +563,9 @@ struct Tile {
 // RAGGED: tiles that are partly empty are common, and a wave without rows or
 // columns of the output takes part in the loads alone; its SIMD's other wave
 // then has the matrix core to itself.
-template <class TL, bool AK, bool BK_, bool GATED, class OP, bool RAGGED = false>
+// DIRECT: the operands' rows may start anywhere, and take the way through the
+// registers: two steps on their way there, and two stages of LDS.
+template <class TL, bool AK, bool BK_, bool GATED, class OP, bool RAGGED = false, bool DIRECT = false>
 TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
@@ -499,8 +577,8 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
   const bool whole = t.part == nullptr;
   const int64_t m0 = t.m0, K = t.K;
   const int n0 = t.n0;
-  using LA = Loader<AK, BM, NT, false>;
-  using LB = Loader<BK_, BN, NT, GATED>;
+  using LA = std::conditional_t<DIRECT, DirectLoader<AK, BM, NT, false, OP>, Loader<AK, BM, NT, false>>;
+  using LB = std::conditional_t<DIRECT, DirectLoader<BK_, BN, NT, GATED, OP>, Loader<BK_, BN, NT, GATED>>;
   LA la;
   LB lb;
   la.init(t.a, t.a, t.lda, t.rows, K, tid);
@@ -513,7 +591,8 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][j][q] = 0;
 
-  const int steps = (int)((K + BK - 1) / BK);
+  constexpr int kStep = DIRECT && OP::kScaled ? 2 * BK : BK;   // k of a step
+  const int steps = (int)((K + kStep - 1) / kStep);
   const bool idle = wm * TM * 16 >= t.rows || wn * (GATED ? TN * 8 : TN * 16) >= t.cols;
   uint16_t *const lds_a = lds, *const lds_b = lds + TL::kStagesA * TL::kA;
   bf16x8 fa[TM], fb[2][TN];
@@ -526,77 +605,133 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = OP::product(fa[i], fb[kk][j], acc[i][j]);
   };
-  // Part `part` of `parts` of the loads of step ks into stage s.
-  auto load = [&](auto& l, int ks, uint16_t* s, int part, int parts) {
-    constexpr int kPer = std::remove_reference_t<decltype(l)>::kPer;
-    const int each = (kPer + parts - 1) / parts;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i / each == part) l.issue(s, wave, K - (int64_t)ks * BK, i);
-  };
-  if (steps > 0) {
-    uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
-    uint16_t *b0 = lds_b, *b1 = lds_b + TL::kB;
-    load(la, 0, a0, 0, 1);
-    load(lb, 0, b0, 0, 1);
-    load(la, 1, a1, 0, 1);
-    load(lb, 1, b1, 0, 1);
-    load(la, 2, a2, 0, 1);
-    hand_over<0, 2 * LA::kPer + LB::kPer>();
-    auto next_step = [&] {
-      uint16_t* s = a0;
-      a0 = a1;
-      a1 = a2;
-      a2 = s;
-      s = b0;
-      b0 = b1;
-      b1 = s;
+  if constexpr (DIRECT) {
+    // The last step comes first if not all of its k exist in both operands.
+    u32x4 ra[2][LA::kPer], rb[2][LB::kPer];
+    const int full = LA::full_steps(K) < LB::full_steps(K) ? LA::full_steps(K) : LB::full_steps(K);
+    auto fetch = [&](int ks, int set) {
+      ks = ks < full ? ks : full - 1;
+      la.load(ks, wave, ra[set]);
+      lb.load(ks, wave, rb[set]);
     };
-    if (RAGGED && idle) {
+    auto put = [&](int set) {   // into the stages of that number
+      LA::store(lds_a + set * TL::kA, tid, ra[set]);
+      LB::store(lds_a + 2 * TL::kA + set * TL::kB, tid, rb[set]);
+    };
+    auto products = [&](int set) {
+      if (RAGGED && idle) return;
+      const uint16_t *sa = lds_a + set * TL::kA, *sb = lds_a + 2 * TL::kA + set * TL::kB;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        read_b(sb, kk);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          read_a(sa, kk, i);
+          multiply(kk, i);
+        }
+      }
+    };
+    const int last = steps - full;   // 0 or 1
+    if (last > 0) {
+      la.load_last(full, K, tid, wave, ra[0]);
+      lb.load_last(full, K, tid, wave, rb[0]);
+    }
+    if (full == 0) {
+      put(0);
+      hand_over<0, -1>();
+      products(0);
+    } else {
+      if (last == 0) fetch(0, 0);
+      fetch(1 - last, 1);
+      put(0);
+      fetch(2 - last, 0);
+      // a step whose operands lie in the stages `set`: puts the next one into the
+      // others, which were read to their end before the barrier
+      auto step = [&](int ks, int set) {
+        hand_over<0, -1>();
+        put(1 - set);
+        fetch(ks + 3 - last, 1 - set);
+        products(set);
+      };
+#pragma unroll 1
+      for (int ks = 0; ks < steps; ks += 2) {
+        step(ks, 0);
+        if (ks + 1 < steps) step(ks + 1, 1);
+      }
+    }
+  } else {
+    // Part `part` of `parts` of the loads of step ks into stage s.
+    auto load = [&](auto& l, int ks, uint16_t* s, int part, int parts) {
+      constexpr int kPer = std::remove_reference_t<decltype(l)>::kPer;
+      const int each = (kPer + parts - 1) / parts;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i / each == part) l.issue(s, wave, K - (int64_t)ks * BK, i);
+    };
+    if (steps > 0) {
+      uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
+      uint16_t *b0 = lds_b, *b1 = lds_b + TL::kB;
+      load(la, 0, a0, 0, 1);
+      load(lb, 0, b0, 0, 1);
+      load(la, 1, a1, 0, 1);
+      load(lb, 1, b1, 0, 1);
+      load(la, 2, a2, 0, 1);
+      hand_over<0, 2 * LA::kPer + LB::kPer>();
+      auto next_step = [&] {
+        uint16_t* s = a0;
+        a0 = a1;
+        a1 = a2;
+        a2 = s;
+        s = b0;
+        b0 = b1;
+        b1 = s;
+      };
+      if (RAGGED && idle) {
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks) {
+          hand_over<0, -1>();
+          load(lb, ks + 2, b0, 0, 1);
+          hand_over<0, LA::kPer + LB::kPer>();
+          load(la, ks + 3, a0, 0, 1);
+          next_step();
+        }
+        hand_over<0, 0>();
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
+      read_b(b0, 0);
+      constexpr int kFreeA = TL::kFreeA, kFreeB = TL::kFreeB, kNextB = kFreeA + 1 < TM ? kFreeA + 1 : kFreeA;
 #pragma unroll 1
       for (int ks = 0; ks < steps; ++ks) {
-        hand_over<0, -1>();
-        load(lb, ks + 2, b0, 0, 1);
-        hand_over<0, LA::kPer + LB::kPer>();
-        load(la, ks + 3, a0, 0, 1);
+        read_b(b0, 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          // b0 has been read to its end: the reads since are those of kFreeB operands of a
+          if (i == kFreeB) hand_over<kFreeB * (AK ? 2 : 1), -1>();
+          if (i >= kFreeB) load(lb, ks + 2, b0, i - kFreeB, TM - kFreeB);
+          multiply(0, i);
+          read_a(a0, 1, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          if (i == kFreeA) {
+            // a0 has been read to its end, a1 and b1 are there; past the last
+            // step what is read from them is not used
+            hand_over<0, LA::kPer + LB::kPer>();
+#pragma unroll
+            for (int q = 0; q < i; ++q) read_a(a1, 0, q);
+          }
+          if (i >= kFreeA) load(la, ks + 3, a0, i - kFreeA, TM - kFreeA);
+          multiply(1, i);
+          if (i >= kFreeA) read_a(a1, 0, i);
+          if (i == kNextB) read_b(b1, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
         next_step();
       }
-      hand_over<0, 0>();
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) read_a(a0, 0, i);
-    read_b(b0, 0);
-    constexpr int kFreeA = TL::kFreeA, kFreeB = TL::kFreeB, kNextB = kFreeA + 1 < TM ? kFreeA + 1 : kFreeA;
-#pragma unroll 1
-    for (int ks = 0; ks < steps; ++ks) {
-      read_b(b0, 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        // b0 has been read to its end: the reads since are those of kFreeB operands of a
-        if (i == kFreeB) hand_over<kFreeB * (AK ? 2 : 1), -1>();
-        if (i >= kFreeB) load(lb, ks + 2, b0, i - kFreeB, TM - kFreeB);
-        multiply(0, i);
-        read_a(a0, 1, i);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        if (i == kFreeA) {
-          // a0 has been read to its end, a1 and b1 are there; past the last
-          // step what is read from them is not used
-          hand_over<0, LA::kPer + LB::kPer>();
-#pragma unroll
-          for (int q = 0; q < i; ++q) read_a(a1, 0, q);
-        }
-        if (i >= kFreeA) load(la, ks + 3, a0, i - kFreeA, TM - kFreeA);
-        multiply(1, i);
-        if (i >= kFreeA) read_a(a1, 0, i);
-        if (i == kNextB) read_b(b1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      next_step();
     }
   }
   hand_over<0, 0>();
@@ -711,11 +846,14 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
 }
 
 
-// `block` of the product's a.whole + a.rest * a.parts.
-template <class TL, bool AK, bool BK_, bool GATED, class OP>
+// `block` of the product's a.whole + a.rest * a.parts. DIRECT: K and ld of the
+// operands in elements, k contiguous.
+template <class TL, bool AK, bool BK_, bool GATED, class OP, bool DIRECT = false>
 TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   constexpr int BM = TL::BM, BN = TL::BN;
   constexpr int kCols = GATED ? BN / 2 : BN;
+  // elements of K to a 16-bit one of a.part, bytes of an element's stride
+  constexpr int kEach = DIRECT && OP::kScaled ? 2 : 1, kBytes = OP::kScaled ? 1 : 2;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)(a.N + kCols - 1) / kCols;
   // the tiles with all of K, then the parts of the others, each in its own order
   const bool whole = block < a.whole;
@@ -729,15 +867,27 @@ TACO_DEV void gemm(const GemmArgs& a, unsigned block) {
   t.N = a.N;
   t.rows = (int)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
   t.cols = a.N - t.n0 < kCols ? a.N - t.n0 : kCols;
-  const int64_t k0 = part * a.part;
-  t.K = whole || a.K - k0 < a.part ? a.K - k0 : a.part;
-  t.a = a.a.p + (AK ? t.m0 + k0 * a.a.ld : t.m0 * a.a.ld + k0);
-  t.b = a.b.p + (BK_ ? t.n0 + k0 * a.b.ld : t.n0 * a.b.ld + k0);
-  t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
-  t.lda = a.a.ld;
-  t.ldb = a.b.ld;
+  const int64_t k0 = part * a.part * kEach;
+  t.K = whole || a.K - k0 < a.part * kEach ? a.K - k0 : a.part * kEach;
+  if constexpr (DIRECT) {
+    static_assert(!AK && !BK_, "k contiguous");
+    t.lda = a.a.ld * kBytes;
+    t.ldb = a.b.ld * kBytes;
+    auto at = [&](const uint16_t* p, int64_t line, int64_t ld) {
+      return reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(p) + line * ld + k0 * kBytes);
+    };
+    t.a = at(a.a.p, t.m0, t.lda);
+    t.b = at(a.b.p, t.n0, t.ldb);
+    t.b2 = GATED ? at(a.b.p, (int64_t)a.N + t.n0, t.ldb) : t.b;
+  } else {
+    t.a = a.a.p + (AK ? t.m0 + k0 * a.a.ld : t.m0 * a.a.ld + k0);
+    t.b = a.b.p + (BK_ ? t.n0 + k0 * a.b.ld : t.n0 * a.b.ld + k0);
+    t.b2 = GATED ? t.b + (int64_t)a.N * a.b.ld : t.b;
+    t.lda = a.a.ld;
+    t.ldb = a.b.ld;
+  }
   t.part = whole ? nullptr : a.partials + (int64_t)index * BM * BN;
-  sum_tile<TL, AK, BK_, GATED, OP>(a.e, t);
+  sum_tile<TL, AK, BK_, GATED, OP, DIRECT, DIRECT>(a.e, t);
 }
 
 template <class TL, bool AK, bool BK_, bool GATED>
@@ -836,30 +986,16 @@ struct FewRows {
   int rows, n0, cols, N;
 };
 
-// 16 bytes of a row of 16-bit elements or bytes, of which `n` exist (zeros past them).
-template <class OP>
-TACO_DEV u32x4 few_load(const char* p, int n) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (n >= 16) {
-    __builtin_memcpy(&v, p, 16);
-  } else if constexpr (OP::kScaled) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) v[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (2 * i < n) v[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
-  }
-  return v;
-}
+template <int TM>
+constexpr size_t few_lds_bytes() { return sizeof(float) * (kFewWaves * TM * 4 * kWave + 16 * TM * 16); }
 
 template <int TM, bool GATED, class OP>
 TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
-  constexpr int kUnits = 2;    // of a wave, loaded together
-  constexpr int kUnit = 128;   // bytes of a row
-  __shared__ float parts[kFewWaves][TM][4 * kWave];
-  __shared__ float sums[16 * TM][16];
+  constexpr int kUnits = TM > 2 ? 1 : 2;   // of a wave, loaded together
+  constexpr int kUnit = 128;               // bytes of a row
+  extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
+  float(*parts)[TM][4 * kWave] = reinterpret_cast<float(*)[TM][4 * kWave]>(lds);
+  float(*sums)[16] = reinterpret_cast<float(*)[16]>(reinterpret_cast<float*>(lds) + kFewWaves * TM * 4 * kWave);
   const int tid = (int)threadIdx.x, lane = tid & (kWave - 1), wave = wave_in_group();
   const int r = lane & 15;
   int n = GATED ? r & 7 : r;   // lanes past the last column repeat it
@@ -909,9 +1045,9 @@ TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
     for (int64_t k = kUnit * (int64_t)units; k < f.K; k += kUnit / 2) {
       const int64_t left = f.K - k - 16 * (lane >> 4);
       const int count = left > 16 ? 16 : left > 0 ? (int)left : 0;
-      const u32x4 w = few_load<OP>(pw + k, count);
+      const u32x4 w = load_part<OP>(pw + k, count);
 #pragma unroll
-      for (int t = 0; t < TM; ++t) product(w, few_load<OP>(px[t] + k, count), t);
+      for (int t = 0; t < TM; ++t) product(w, load_part<OP>(px[t] + k, count), t);
     }
   }
   // accumulator q of lane l holds weight row 4 (l / 16) + q, row l % 16 of x
@@ -1240,11 +1376,11 @@ unsigned set_few_columns(GemmArgs* a) {
 static void launch_few_rows(GemmArgs a, hipStream_t s) {
   const dim3 grid(set_few_columns(&a)), block(kFewWaves * kWave);
   if (a.M <= 16) {
-    if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true, Bf16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_few_rows<1, false, Bf16>), grid, block, 0, s, a);
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<1, true, Bf16>), grid, block, few_lds_bytes<1>(), s, a);
+    else hipLaunchKernelGGL((k_few_rows<1, false, Bf16>), grid, block, few_lds_bytes<1>(), s, a);
   } else {
-    if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true, Bf16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_few_rows<2, false, Bf16>), grid, block, 0, s, a);
+    if (a.gated) hipLaunchKernelGGL((k_few_rows<2, true, Bf16>), grid, block, few_lds_bytes<2>(), s, a);
+    else hipLaunchKernelGGL((k_few_rows<2, false, Bf16>), grid, block, few_lds_bytes<2>(), s, a);
   }
 }
 
