@@ -311,7 +311,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_experts_dw(GemmArgs a, Grou
 }
 
 // Few rows: of each group that has any, 16 * TM at a time.
-template <int TM, bool GATED>
+template <int TM, bool GATED, bool ANY>
 __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, Groups gr, int64_t b_rows) {
   const unsigned ntn = (unsigned)(a.N + a.cols - 1) / (unsigned)a.cols;
   const GroupTiles<kAllTiles> gt(gr, 31);   // one tile to a group
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, G
     f.m0 = m;
     f.rows = g.hi - m < 16 * TM ? g.hi - m : 16 * TM;
     f.a = reinterpret_cast<const char*>(a.a.p + m * a.a.ld);
-    few_rows_product<TM, GATED, Bf16>(e, f);
+    few_rows_product<TM, GATED, Bf16, ANY>(e, f);
   }
 }
 
@@ -520,8 +520,13 @@ hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows,
     a.cols = a.gated ? 8 : 16;
     const dim3 grid((unsigned)((a.N + a.cols - 1) / a.cols) * (unsigned)std::min(g.count, g.rows));
     const dim3 block(kFewWaves * kWave);
-    if (a.gated) hipLaunchKernelGGL((k_experts_few<1, true>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
-    else hipLaunchKernelGGL((k_experts_few<1, false>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
+    auto few = [&](auto any) {
+      constexpr bool ANY = any();
+      if (a.gated) hipLaunchKernelGGL((k_experts_few<1, true, ANY>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
+      else hipLaunchKernelGGL((k_experts_few<1, false, ANY>), grid, block, few_lds_bytes<1>(), s, a, g, b_rows);
+    };
+    if (on_dwords(a.a.p, 2 * a.a.ld) && on_dwords(a.b.p, 2 * a.b.ld)) few(std::false_type());
+    else few(std::true_type());
     return hipGetLastError();
   }
   const ExpertsPlan p = experts_plan(g, a.N, a.K, a.gated);

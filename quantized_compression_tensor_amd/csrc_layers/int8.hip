@@ -32,47 +32,70 @@ static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((k_join<TL, GATED, Int8>), dim3(a.rest, (unsigned)(TL::BM / rows)), dim3(256), 0, s, a);
 }
 
-// Products of up to kDirectRows rows: read every weight once or twice, from where
-// it lies.
-constexpr int kDirectRows = 256;
-bool direct_int8(int64_t M) { return M <= kDirectRows; }
-
+// Products whose operands are not aligned take them from where they lie
+// (DIRECT), in tiles of 32 or 64 rows, or copies of them in the other tiles,
+// whichever a model of either's time says is less. In us: a step of the direct
+// tiles, of which a CU holds one or two; parts of K, as in linear.hip's plan; a
+// copy at 4 TB/s and its launch. 100 rows, 3 bytes off, by 4096 x 4096 19.4 us,
+// copied 22.1; 200 by 8192 x 1024 12.5 and 19.2; 200 by 4096 x 4096 25.5 and
+// 24.4; 300 by 1000 x 1280 13.3 and 14.7.
 struct Int8Plan {
   int height;               // of a tile
   unsigned tiles, parts;    // parts of K
   int64_t part;             // pairs of codes
+  double us;
 };
 static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
-  Int8Plan p;
-  p.height = M <= TilesFlat::BM ? TilesFlat::BM : M <= TilesTall::BM ? TilesTall::BM : TilesSmall::BM;
+  Int8Plan p = {M <= TilesFlat::BM ? TilesFlat::BM : TilesTall::BM, 0, 1, 0, 0.0};
   const int64_t cols = gated ? 64 : 128, steps = (K + 127) / 128;
-  p.tiles = (unsigned)((M + p.height - 1) / p.height * ((N + cols - 1) / cols));
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({512 / p.tiles, steps / 4, 16})), per = (steps + parts - 1) / parts;
-  p.parts = (unsigned)((steps + per - 1) / per);
-  p.part = per * 64;
+  const int64_t tiles = (M + p.height - 1) / p.height * ((N + cols - 1) / cols);
+  const double step = 0.85, part_us = 2.0 * p.height * 128 * sizeof(float) / 4e6;
+  for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
+    const int64_t per = (steps + parts - 1) / parts;
+    const double rounds = std::max(1.0, (double)(tiles * parts) / 384.0);
+    const double us = rounds * (double)per * step + (parts > 1 ? 5.0 + (double)(tiles * parts) * part_us : 0.0);
+    if (parts == 1 || us < p.us) {
+      p.parts = (unsigned)((steps + per - 1) / per);
+      p.part = per * 64;
+      p.us = us;
+    }
+  }
+  p.tiles = (unsigned)tiles;
   return p;
+}
+bool direct_int8(int64_t M, int64_t N, int64_t K, bool gated) {
+  if (M > 1024) return false;
+  const double copy = 3.5 + 2.0 * (double)((M + (gated ? 2 * N : N)) * K) / 4e6;
+  return int8_plan(M, N, K, gated).us < copy + gemm_plan_us(M, N, (K + 1) / 2, gated);
 }
 size_t direct_int8_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
   const Int8Plan p = int8_plan(M, N, K, gated);
-  return p.parts == 1 ? 0 : (size_t)p.tiles * p.parts * p.height * 128 * sizeof(float);
+  return p.parts == 1 ? 0 : (size_t)p.tiles * p.parts * (size_t)p.height * 128 * sizeof(float);
 }
 
+// As few_rows(), for rows of half the bytes: 48 rows by 4096 x 4096 11.8 us, in
+// tiles 13.8; 64 by 8192 x 1024 8.5 and 11.2; but 64 by 1248 x 6912 17.2 and 13.8.
 bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated) {
   const int64_t weights = (gated ? 2 : 1) * N * K;
   return M <= 4 || (M <= 64 && weights * M <= int64_t(1) << 30);
 }
 
-hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s) {
-  if (few_rows_int8(a.M, a.N, a.K, a.gated)) {
+hipError_t launch_gemm_int8(Int8Kernel kernel, GemmArgs a, void* partials, hipStream_t s) {
+  if (kernel == kInt8Few) {
     const dim3 grid(set_few_columns(&a)), block(kFewWaves * kWave);
-    auto few = [&](auto tiles) {
+    auto few = [&](auto tiles, auto any) {
       constexpr int TM = tiles();
-      if (a.gated) hipLaunchKernelGGL((k_few_rows<TM, true, Int8>), grid, block, few_lds_bytes<TM>(), s, a);
-      else hipLaunchKernelGGL((k_few_rows<TM, false, Int8>), grid, block, few_lds_bytes<TM>(), s, a);
+      constexpr bool ANY = any();
+      if (a.gated) hipLaunchKernelGGL((k_few_rows<TM, true, Int8, ANY>), grid, block, few_lds_bytes<TM>(), s, a);
+      else hipLaunchKernelGGL((k_few_rows<TM, false, Int8, ANY>), grid, block, few_lds_bytes<TM>(), s, a);
     };
-    if (a.M <= 16) few(std::integral_constant<int, 1>());
-    else if (a.M <= 32) few(std::integral_constant<int, 2>());
-    else few(std::integral_constant<int, 4>());
+    auto with = [&](auto any) {
+      if (a.M <= 16) few(std::integral_constant<int, 1>(), any);
+      else if (a.M <= 32) few(std::integral_constant<int, 2>(), any);
+      else few(std::integral_constant<int, 4>(), any);
+    };
+    if (on_dwords(a.a.p, a.a.ld) && on_dwords(a.b.p, a.b.ld)) with(std::false_type());
+    else with(std::true_type());
     return hipGetLastError();
   }
   auto launch = [&](auto tiles, auto direct) {
@@ -80,7 +103,7 @@ hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s) {
     if (a.gated) launch_tiles_int8<TL, true, direct()>(a, s);
     else launch_tiles_int8<TL, false, direct()>(a, s);
   };
-  if (a.direct) {
+  if (kernel == kInt8Direct) {
     const Int8Plan p = int8_plan(a.M, a.N, a.K, a.gated);
     a.whole = p.parts == 1 ? p.tiles : 0;
     a.rest = p.tiles - a.whole;
@@ -88,8 +111,7 @@ hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s) {
     a.part = p.part;
     a.partials = static_cast<float*>(partials);
     if (p.height == TilesFlat::BM) launch(TilesFlat(), std::true_type());
-    else if (p.height == TilesTall::BM) launch(TilesTall(), std::true_type());
-    else launch(TilesSmall(), std::true_type());
+    else launch(TilesTall(), std::true_type());
   } else if (set_gemm_plan(&a, partials)) {
     launch(TilesLarge(), std::false_type());
   } else {

@@ -34,14 +34,17 @@ struct Int8Call {
     const bool worst = what == kSizeOfAny;
     GemmArgs g = {};
     g.M = m; g.N = (int)n; g.gated = gated; g.e = e;
-    const bool few = few_rows_int8(m, n, k, gated);
-    if (few || direct_int8(m)) {
+    const bool few = few_rows_int8(m, n, k, gated), direct = !few && direct_int8(m, n, k, gated);
+    const bool aligned = !worst && codes_in_place(x.m, k) && codes_in_place(w.m, k);
+    if (few || (direct && !aligned)) {
       g.K = k;
       g.a = Operand{static_cast<const uint16_t*>(x.m.p), x.m.ld, false};
       g.b = Operand{static_cast<const uint16_t*>(w.m.p), w.m.ld, false};
-      g.direct = !few;
-      void* partials = space->take(few ? 0 : direct_int8_bytes(m, n, k, gated));
-      return what == kRun ? launch_gemm_int8(g, partials, stream) : hipSuccess;
+      // (arrays of any alignment: aligned ones, too)
+      const size_t own = direct ? direct_int8_bytes(m, n, k, gated) : 0;
+      const size_t tiles = worst && !few ? gemm_partial_bytes(m, n, up(k, 16) / 2, gated) : 0;
+      void* partials = space->take(std::max(own, tiles));
+      return what == kRun ? launch_gemm_int8(few ? kInt8Few : kInt8Direct, g, partials, stream) : hipSuccess;
     }
     PackArgs pack = {};
     g.K = up(k, 16) / 2;
@@ -53,7 +56,7 @@ struct Int8Call {
       const hipError_t err = launch_pack_int8(pack, stream);
       if (err != hipSuccess) return err;
     }
-    return launch_gemm_int8(g, partials, stream);
+    return launch_gemm_int8(kInt8Tiles, g, partials, stream);
   }
 };
 

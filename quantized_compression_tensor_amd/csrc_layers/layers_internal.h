@@ -102,7 +102,7 @@ struct GemmArgs {
   int64_t part;
   float* partials;
   int cols;   // output columns of a workgroup, for few rows
-  bool direct;   // a and b may start and end anywhere (by group and of codes only)
+  bool direct;   // a and b may start and end anywhere (products by group only)
 };
 
 // dz = dout * act'(z) (gated: both halves), and the column sums of dz.
@@ -127,6 +127,8 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated);
 // Bytes of partial sums that a product of this size takes (0: K is not cut).
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_gemm(GemmArgs a, void* partials, hipStream_t s);
+// The time of a product that its plan goes by, without its launch and epilogue.
+double gemm_plan_us(int64_t M, int64_t N, int64_t K, bool gated);
 // Fills in the plan of a product; whether its tiles are the large ones.
 bool set_gemm_plan(GemmArgs* a, void* partials);
 // Fills in the columns of a workgroup of the kernel for few rows; its grid.
@@ -148,15 +150,17 @@ struct QuantizeArgs {
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
 
 // Forward products of codes of 8 bits: in GemmArgs, ld and K in elements for
-// few rows, else in pairs of them (lines of whole 16 bytes, zeros past the
-// last k). launch_pack_int8: copies of such lines; here all sizes in elements.
+// few rows and direct ones, else in pairs of them (lines of whole 16 bytes,
+// zeros past the last k). launch_pack_int8: copies of such lines; here all
+// sizes in elements.
+enum Int8Kernel { kInt8Few, kInt8Direct, kInt8Tiles };
 bool few_rows_int8(int64_t M, int64_t N, int64_t K, bool gated);
-// Whether operands are taken as they are (GemmArgs::direct, ld and K in
-// elements), and the bytes of partial sums that it needs then.
-bool direct_int8(int64_t M);
+// Whether operands that are not aligned are taken as they are (kInt8Direct), and
+// the bytes of partial sums that it needs then.
+bool direct_int8(int64_t M, int64_t N, int64_t K, bool gated);
 size_t direct_int8_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_pack_int8(const PackArgs& a, hipStream_t s);
-hipError_t launch_gemm_int8(GemmArgs a, void* partials, hipStream_t s);
+hipError_t launch_gemm_int8(Int8Kernel kernel, GemmArgs a, void* partials, hipStream_t s);
 
 // Rows offsets[g] ... offsets[g + 1] of a matrix of `rows` rows are group g's;
 // `count` groups. An offset outside of [0, rows] counts as its nearer end.

@@ -444,6 +444,30 @@ TACO_DEV u32x4 load_part(const char* p, int n) {
   return v;
 }
 
+// 16 bytes from an address of any alignment, as whole dwords: where lanes read
+// many rows at a time, a load from within dwords takes several times as long (48
+// rows of codes 3 bytes off by 4096 x 4096: 26.7 us, so 14.0, with rows on
+// dwords 11.0). The dwords read are those that hold one of the 16 bytes. (The
+// tiles' loads, of 128 bytes of a row by eight lanes, are not faster for it:
+// 256 rows over 8 experts of 2 x 2816 x 4097 143 us, so 158.)
+TACO_DEV u32x4 load16_any(const char* p) {
+  typedef unsigned dwords __attribute__((ext_vector_type(4), aligned(4)));
+  const unsigned in = (unsigned)reinterpret_cast<uintptr_t>(p) & 3u;
+  const dwords v = *reinterpret_cast<const dwords*>(p - in);
+  const unsigned more = *reinterpret_cast<const unsigned*>(p + (in ? 16 - (int)in : 12));
+  return u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], in), __builtin_amdgcn_alignbyte(v[2], v[1], in),
+               __builtin_amdgcn_alignbyte(v[3], v[2], in), __builtin_amdgcn_alignbyte(more, v[3], in)};
+}
+// The same where ANY, else from an address on a dword.
+template <bool ANY>
+TACO_DEV u32x4 load16(const char* p) {
+  if constexpr (ANY) return load16_any(p);
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+inline bool on_dwords(const void* p, int64_t ld_bytes) { return (reinterpret_cast<uintptr_t>(p) | (uintptr_t)ld_bytes) % 4 == 0; }
+
 // Moves an operand's tiles by way of the registers, from rows that may start
 // anywhere. For weights that a product reads once or twice, which a copy to
 // aligned rows would read and write once more. Lines that do not exist repeat
@@ -989,7 +1013,8 @@ struct FewRows {
 template <int TM>
 constexpr size_t few_lds_bytes() { return sizeof(float) * (kFewWaves * TM * 4 * kWave + 16 * TM * 16); }
 
-template <int TM, bool GATED, class OP>
+// ANY: rows that start within dwords.
+template <int TM, bool GATED, class OP, bool ANY>
 TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
   constexpr int kUnits = TM > 2 ? 1 : 2;   // of a wave, loaded together
   constexpr int kUnit = 128;               // bytes of a row
@@ -1025,11 +1050,11 @@ TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
       for (int h = 0; h < 2; ++h) {
         const int64_t at = kUnit * (int64_t)unit + kUnit / 2 * h;
         w[u][h] = u32x4{0u, 0u, 0u, 0u};
-        if (unit < units) __builtin_memcpy(&w[u][h], pw + at, 16);
+        if (unit < units) w[u][h] = load16<ANY>(pw + at);
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
           x[u][t][h] = u32x4{0u, 0u, 0u, 0u};
-          if (unit < units) __builtin_memcpy(&x[u][t][h], px[t] + at, 16);
+          if (unit < units) x[u][t][h] = load16<ANY>(px[t] + at);
         }
       }
     }
@@ -1093,7 +1118,7 @@ TACO_DEV void few_rows_product(const Epilogue& e, const FewRows& f) {
   else finish(e, f.m0 + m, f.n0 + c, count, z);
 }
 
-template <int TM, bool GATED, class OP>
+template <int TM, bool GATED, class OP, bool ANY = false>
 __global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
   constexpr int kBytes = OP::kScaled ? 1 : 2;   // of an element
   FewRows f;
@@ -1107,7 +1132,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_few_rows(GemmArgs a) {
   f.n0 = (int)blockIdx.x * a.cols;
   f.cols = a.N - f.n0 < a.cols ? a.N - f.n0 : a.cols;
   f.N = a.N;
-  few_rows_product<TM, GATED, OP>(a.e, f);
+  few_rows_product<TM, GATED, OP, ANY>(a.e, f);
 }
 
 // ----------------------------------------------------------------- packing --
@@ -1265,6 +1290,7 @@ struct Plan {
   bool large;
   unsigned whole, rest, parts;
   int64_t part;
+  double us;   // of the model
 };
 
 constexpr int kCus = 256;   // of an MI355X; not asked of the device, so that sizes alone decide a workspace
@@ -1294,9 +1320,11 @@ static Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int64_t other =
     const double t = busy * step + (p > 1 ? launch + round * (double)(rest * p) / (double)kCus : 0.0);
     if (p == 1 || t < least) parts = p, least = t;
   }
-  if (parts <= 1) return Plan{is_large, (unsigned)tiles, 0, 1, 0};
+  const double rounds = (double)(tiles / kCus * steps) * step;
+  if (parts <= 1) return Plan{is_large, (unsigned)tiles, 0, 1, 0, rounds + least};
   const int64_t per = (steps + parts - 1) / parts;
-  return Plan{is_large, (unsigned)(tiles - rest), (unsigned)rest, (unsigned)((steps + per - 1) / per), per * 64};
+  return Plan{is_large, (unsigned)(tiles - rest), (unsigned)rest, (unsigned)((steps + per - 1) / per), per * 64,
+              rounds + least};
 }
 
 static size_t partial_bytes(const Plan& p) {
@@ -1383,6 +1411,8 @@ static void launch_few_rows(GemmArgs a, hipStream_t s) {
     else hipLaunchKernelGGL((k_few_rows<2, false, Bf16>), grid, block, few_lds_bytes<2>(), s, a);
   }
 }
+
+double gemm_plan_us(int64_t M, int64_t N, int64_t K, bool gated) { return plan_of(M, N, K, gated).us; }
 
 bool set_gemm_plan(GemmArgs* a, void* partials) {
   const Plan p = plan_of(a->M, a->N, a->K, a->gated);

@@ -50,8 +50,8 @@ def linear(gated=False, M=4, N=16, K=24, x=None, xs=at(5), w=None, ws=at(6), bia
     (INVALID, dict(x=NONE)), (INVALID, dict(w=NONE)), (INVALID, dict(out=NONE)), (INVALID, dict(xs=None)),
     (INVALID, dict(ws=None)), (ALIGN, dict(xs=at(5) + 2)), (ALIGN, dict(ws=at(6) + 1)), (ALIGN, dict(out=arr(2, 16, B, 1))),
     (INVALID, dict(out=arr(0, 24))), (INVALID, dict(out=arr(5, 16))), (INVALID, dict(out=arr(6, 16, F, 60))),
-    (WORKSPACE, dict(M=300, space=None)), (WORKSPACE, dict(M=300, bytes_=100)), (WORKSPACE, dict(M=300, space=at(9) + 8)),
-    (INVALID, dict(M=300, out=arr(9, 16))), (INVALID, dict(M=300, space=at(0))), (INVALID, dict(M=300, space=at(5))),
+    (WORKSPACE, dict(M=2000, space=None)), (WORKSPACE, dict(M=2000, bytes_=100)), (WORKSPACE, dict(M=2000, space=at(9) + 8)),
+    (INVALID, dict(M=2000, out=arr(9, 16))), (INVALID, dict(M=2000, space=at(0))), (INVALID, dict(M=2000, space=at(5))),
 ])
 def test_int8_refusals(gated, want, kw):
     assert linear(gated, **kw) == want
@@ -147,7 +147,7 @@ def test_workspaces():
         size = getattr(T, f"taco_{n}_workspace_bytes")
         for refused in ((-1, 8, 8), (8, 0, 8), (8, 8, 0), (8, 8, 131072)):
             assert size(*refused) == 0
-        assert size(1, 4096, 4096) == 0 and size(300, 20, 20) > 0
+        assert size(1, 4096, 4096) == 0 and size(2000, 20, 20) > 0
 
 
 def fake(shape, where, dtype=torch.bfloat16):

@@ -168,6 +168,26 @@ def test_large_tiles(size):
     assert torch.equal(half.t.double(), z[:, :N // 2].clamp(min=0) * z[:, N // 2:])
 
 
+# about where rows stop being few: the same sizes in rows of codes and of pairs
+# of them, copied, and where they lie
+@pytest.mark.parametrize("pad", [0, 16, 3])
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 4096), (64, 4096, 4112), (64, 4096, 8192), (33, 8192, 4096), (5, 16384, 16384)])
+def test_where_rows_stop_being_few(M, N, K, pad):
+    gen = generator(M + N + K)
+    x, w = codes(gen, M, K, 3, pad), codes(gen, N, K, 3, pad)
+    xs, ws = powers(gen, M), powers(gen, N)
+    out, half = Out(M, N, F), Out(M, N // 2, F)
+    T.taco_linear_int8(x, xs, w, ws, out.t, workspace=space(T.taco_linear_int8_workspace_bytes(M, N, K)))
+    T.taco_gated_linear_int8(x, xs, w, ws, half.t, act=NONE, workspace=space(T.taco_gated_linear_int8_workspace_bytes(M, N // 2, K)))
+    torch.cuda.synchronize()
+    out.check("out")
+    half.check("gated")
+    z = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    assert torch.equal(out.t.double(), z)
+    want = z[:, :N // 2] * z[:, N // 2:]
+    within(half.t, want, U32 * want.abs(), "gated")
+
+
 @pytest.mark.parametrize("M,N", [(1, 16), (3, 40), (130, 260)])
 def test_largest_sums(M, N):
     """-128 times -128 over the longest K: 131071 * 2^14, the largest sum that 32
