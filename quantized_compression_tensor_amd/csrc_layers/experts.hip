@@ -278,7 +278,7 @@ struct OneGroup {
 // A group's tiles take as long as it has rows, so each XCD has an eighth of
 // every group's (a range of its own, where there are enough of them).
 TACO_DEV unsigned dw_blocks(unsigned per) { return per < 2 * kXcds ? per : (per + kXcds - 1) / kXcds * kXcds; }
-template <class TL>
+template <class TL, bool SINGLE = false>
 TACO_DEV void experts_dw(const GemmArgs& a, const Groups& gr, unsigned block) {
   constexpr int BM = TL::BM, BN = TL::BN;
   const unsigned ntm = (unsigned)((a.M + BM - 1) / BM), ntn = (unsigned)((a.N + BN - 1) / BN);
@@ -303,11 +303,16 @@ TACO_DEV void experts_dw(const GemmArgs& a, const Groups& gr, unsigned block) {
   t.part = nullptr;
   Epilogue e = a.e;
   e.out.p = static_cast<char*>(e.out.p) + g * a.M * e.out.ld * (e.out.dt == kBF16 ? 2 : 4);
-  sum_tile<TL, true, true, false, Bf16>(e, t);
+  sum_tile<TL, true, true, false, Bf16, SINGLE, false, SINGLE>(e, t);
 }
 template <class TL>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_experts_dw(GemmArgs a, Groups gr) {
   experts_dw<TL>(a, gr, blockIdx.x);
+}
+// Sums of few rows: a tile's time is that of its loads, one after the other, and
+// of its stores, so four workgroups share a CU.
+__global__ __launch_bounds__(TilesSmall::kThreads, 4) void k_experts_dw_short(GemmArgs a, Groups gr) {
+  experts_dw<TilesSmall, true>(a, gr, blockIdx.x);
 }
 
 // Few rows: of each group that has any, 16 * TM at a time.
@@ -558,6 +563,13 @@ static unsigned dw_grid(const GemmArgs& a, const Groups& g) {
   const unsigned per = (unsigned)(((a.M + TL::BM - 1) / TL::BM) * ((a.N + TL::BN - 1) / TL::BN));
   return (per < 2 * kXcds ? per : (per + kXcds - 1) / kXcds * kXcds) * (unsigned)g.count;   // as dw_blocks()
 }
+// Whether dw takes the kernel for short sums, in a launch of its own: sums of
+// about two steps at most, and many tiles (64 groups of 2048 x 2048: 512 rows in
+// all 324 to 241 us, 8192 rows 447 to 369; but 32 of 512 x 1024, 1024 tiles, 33 to
+// 40, and 8 of 3552 x 2248, 4032 tiles, 105 to 121: nothing runs beside it).
+static bool dw_short(const GemmArgs& a, const Groups& g) {
+  return g.rows / g.count <= 128 && ((a.M + 127) / 128) * ((a.N + 127) / 128) * g.count >= 8192;
+}
 template <class TL>
 static void launch_dw_tiles(const GemmArgs& a, const Groups& g, hipStream_t s) {
   hipLaunchKernelGGL((k_experts_dw<TL>), dim3(dw_grid<TL>(a, g)), dim3(TL::kThreads), TL::kLdsBytes, s, a, g);
@@ -580,7 +592,8 @@ hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const flo
   const DbiasArgs db = {sums, (int)N, dbias, (unsigned)experts_back_ranges(g)};
   const bool large_dw = dw && dw_large(*dw, g);
   const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
-  if (dx && dw && (shape == kLarge) == large_dw) {
+  const bool short_dw = dw && !large_dw && dw_short(*dw, g);
+  if (dx && dw && !short_dw && (shape == kLarge) == large_dw) {
     GemmArgs x = *dx;
     const ExpertsPlan p = dx_plan(g, x.N, x.K);
     set_experts_plan(&x, p, partials);
@@ -604,6 +617,9 @@ hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const flo
   if (dbias.p) launch_dbias(db, g, s);
   if (dw) {
     if (large_dw) launch_dw_tiles<TilesLarge>(*dw, g, s);
+    else if (short_dw)
+      hipLaunchKernelGGL(k_experts_dw_short, dim3(dw_grid<TilesSmall>(*dw, g)), dim3(TilesSmall::kThreads),
+                         TilesSmall::kSingleLdsBytes, s, *dw, g);
     else launch_dw_tiles<TilesSmall>(*dw, g, s);
   }
   return dx ? launch_experts(*dx, g, b_rows, partials, s) : hipGetLastError();

@@ -279,7 +279,9 @@ struct Tiles {
   static constexpr int kTurnLd = TN * 16 + 4, kTurnMost = TM < 2 ? 16 : 32;   // the epilogue's turn: floats of a row, rows at most
   static constexpr int kLdsBytes = (kStagesA * kA + kStagesB * kB) * 2;
   static constexpr int kDirectLdsBytes = 2 * (kA + kB) * 2;      // two stages of either
-  static_assert(WGM * WGN * kTurnMost * kTurnLd * 4 <= kDirectLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
+  static constexpr int kTurnBytes = WGM * WGN * kTurnMost * kTurnLd * 4;
+  static constexpr int kSingleLdsBytes = kTurnBytes > (kA + kB) * 2 ? kTurnBytes : (kA + kB) * 2;
+  static_assert(kTurnBytes <= kDirectLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
 };
 using TilesLarge = Tiles<256, 256, 2, 4>;
 using TilesSmall = Tiles<128, 128, 2, 2>;
@@ -589,7 +591,9 @@ struct Tile {
 // then has the matrix core to itself.
 // DIRECT: the operands' rows may start anywhere, and take the way through the
 // registers: two steps on their way there, and two stages of LDS.
-template <class TL, bool AK, bool BK_, bool GATED, class OP, bool RAGGED = false, bool DIRECT = false>
+// SINGLE: for sums of one or two steps, where nothing can be loaded ahead: one
+// stage of LDS of either operand, so that more workgroups share a CU.
+template <class TL, bool AK, bool BK_, bool GATED, class OP, bool RAGGED = false, bool DIRECT = false, bool SINGLE = false>
 TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
   constexpr int BM = TL::BM, BN = TL::BN, BK = TL::BK, TM = TL::TM, TN = TL::TN, NT = TL::kThreads;
   constexpr int kCols = GATED ? BN / 2 : BN;   // output columns of a tile
@@ -692,7 +696,25 @@ TACO_DEV void sum_tile(const Epilogue& e, const Tile& t) {
       for (int i = 0; i < kPer; ++i)
         if (i / each == part) l.issue(s, wave, K - (int64_t)ks * BK, i);
     };
-    if (steps > 0) {
+    if constexpr (SINGLE) {
+#pragma unroll 1
+      for (int ks = 0; ks < steps; ++ks) {
+        if (ks > 0) hand_over<0, -1>();   // the stages are read to their end
+        load(la, ks, lds_a, 0, 1);
+        load(lb, ks, lds_a + TL::kA, 0, 1);
+        hand_over<0, 0>();
+        if (RAGGED && idle) continue;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          read_b(lds_a + TL::kA, kk);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            read_a(lds_a, kk, i);
+            multiply(kk, i);
+          }
+        }
+      }
+    } else if (steps > 0) {
       uint16_t *a0 = lds_a, *a1 = lds_a + TL::kA, *a2 = lds_a + 2 * TL::kA;   // of this step and the next two
       uint16_t *b0 = lds_b, *b1 = lds_b + TL::kB;
       load(la, 0, a0, 0, 1);

@@ -66,6 +66,9 @@ CASES = [
     Case(7, 3500, 264, 136), Case(2, 700, 1032, 1288, "some", 11, 5), Case(4, 6000, 520, 72, "some", 8, 8, 24, 16),
     Case(8, 8200, 1536, 72, "even"), Case(3, 9000, 1540, 136, "some", 4, 100), Case(9, 0, 24, 40, "even", 6, 7),
     Case(5, 4097, 1100, 80, "one", 1, 2, 5, 3),
+    # many tiles of dw with short sums; few tiles with a long K, forward and dx; 64 and 65 groups
+    Case(40, 300, 2060, 1544, "some", 3, 2), Case(3, 70, 136, 4104, "some"), Case(2, 100, 4100, 136, "some", 1, 0, 1),
+    Case(64, 3000, 136, 72), Case(65, 3000, 136, 72, "some", 1, 1), Case(3, 1600, 1000, 1001, "some", 0, 0, 2, 1),
 ]
 
 
