@@ -344,15 +344,14 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, G
 
 // ------------------------------------------- backward of activations, dbias --
 
-// dz, and the sums over ranges of 8 rows of one group each.
-constexpr int kRangeLog = 3;
+// dz, and the sums over ranges of 2^log rows of one group each.
 template <bool GATED>
-__global__ __launch_bounds__(256) void k_experts_act_back(ActBackArgs a, Groups gr, unsigned slabs, unsigned bound) {
-  const GroupTiles<kAllTiles> gt(gr, kRangeLog);
+__global__ __launch_bounds__(256) void k_experts_act_back(ActBackArgs a, Groups gr, int log, unsigned slabs, unsigned bound) {
+  const GroupTiles<kAllTiles> gt(gr, log);
   const unsigned range = blockIdx.x / slabs;
   Group g;
   if (range >= bound || !group_of_tile(gt, range, &g)) return;
-  const int64_t first = g.lo + ((int64_t)(range - g.before) << kRangeLog), end = first + (1 << kRangeLog);
+  const int64_t first = g.lo + ((int64_t)(range - g.before) << log), end = first + (int64_t(1) << log);
   act_back<GATED>(a, first, end < g.hi ? end : g.hi, range, blockIdx.x % slabs);
 }
 
@@ -363,10 +362,11 @@ struct DbiasArgs {
   int N;
   Mat dbias;        // p null: not wanted
   unsigned bound;   // ranges that there is room for
+  int log;          // of a range's rows
 };
 template <int WAVES>
 TACO_DEV void experts_dbias(const DbiasArgs& a, const Groups& gr, unsigned block, int g, float* sums) {
-  const GroupTiles<kAllTiles> gt(gr, kRangeLog);
+  const GroupTiles<kAllTiles> gt(gr, a.log);
   // ranges before the lane that has the group, and before it in that lane
   const int lane = g / gt.per;
   unsigned before = lane_value(gt.upto - gt.mine, lane);
@@ -421,8 +421,11 @@ template <class TL>
 static int64_t most_row_tiles(const Groups& g) {
   using TR = typename RestOf<TL>::Type;
   const int64_t used = std::min(g.count, g.rows);
+  if (TL::BM == TR::BM) return most_tiles(g, log2_of(TL::BM));
   return g.rows / TL::BM + std::min<int64_t>(TL::BM / TR::BM * used, most_tiles(g, log2_of(TR::BM)));
 }
+// A launch has fewer than 2^32 threads.
+static bool fits_launch(int64_t workgroups, int threads) { return workgroups * threads < int64_t(1) << 32; }
 
 // Which tiles the rows of groups take (dx, and forward products that are not of few rows).
 constexpr int kDirectRows = 512;
@@ -579,30 +582,39 @@ static void launch_dbias(const DbiasArgs& a, const Groups& g, hipStream_t s) {
   hipLaunchKernelGGL(k_experts_dbias, grid, dim3(256), 0, s, a, g);
 }
 
-int64_t experts_back_ranges(const Groups& g) { return most_tiles(g, kRangeLog); }
+// Rows of a range: eight, as in a dense layer's pass, or more where there would
+// be over 2048 ranges.
+static int range_log(const Groups& g) {
+  int log = 3;
+  while (g.rows >> log > 2048) ++log;
+  return log;
+}
+int64_t experts_back_ranges(const Groups& g) { return most_tiles(g, range_log(g)); }
 
 hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStream_t s) {
   const unsigned bound = (unsigned)experts_back_ranges(g), slabs = (unsigned)((a.N + 511) / 512);
-  if (bound > 0) hipLaunchKernelGGL((k_experts_act_back<false>), dim3(bound * slabs), dim3(256), 0, s, a, g, slabs, bound);
+  if (bound > 0) hipLaunchKernelGGL((k_experts_act_back<false>), dim3(bound * slabs), dim3(256), 0, s, a, g, range_log(g), slabs, bound);
   return hipGetLastError();
 }
 
 hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const float* sums, int64_t N, const Mat& dbias,
                                const Groups& g, int64_t b_rows, void* partials, hipStream_t s) {
-  const DbiasArgs db = {sums, (int)N, dbias, (unsigned)experts_back_ranges(g)};
+  const DbiasArgs db = {sums, (int)N, dbias, (unsigned)experts_back_ranges(g), range_log(g)};
   const bool large_dw = dw && dw_large(*dw, g);
   const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
   const bool short_dw = dw && !large_dw && dw_short(*dw, g);
-  if (dx && dw && !short_dw && (shape == kLarge) == large_dw) {
+  const ExpertsPlan p = dx ? dx_plan(g, dx->N, dx->K) : ExpertsPlan();
+  const unsigned count_dx = (unsigned)p.tiles * p.parts;
+  const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
+  const unsigned count_dw = !dw ? 0 : large_dw ? dw_grid<TilesLarge>(*dw, g) : dw_grid<TilesSmall>(*dw, g);
+  if (dx && dw && !short_dw && (shape == kLarge) == large_dw &&
+      fits_launch((int64_t)count_dx + count_dw + count_db, large_dw ? TilesLarge::kThreads : TilesSmall::kThreads)) {
     GemmArgs x = *dx;
-    const ExpertsPlan p = dx_plan(g, x.N, x.K);
     set_experts_plan(&x, p, partials);
     with_tiles(shape, [&](auto tiles) {
       using TLX = decltype(tiles);
       using TLW = std::conditional_t<TLX::BM == TilesLarge::BM, TilesLarge, TilesSmall>;
       auto launch = [&](auto direct) {
-        const unsigned count_dw = dw_grid<TLW>(*dw, g), count_dx = (unsigned)p.tiles * p.parts;
-        const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
         hipLaunchKernelGGL((k_experts_back<TLX, TLW, direct()>), dim3(count_dx + count_dw + count_db),
                            dim3(TLW::kThreads), TLW::kLdsBytes, s, x, *dw, db, g, b_rows, count_dx, count_dw);
       };

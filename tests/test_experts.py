@@ -68,6 +68,11 @@ CASES = [
     Case(5, 4097, 1100, 80, "one", 1, 2, 5, 3),
     # many tiles of dw with short sums; few tiles with a long K, forward and dx; 64 and 65 groups
     Case(40, 300, 2060, 1544, "some", 3, 2), Case(3, 70, 136, 4104, "some"), Case(2, 100, 4100, 136, "some", 1, 0, 1),
+    # K cut, in tiles of 64 and 128 rows, in place and not: forward, and dx
+    Case(2, 100, 136, 4104, "some"), Case(2, 300, 200, 4104, "some", 1, 1), Case(2, 90, 130, 4099, "some", 0, 2, 1, 1),
+    Case(2, 300, 200, 4101, "some", 0, 0, 1, 1), Case(2, 300, 4104, 136), Case(3, 60, 4104, 72), Case(2, 300, 4101, 130, pad=1),
+    # ranges of more than eight rows in dbias
+    Case(3, 40000, 24, 16, "some", 2, 9), Case(300, 36000, 17, 8),
     Case(64, 3000, 136, 72), Case(65, 3000, 136, 72, "some", 1, 1), Case(3, 1600, 1000, 1001, "some", 0, 0, 2, 1),
 ]
 
