@@ -501,7 +501,7 @@ def _codes(t, rows, cols, what):
 
 def taco_quantize_rows(x, q, scale, stream=None):
     """q (int8 [rows, cols]) and scale (float32 [rows]) of the rows of x: scale =
-    max |x| / 127, q = x * (127 / max |x|) to the nearest."""
+    max |x| / 127, q = x * ((1 / max |x|) * 127) to the nearest."""
     rows, cols = x.shape
     return _check(_lib.taco_quantize_rows(_matrix(x, rows, cols, "x"), rows, cols, _codes(q, rows, cols, "q"),
                                           _floats(scale, rows, "scale"), _stream(stream)), "taco_quantize_rows")

@@ -159,16 +159,17 @@ TACO_DEV unsigned lanes_max(unsigned v) {
   return v;
 }
 
-// A row's scale A / 127 and what its elements are multiplied by, 127 / A: the
-// codec INT8_SYM's. Rows below kTiny are zeros; rows with an infinity or NaN
-// have that as their scale, and codes of zero.
+// A row's scale A / 127 and what its elements are multiplied by, (1 / A) 127 in
+// two roundings, as a program that has the reciprocals makes it; each is at most
+// 2^-23 off. Rows below kTiny are zeros; rows with an infinity or NaN have that
+// as their scale, and codes of zero.
 struct RowScale {
   float scale, inv;
   TACO_DEV explicit RowScale(unsigned bits) {
     const float largest = __builtin_bit_cast(float, bits);
     const bool finite = bits < 0x7F800000u, zero = finite && largest < kTiny;
     scale = zero ? 0.0f : finite ? largest / 127.0f : largest;
-    inv = finite && !zero ? 127.0f / largest : 0.0f;
+    inv = finite && !zero ? 1.0f / largest * 127.0f : 0.0f;
   }
   // |x inv| is below 127.5, so the codes need no clamp
   TACO_DEV int code(float x) const { return inv == 0.0f ? 0 : rne_int(x * inv); }

@@ -58,7 +58,7 @@ def quantized(x):
         finite = np.isfinite(largest)
         zero = finite & (largest < np.float32(2.0 ** -100))
         scale = np.where(zero, np.float32(0), np.where(finite, largest / np.float32(127), largest)).astype(np.float32)
-        inv = np.where(finite & ~zero, np.float32(127) / largest, np.float32(0)).astype(np.float32)
+        inv = np.where(finite & ~zero, np.float32(1) / largest * np.float32(127), np.float32(0)).astype(np.float32)
         q = np.rint((np.where(inv[:, None] == 0, np.float32(0), v) * inv[:, None]).astype(np.float32))
     return q.astype(np.int8), scale
 
