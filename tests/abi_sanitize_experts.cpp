@@ -78,12 +78,14 @@ static void limits() {
   EXPECT(taco_linear_int8_workspace_bytes(64, 64, TACO_INT8_MAX_K + 1), 0);
   EXPECT(taco_gated_linear_int8_workspace_bytes(INT64_C(1) << 30, 16, 32) > 0, 1);
   EXPECT(taco_gated_linear_int8_workspace_bytes((INT64_C(1) << 30) + 1, 1, 1), 0);
-  EXPECT(taco_grouped_linear_workspace_bytes(1024, 32768, dim, 32) > 0, 1);
+  EXPECT(taco_grouped_linear_workspace_bytes(1024, 32768, dim, 32), 0);   // taken from where it lies
+  EXPECT(taco_grouped_linear_workspace_bytes(32, INT64_C(1) << 25, 1024, 1024) > 0, 1);
   EXPECT(taco_grouped_linear_workspace_bytes(1024, 32768, dim, 33), 0);
-  EXPECT(taco_grouped_gated_linear_workspace_bytes(1024, 32768, dim / 2, 32) > 0, 1);
+  EXPECT(taco_grouped_gated_linear_workspace_bytes(1024, 32768, dim / 2, 32), 0);
+  EXPECT(taco_grouped_gated_linear_workspace_bytes(32, INT64_C(1) << 25, 512, 1024) > 0, 1);
   EXPECT(taco_grouped_linear_backward_workspace_bytes(1024, INT64_C(1) << 30, 32, 32) > 0, 1);
   EXPECT(taco_grouped_gated_linear_backward_workspace_bytes(1024, INT64_C(1) << 30, 16, 32) > 0, 1);
-  EXPECT(taco_grouped_linear_backward_workspace_bytes(1, 0, 8, 8) > 0, 1);
+  EXPECT(taco_grouped_linear_backward_workspace_bytes(1, 4, 8, 8) > 0, 1);
 }
 
 int main() {
