@@ -62,15 +62,17 @@ def test_products_hand_over_what_they_count(assembly):
             loops = list(main_loops(body[:body.index(".Lfunc_end")].splitlines()))
             # dw reads both operands transposed; forward products neither
             gradient = name == "k_experts" and flags[0]
-            direct = name != "k_experts_dw" and flags[-1]     # by way of the registers: nothing is counted but dw's
+            # by way of the registers (the first of the gradients' two flags): nothing is counted but dw's
+            direct = name != "k_experts_dw" and flags[0 if name == "k_experts_back" else -1]
+            few = name == "k_experts_back" and flags[1]       # and there dw's is not either
             dw = [name != "k_experts" and not any(i.startswith("ds_read_b128") for i in l) for l in loops]
             rest = [REST[t[0]] if name in ("k_experts", "k_experts_back") else None for t in tiles[:1]]
             if direct:
                 loops = [l for l, is_dw in zip(loops, dw) if is_dw]
                 dw = [True] * len(loops)
-            expect = {"k_int8": 1, "k_experts_dw": 1, "k_experts": 2, "k_experts_back": 3}[name]
+            expect = {"k_int8": 1, "k_experts_dw": 1, "k_experts": 2, "k_experts_back": 3}[name] - few
             expect -= {"k_int8": 1, "k_experts": 2, "k_experts_back": 2}[name] if direct else 0
-            assert len(loops) == expect and sum(dw) == (name in ("k_experts_dw", "k_experts_back")), symbol
+            assert len(loops) == expect and sum(dw) == (name in ("k_experts_dw", "k_experts_back")) - few, symbol
             for loop, is_dw in zip(loops, dw):
                 # which tile it is of: full ones, those of the rows left (half as high), or dw's
                 products = sum(i.startswith("v_mfma") for i in loop)
