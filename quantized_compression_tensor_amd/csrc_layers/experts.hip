@@ -417,7 +417,15 @@ static int64_t most_tiles(const Groups& g, int log) {
   return (g.rows + used * ((int64_t(1) << log) - 1)) >> log;
 }
 
-bool few_rows_experts(const Groups& g, int64_t, int64_t, bool) { return g.rows <= kFewRows; }
+// Whether a forward product takes the kernel for few rows, which reads a group's
+// rows again for every 16 of its columns, or tiles. In us, that kernel and tiles:
+// gated 2 x 1024 x 2048, 8 rows over 64 groups 16.0 and 17.7, 16 rows over 8 13.4
+// and 16.0, 32 rows over 64 39.2 and 30.6; 4096 x 4096, 3 groups, 4 rows 10.0 and
+// 13.6, 8 groups, 8 rows 36.0 and 31.8, 32 rows 57.5 and 41.2; 520 x 1000, 8 groups,
+// 32 rows 8.6 and 12.3.
+bool few_rows_experts(const Groups& g, int64_t n, int64_t k, bool gated) {
+  return g.rows <= 4 || (g.rows <= kFewRows && g.rows * (gated ? 2 : 1) * n * k <= int64_t(1) << 26);
+}
 
 // Row tiles of k_experts at most: full ones, and those of the rows left.
 template <class TL>
@@ -430,8 +438,10 @@ static int64_t most_row_tiles(const Groups& g) {
 // A launch has fewer than 2^32 threads.
 static bool fits_launch(int64_t workgroups, int threads) { return workgroups * threads < int64_t(1) << 32; }
 
-// Which tiles the rows of groups take (dx, and forward products that are not of few rows).
-constexpr int kDirectRows = 512;
+// Which tiles the rows of groups take (dx, and forward products that are not of
+// few rows). Large ones where they fill the device and most groups have a whole
+// one or two: 8 groups of 2 x 4096 x 4096, 256 rows to a group 170 us, in small tiles
+// 214 (350 rows 238 and 274; 175 rows 172 either way).
 enum Shape { kFlat, kTall, kSmall, kLarge };
 static Shape shape_of(const Groups& g, int64_t wide) {
   const int64_t rows = g.rows / g.count;
@@ -440,9 +450,22 @@ static Shape shape_of(const Groups& g, int64_t wide) {
   return rows >= 256 && g.rows * wide >= int64_t(192) << 16 ? kLarge : kSmall;
 }
 
+// The same for a forward product of `ntn` columns of small tiles. More than one
+// small tile to a CU: low tiles would read the weights of groups that have more
+// rows than they hold in two rounds (8 groups of 2 x 2816 x 4096, 32, 48 and 64
+// rows to a group 92, 99 and 94 us in flat or tall tiles, 78, 82 and 82 in small
+// ones; but of 4096 x 4096, 256 small tiles, 48 and 64 rows 59 and 56, and 67 and 70).
+static Shape forward_shape(const Groups& g, int64_t wide, int64_t ntn) {
+  const Shape shape = shape_of(g, wide);
+  if (shape == kLarge || g.rows / g.count < 32) return shape;
+  return std::min(g.count, g.rows) * ntn > 256 ? kSmall : shape;
+}
+
 // Whether weights of another alignment are taken as they are, not copied: they
-// are read about as often as the groups' rows fill tiles.
-// (Lines below 16 bytes are not taken.)
+// are read about as often as the groups' rows fill tiles. 8 groups of 2 x 2816 x
+// 4097, 256 rows to a group 252 us, copied 336; of 1000 x 1001, 512 rows 33.1 and
+// 30.6. (Lines below 16 bytes are not taken.)
+constexpr int kDirectRows = 512;
 bool direct_experts(const Groups& g, int64_t wide) {
   return wide >= 8 && shape_of(g, wide) != kLarge && g.rows / g.count <= kDirectRows;
 }
@@ -468,8 +491,8 @@ struct ExpertsPlan {
   size_t bytes;         // of partial sums
 };
 // `other`: us of the tiles of another product that run at the same time.
-static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gated, double other = 0.0) {
-  ExpertsPlan p = {shape_of(g, gated ? 2 * N : N), 0, 1, K, 0};
+static ExpertsPlan plan_of(const Groups& g, Shape shape, int64_t N, int64_t K, bool gated, double other) {
+  ExpertsPlan p = {shape, 0, 1, K, 0};
   with_tiles(p.shape, [&](auto tiles) {
     using TL = decltype(tiles);
     const int64_t cols = gated ? TL::BN / 2 : TL::BN, ntn = (N + cols - 1) / cols, steps = (K + 63) / 64;
@@ -494,6 +517,17 @@ static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gate
   });
   return p;
 }
+static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gated) {
+  const int64_t wide = gated ? 2 * N : N;
+  return plan_of(g, forward_shape(g, wide, (wide + TilesSmall::BN - 1) / TilesSmall::BN), N, K, gated, 0.0);
+}
+// dx alone, and beside dw [wide, N] of every group, whose small tiles take about
+// 5 us besides their steps.
+static ExpertsPlan dx_plan(const Groups& g, int64_t N, int64_t wide, bool beside) {
+  const double steps = (double)(g.rows / g.count) / 64.0;
+  const double other = (double)(((wide + 127) / 128) * ((N + 127) / 128) * g.count) * (5.0 + 0.6 * steps);
+  return plan_of(g, shape_of(g, N), N, wide, false, beside ? other : 0.0);
+}
 static void set_experts_plan(GemmArgs* a, const ExpertsPlan& p, void* partials) {
   a->parts = p.parts;
   a->part = p.part;
@@ -504,15 +538,8 @@ size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated) 
   return g.rows == 0 ? 0 : experts_plan(g, N, K, gated).bytes;
 }
 
-// dx beside dw [wide, N] of every group, whose small tiles take about 5 us
-// besides their steps.
-static ExpertsPlan dx_plan(const Groups& g, int64_t N, int64_t wide) {
-  const double steps = (double)(g.rows / g.count) / 64.0;
-  return experts_plan(g, N, wide, false,
-                      (double)(((wide + 127) / 128) * ((N + 127) / 128) * g.count) * (5.0 + 0.6 * steps));
-}
 size_t experts_back_bytes(const Groups& g, int64_t N, int64_t wide) {
-  return g.rows == 0 ? 0 : std::max(experts_plan(g, N, wide, false).bytes, dx_plan(g, N, wide).bytes);
+  return g.rows == 0 ? 0 : std::max(dx_plan(g, N, wide, false).bytes, dx_plan(g, N, wide, true).bytes);
 }
 
 template <class TL>
@@ -540,7 +567,7 @@ hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows,
     else few(std::true_type());
     return hipGetLastError();
   }
-  const ExpertsPlan p = experts_plan(g, a.N, a.K, a.gated);
+  const ExpertsPlan p = a.b.by_k ? dx_plan(g, a.N, a.K, false) : experts_plan(g, a.N, a.K, a.gated);
   set_experts_plan(&a, p, partials);
   with_tiles(p.shape, [&](auto tiles) {
     using TL = decltype(tiles);
@@ -606,7 +633,7 @@ hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const flo
   const bool large_dw = dw && dw_large(*dw, g);
   const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
   const bool short_dw = dw && !large_dw && dw_short(*dw, g);
-  const ExpertsPlan p = dx ? dx_plan(g, dx->N, dx->K) : ExpertsPlan();
+  const ExpertsPlan p = dx ? dx_plan(g, dx->N, dx->K, true) : ExpertsPlan();
   const unsigned count_dx = (unsigned)p.tiles * p.parts;
   const unsigned count_db = dbias.p ? (unsigned)((N + kWave - 1) / kWave) * (unsigned)g.count : 0;
   const unsigned count_dw = !dw ? 0 : large_dw ? dw_grid<TilesLarge>(*dw, g) : dw_grid<TilesSmall>(*dw, g);
