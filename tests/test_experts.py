@@ -74,6 +74,9 @@ CASES = [
     # ranges of more than eight rows in dbias
     Case(3, 40000, 24, 16, "some", 2, 9), Case(300, 36000, 17, 8),
     Case(64, 3000, 136, 72), Case(65, 3000, 136, 72, "some", 1, 1), Case(3, 1600, 1000, 1001, "some", 0, 0, 2, 1),
+    # 32 to 64 rows to a group and many tiles, in place and not; up to 32 rows times many weights
+    Case(20, 1000, 1800, 136, "some", 2, 3), Case(20, 900, 1800, 137, "even", 1, 0, 1, 1),
+    Case(9, 32, 1540, 1544, "some", 1, 2), Case(9, 30, 1541, 1543, "some", 0, 1, 2, 1), Case(32, 32, 1540, 1544, "even"),
 ]
 
 
@@ -367,6 +370,34 @@ def test_offsets_out_of_range_or_decreasing():
     o = offsets.clamp(0, M).tolist()
     for g in range(G):
         assert torch.equal(out.t[o[g]:o[g + 1]].double(), x[o[g]:o[g + 1]].double() @ w[g].double().t())
+
+
+@pytest.mark.parametrize("rows,N,K", [(20, 40, 72), (100, 136, 200), (400, 264, 136), (900, 264, 130), (3000, 520, 264)])
+def test_a_groups_nan_stays_in_it(rows, N, K):
+    """Rows of NaN and infinities at the ends of one group leave the others' bits."""
+    gen = generator(rows)
+    G = 4
+    o = [0, rows // 3, rows // 3 + rows // 4 + 1, rows // 2 + rows // 3, rows]
+    offsets = torch.tensor(o, dtype=torch.int32, device=DEV)
+    x, d, w = matrix(gen, rows, K, BF), matrix(gen, rows, N, BF), whole3(gen, G, N, K, 2)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[o[1]], x[o[2] - 1], d[o[1]], d[o[2] - 1] = math.nan, math.inf, -math.inf, math.nan
+        out, dx, dw, db = (torch.zeros(*s, device=DEV) for s in ((rows, N), (rows, K), (G, N, K), (G, N)))
+        T.taco_grouped_linear(x, w, offsets, out, workspace=space(T.taco_grouped_linear_workspace_bytes(G, rows, N, K)))
+        T.taco_grouped_linear_backward(d, x, w, offsets, dx=dx, dw=dw, dbias=db,
+                                       workspace=space(T.taco_grouped_linear_backward_workspace_bytes(G, rows, N, K)))
+        outs.append((out, dx, dw, db))
+    torch.cuda.synchronize()
+    live = torch.ones(rows, dtype=torch.bool, device=DEV)
+    live[[o[1], o[2] - 1]] = False
+    others = [0, 2, 3]
+    for i, (was, now) in enumerate(zip(*outs)):
+        part = live if i < 2 else others
+        assert torch.equal(was[part], now[part]) and not bool(torch.isnan(now[part]).any())
+        rest = now[~live] if i < 2 else now[1]
+        assert not bool(torch.isfinite(rest).any()) if i != 1 else bool((~torch.isfinite(rest)).any())
 
 
 def test_no_rows():
