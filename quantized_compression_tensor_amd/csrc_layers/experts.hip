@@ -503,7 +503,7 @@ struct ExpertsPlan {
   size_t bytes;         // of partial sums
 };
 // `other`: us of the tiles of another product that run at the same time.
-static ExpertsPlan plan_of(const Groups& g, Shape shape, int64_t N, int64_t K, bool gated, double other) {
+static ExpertsPlan plan_of(const Groups& g, Shape shape, int64_t N, int64_t K, bool gated, bool direct, double other) {
   ExpertsPlan p = {shape, 0, 1, K, 0};
   with_tiles(p.shape, [&](auto tiles) {
     using TL = decltype(tiles);
@@ -512,8 +512,10 @@ static ExpertsPlan plan_of(const Groups& g, Shape shape, int64_t N, int64_t K, b
     if (p.shape == kLarge) return;
     // about as many tiles as there will be: every group with rows has some left
     const double tiles_now = (double)((g.rows / TL::BM + std::min(g.count, g.rows)) * ntn);
-    // two tiles to a CU, a step of either 0.6 us; the parts' way through memory at 4 TB/s, and a launch
-    const double tile_us = 2.0 * TL::BM * TL::BN * sizeof(float) / 4e6, step = 0.6, launch = 4.0;
+    // two tiles to a CU, a step of either 0.6 us, by way of the registers 0.65 to 1.2; the parts' way
+    // through memory at 4 TB/s, and a launch
+    const double tile_us = 2.0 * TL::BM * TL::BN * sizeof(float) / 4e6, launch = 4.0;
+    const double step = !direct ? 0.6 : TL::BM == TilesFlat::BM ? 0.65 : TL::BM == TilesTall::BM ? 0.9 : 1.2;
     double least = 0.0;
     for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
       const int64_t per = (steps + parts - 1) / parts;
@@ -529,16 +531,16 @@ static ExpertsPlan plan_of(const Groups& g, Shape shape, int64_t N, int64_t K, b
   });
   return p;
 }
-static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gated) {
+static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gated, bool direct) {
   const int64_t wide = gated ? 2 * N : N;
-  return plan_of(g, forward_shape(g, wide, (wide + TilesSmall::BN - 1) / TilesSmall::BN), N, K, gated, 0.0);
+  return plan_of(g, forward_shape(g, wide, (wide + TilesSmall::BN - 1) / TilesSmall::BN), N, K, gated, direct, 0.0);
 }
 // dx alone, and beside dw [wide, N] of every group, whose small tiles take about
 // 5 us besides their steps.
 static ExpertsPlan dx_plan(const Groups& g, int64_t N, int64_t wide, bool beside) {
   const double steps = (double)(g.rows / g.count) / 64.0;
   const double other = (double)(((wide + 127) / 128) * ((N + 127) / 128) * g.count) * (5.0 + 0.6 * steps);
-  return plan_of(g, shape_of(g, N), N, wide, false, beside ? other : 0.0);
+  return plan_of(g, shape_of(g, N), N, wide, false, false, beside ? other : 0.0);
 }
 static void set_experts_plan(GemmArgs* a, const ExpertsPlan& p, void* partials) {
   a->parts = p.parts;
@@ -546,8 +548,8 @@ static void set_experts_plan(GemmArgs* a, const ExpertsPlan& p, void* partials) 
   a->rest = (unsigned)p.tiles;
   a->partials = static_cast<float*>(partials);
 }
-size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated) {
-  return g.rows == 0 ? 0 : experts_plan(g, N, K, gated).bytes;
+size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated, bool direct) {
+  return g.rows == 0 ? 0 : experts_plan(g, N, K, gated, direct).bytes;
 }
 
 size_t experts_back_bytes(const Groups& g, int64_t N, int64_t wide) {
@@ -579,7 +581,7 @@ hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows,
     else few(std::true_type());
     return hipGetLastError();
   }
-  const ExpertsPlan p = a.b.by_k ? dx_plan(g, a.N, a.K, false) : experts_plan(g, a.N, a.K, a.gated);
+  const ExpertsPlan p = a.b.by_k ? dx_plan(g, a.N, a.K, false) : experts_plan(g, a.N, a.K, a.gated, a.direct);
   set_experts_plan(&a, p, partials);
   with_tiles(p.shape, [&](auto tiles) {
     using TL = decltype(tiles);

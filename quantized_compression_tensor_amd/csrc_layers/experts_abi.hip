@@ -42,7 +42,12 @@ struct GroupedForward {
     g.b = packed(w.m, groups.count * wide, k, false, any || (!worst && in_place(w.m, k)), space, &pack);
     g.direct = any && !(in_place(x.m, k) && in_place(w.m, k));
     g.M = m; g.N = (int)n; g.K = k; g.gated = gated; g.e = e;
-    void* partials = space->take(few_rows_experts(groups, n, k, gated) ? 0 : experts_partial_bytes(groups, n, k, gated));
+    size_t sums = 0;
+    if (!few_rows_experts(groups, n, k, gated)) {
+      if (worst || g.direct) sums = any ? experts_partial_bytes(groups, n, k, gated, true) : 0;
+      if (worst || !g.direct) sums = std::max(sums, experts_partial_bytes(groups, n, k, gated, false));
+    }
+    void* partials = space->take(sums);
     if (what != kRun) return hipSuccess;
     if (pack.count > 0) {
       const hipError_t err = launch_pack(pack, stream);

@@ -171,7 +171,7 @@ struct Groups {
 };
 // Products by group: rows of a with the group's part of b (`b_rows` rows of it);
 // a.M is not looked at. partials: experts_partial_bytes.
-size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated);
+size_t experts_partial_bytes(const Groups& g, int64_t N, int64_t K, bool gated, bool direct);
 hipError_t launch_experts(const GemmArgs& a, const Groups& g, int64_t b_rows, void* partials, hipStream_t s);
 // Whether the forward product takes the kernel for few rows.
 bool few_rows_experts(const Groups& g, int64_t N, int64_t K, bool gated);

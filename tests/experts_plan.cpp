@@ -15,7 +15,7 @@ int main() {
   while (scanf("%lld %lld %lld %lld", &groups, &m, &n, &k) == 4) {
     const taco::Groups g = {nullptr, (int)groups, (int)m};
     for (int dx = 0; dx < 2; ++dx) {
-      const taco::ExpertsPlan p = dx ? taco::dx_plan(g, n, k, true) : taco::experts_plan(g, n, k, false);
+      const taco::ExpertsPlan p = dx ? taco::dx_plan(g, n, k, true) : taco::experts_plan(g, n, k, false, false);
       int height = 0, threads = 0;
       taco::with_tiles(p.shape, [&](auto tiles) {
         height = decltype(tiles)::BM;
