@@ -41,11 +41,11 @@ static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
 
 // Products whose operands are not aligned take them from where they lie
 // (DIRECT), in tiles of 32 or 64 rows, or copies of them in the other tiles,
-// whichever a model of either's time says is less. In us: a step of the direct
-// tiles, of which a CU holds one or two; parts of K, as in linear.hip's plan; a
-// copy at 4 TB/s and its launch. 100 rows, 3 bytes off, by 4096 x 4096 19.4 us,
-// copied 22.1; 200 by 8192 x 1024 12.5 and 19.2; 200 by 4096 x 4096 25.5 and
-// 24.4; 300 by 1000 x 1280 13.3 and 14.7.
+// whichever a model of their times says is least. In us: a step of the direct
+// tiles, of which a CU holds one; parts of K, as in linear.hip's plan; a copy at
+// 4 TB/s and its launch. Tiles of 32 and of 64 rows, 3 bytes off: 200 rows by 4096
+// x 4096 20.6 and 27.2, 301 by 1001 x 1285 12.1 and 14.7; but 100 by 4096 x 4096 21.9
+// and 17.9 (copied 22.1).
 struct Int8Plan {
   int height;               // of a tile
   unsigned tiles, parts;    // parts of K
@@ -53,21 +53,18 @@ struct Int8Plan {
   double us;
 };
 static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
-  Int8Plan p = {M <= TilesFlat::BM ? TilesFlat::BM : TilesTall::BM, 0, 1, 0, 0.0};
+  Int8Plan p = {0, 0, 1, 0, 0.0};
   const int64_t cols = gated ? 64 : 128, steps = (K + 127) / 128;
-  const int64_t tiles = (M + p.height - 1) / p.height * ((N + cols - 1) / cols);
-  const double step = 0.85, part_us = 2.0 * p.height * 128 * sizeof(float) / 4e6;
-  for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
-    const int64_t per = (steps + parts - 1) / parts;
-    const double rounds = std::max(1.0, (double)(tiles * parts) / 384.0);
-    const double us = rounds * (double)per * step + (parts > 1 ? 5.0 + (double)(tiles * parts) * part_us : 0.0);
-    if (parts == 1 || us < p.us) {
-      p.parts = (unsigned)((steps + per - 1) / per);
-      p.part = per * 64;
-      p.us = us;
+  for (const int height : {TilesFlat::BM, TilesTall::BM}) {
+    const int64_t tiles = (M + height - 1) / height * ((N + cols - 1) / cols);
+    const double step = height == TilesFlat::BM ? 0.65 : 0.85, part_us = 2.0 * height * 128 * sizeof(float) / 4e6;
+    for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
+      const int64_t per = (steps + parts - 1) / parts;
+      const double rounds = std::max(1.0, (double)(tiles * parts) / 256.0);
+      const double us = rounds * (double)per * step + (parts > 1 ? 5.0 + (double)(tiles * parts) * part_us : 0.0);
+      if (p.height == 0 || us < p.us) p = {height, (unsigned)tiles, (unsigned)((steps + per - 1) / per), per * 64, us};
     }
   }
-  p.tiles = (unsigned)tiles;
   return p;
 }
 bool direct_int8(int64_t M, int64_t N, int64_t K, bool gated) {
