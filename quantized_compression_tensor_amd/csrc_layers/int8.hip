@@ -45,7 +45,8 @@ static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
 // tiles, of which a CU holds one; parts of K, as in linear.hip's plan; a copy at
 // 4 TB/s and its launch. Tiles of 32 and of 64 rows, 3 bytes off: 200 rows by 4096
 // x 4096 20.6 and 27.2, 301 by 1001 x 1285 12.1 and 14.7; but 100 by 4096 x 4096 21.9
-// and 17.9 (copied 22.1).
+// and 17.9 (copied 22.1). 8000 by 129 x 777 15.1, copied 19.4; 1000 by 6000 x 511
+// 26.5 and 20.4.
 struct Int8Plan {
   int height;               // of a tile
   unsigned tiles, parts;    // parts of K
@@ -60,7 +61,7 @@ static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
     const double step = height == TilesFlat::BM ? 0.65 : 0.85, part_us = 2.0 * height * 128 * sizeof(float) / 4e6;
     for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min<int64_t>(steps / 4, 16)); ++parts) {
       const int64_t per = (steps + parts - 1) / parts;
-      const double rounds = std::max(1.0, (double)(tiles * parts) / 256.0);
+      const double rounds = (double)((tiles * parts + 255) / 256);
       const double us = rounds * (double)per * step + (parts > 1 ? 5.0 + (double)(tiles * parts) * part_us : 0.0);
       if (p.height == 0 || us < p.us) p = {height, (unsigned)tiles, (unsigned)((steps + per - 1) / per), per * 64, us};
     }
@@ -68,9 +69,10 @@ static Int8Plan int8_plan(int64_t M, int64_t N, int64_t K, bool gated) {
   return p;
 }
 bool direct_int8(int64_t M, int64_t N, int64_t K, bool gated) {
-  if (M > 1024) return false;
+  const Int8Plan p = int8_plan(M, N, K, gated);
   const double copy = 3.5 + 2.0 * (double)((M + (gated ? 2 * N : N)) * K) / 4e6;
-  return int8_plan(M, N, K, gated).us < copy + gemm_plan_us(M, N, (K + 1) / 2, gated);
+  // (a launch has fewer than 2^32 threads)
+  return (int64_t)p.tiles * p.parts < int64_t(1) << 20 && p.us < copy + gemm_plan_us(M, N, (K + 1) / 2, gated);
 }
 size_t direct_int8_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
   const Int8Plan p = int8_plan(M, N, K, gated);

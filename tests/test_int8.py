@@ -109,6 +109,10 @@ def test_quantize_rows_of_special_values():
 
 # ----------------------------------------------------------------- exactly --
 
+# many rows of any alignment, in tiles of 32 or 64 rows and in copies
+SIZES += [(2000, 777, 1001, 0, 0), (8000, 129, 300, 3, 1), (1500, 260, 2001, 0, 0), (1100, 2000, 259, 0, 0)]
+
+
 @pytest.mark.parametrize("size", SIZES, ids=ids)
 def test_linear_exact(size):
     M, N, K, pad, offset = size
