@@ -156,9 +156,10 @@ hipError_t launch_pack_int8(const PackArgs& a, hipStream_t s) {
 // in the order of the values, with infinity and then NaN above all others.
 TACO_DEV unsigned magnitude(float f) { return __builtin_bit_cast(unsigned, f) & 0x7FFFFFFFu; }
 
+template <int LANES>
 TACO_DEV unsigned lanes_max(unsigned v) {
 #pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
+  for (int d = 1; d < LANES; d *= 2) {
     const unsigned o = (unsigned)__shfl_xor((int)v, d, kWave);
     v = o > v ? o : v;
   }
@@ -190,15 +191,19 @@ constexpr int kQuantizeSteps = 4;   // eights of a row that a lane holds
 // A row is held by `waves` waves, four eights to a lane at most; where it is
 // longer (SECOND) its parts are read again for the codes. Bound by memory: 8192 x
 // 8192 bf16 32.0 us on the device (6.3 TB/s), 38.6 in a stream of calls over three
-// inputs, which the caches do not hold (5.2 TB/s, a copy's rate).
-template <int DT, bool SECOND>
+// inputs, which the caches do not hold (5.2 TB/s, a copy's rate). Narrow rows are
+// held by LANES lanes of a wave, or most of it would have nothing to do (64767 x
+// 205 bf16 51.0 us with a wave to a row, 11.7; 30000 x 500 25.0 and 11.7).
+template <int DT, bool SECOND, int LANES>
 __global__ __launch_bounds__(1024) void k_quantize(QuantizeArgs a, int waves) {
   __shared__ unsigned largest[2][16];   // used in turn, so that one barrier a row is enough
-  const int wave = wave_in_group(), size = waves * kWave, first_wave = wave / waves * waves;
-  const int lane = (int)threadIdx.x - first_wave * kWave, rows_at_once = (int)blockDim.x / size;
+  static_assert(LANES == kWave || !SECOND, "a narrow row is read once");
+  const int wave = wave_in_group(), size = LANES < kWave ? LANES : waves * kWave, first_wave = wave / waves * waves;
+  const int lane = LANES < kWave ? (int)threadIdx.x % LANES : (int)threadIdx.x - first_wave * kWave;
+  const int rows_at_once = (int)blockDim.x / size;
   int turn = 0;
   for (int64_t block = (int64_t)blockIdx.x * rows_at_once; block < a.rows; block += (int64_t)gridDim.x * rows_at_once) {
-    const int64_t row = block + wave / waves;
+    const int64_t row = block + (LANES < kWave ? (int)threadIdx.x / LANES : wave / waves);
     const bool live = row < a.rows;
     const char* x = static_cast<const char*>(a.x.p) + (live ? row : 0) * a.x.ld * (DT == kBF16 ? 2 : 4);
     char* q = static_cast<char*>(a.q.p) + (live ? row : 0) * a.q.ld;
@@ -233,8 +238,8 @@ __global__ __launch_bounds__(1024) void k_quantize(QuantizeArgs a, int waves) {
         look();
       }
     }
-    m = lanes_max(m);
-    if (waves > 1) {
+    m = lanes_max<LANES>(m);
+    if (LANES == kWave && waves > 1) {
       if (lane % kWave == 0) largest[turn][wave] = m;
       __syncthreads();
       for (int w = 0; w < waves; ++w) m = largest[turn][first_wave + w] > m ? largest[turn][first_wave + w] : m;
@@ -275,15 +280,18 @@ hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s) {
   int waves = 1;
   while (waves < 16 && (int64_t)waves * kWave * kQuantizeSteps < octs) waves *= 2;
   const bool second = (int64_t)waves * kWave * kQuantizeSteps < octs;
-  const int per = std::max(1, 4 / waves);
-  const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 16)), block((unsigned)(per * waves * kWave));
-  if (a.x.dt == kBF16) {
-    if (second) hipLaunchKernelGGL((k_quantize<kBF16, true>), grid, block, 0, s, a, waves);
-    else hipLaunchKernelGGL((k_quantize<kBF16, false>), grid, block, 0, s, a, waves);
-  } else {
-    if (second) hipLaunchKernelGGL((k_quantize<kF32, true>), grid, block, 0, s, a, waves);
-    else hipLaunchKernelGGL((k_quantize<kF32, false>), grid, block, 0, s, a, waves);
-  }
+  const int lanes = octs <= 8 * kQuantizeSteps ? 8 : octs <= 16 * kQuantizeSteps ? 16 : waves * kWave;
+  const int per = std::max(1, 256 / lanes);
+  const dim3 grid((unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 16)), block((unsigned)(per * lanes));
+  auto launch = [&](auto dt) {
+    constexpr int DT = dt();
+    if (lanes == 8) hipLaunchKernelGGL((k_quantize<DT, false, 8>), grid, block, 0, s, a, waves);
+    else if (lanes == 16) hipLaunchKernelGGL((k_quantize<DT, false, 16>), grid, block, 0, s, a, waves);
+    else if (second) hipLaunchKernelGGL((k_quantize<DT, true, kWave>), grid, block, 0, s, a, waves);
+    else hipLaunchKernelGGL((k_quantize<DT, false, kWave>), grid, block, 0, s, a, waves);
+  };
+  if (a.x.dt == kBF16) launch(std::integral_constant<int, kBF16>());
+  else launch(std::integral_constant<int, kF32>());
   return hipGetLastError();
 }
 

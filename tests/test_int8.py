@@ -79,7 +79,8 @@ def check_quantized(x, pad=0, offset=0):
 @pytest.mark.parametrize("rows,cols,pad,offset", [
     (1, 1, 0, 0), (3, 7, 1, 1), (5, 8, 0, 0), (129, 9, 3, 2), (1, 5120, 0, 0), (64, 511, 0, 0), (7, 512, 8, 8),
     (3, 2048, 0, 0), (5, 2049, 3, 1), (6, 4096, 0, 0), (4, 4100, 0, 3), (3, 8192, 0, 0), (3, 8200, 0, 0),
-    (2, 16384, 0, 0), (2, 16391, 1, 1), (3, 32768, 0, 0), (2, 32769, 0, 0), (2, 70001, 3, 5), (70000, 24, 0, 0)])
+    (2, 16384, 0, 0), (2, 16391, 1, 1), (3, 32768, 0, 0), (2, 32769, 0, 0), (2, 70001, 3, 5), (70000, 24, 0, 0),
+    (33, 255, 1, 1), (31, 256, 0, 0), (65, 257, 3, 1), (17, 512, 8, 0), (15, 513, 0, 1), (1000, 205, 0, 0)])
 def test_quantize_rows(rows, cols, pad, offset, dtype):
     gen = generator(rows + cols)
     x = matrix(gen, rows, cols, dtype, pad, offset, sigma=3.0)
@@ -92,6 +93,7 @@ def test_quantize_more_rows_than_workgroups():
     x = matrix(generator(5), (1 << 16) * 4 + 13, 3, BF)
     check_quantized(x)
     check_quantized(matrix(generator(6), (1 << 16) + 5, 2056, BF, 8))
+    check_quantized(matrix(generator(7), (1 << 16) * 32 + 13, 3, BF))
 
 
 def test_quantize_rows_of_special_values():
