@@ -39,6 +39,10 @@ def linear(gated=False, M=4, N=16, K=24, x=None, xs=at(5), w=None, ws=at(6), bia
     return T.lib().taco_linear_int8(x, xs, w, ws, bias or NONE, act, residual or NONE, out, M, N, K, space, bytes_, None)
 
 
+# a long K, cut into parts whose sums need a workspace
+CUT = dict(M=100, K=4112, x=arr(0, 4112, C), w=arr(1, 4112, C))
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("want,kw", [
     (T.TACO_OK, dict(M=0)), (T.TACO_OK, dict(M=0, x=NONE, out=NONE, xs=None)), (INVALID, dict(M=0, ws=None)),
@@ -50,8 +54,8 @@ def linear(gated=False, M=4, N=16, K=24, x=None, xs=at(5), w=None, ws=at(6), bia
     (INVALID, dict(x=NONE)), (INVALID, dict(w=NONE)), (INVALID, dict(out=NONE)), (INVALID, dict(xs=None)),
     (INVALID, dict(ws=None)), (ALIGN, dict(xs=at(5) + 2)), (ALIGN, dict(ws=at(6) + 1)), (ALIGN, dict(out=arr(2, 16, B, 1))),
     (INVALID, dict(out=arr(0, 24))), (INVALID, dict(out=arr(5, 16))), (INVALID, dict(out=arr(6, 16, F, 60))),
-    (WORKSPACE, dict(M=2000, space=None)), (WORKSPACE, dict(M=2000, bytes_=100)), (WORKSPACE, dict(M=2000, space=at(9) + 8)),
-    (INVALID, dict(M=2000, out=arr(9, 16))), (INVALID, dict(M=2000, space=at(0))), (INVALID, dict(M=2000, space=at(5))),
+    (WORKSPACE, dict(CUT, space=None)), (WORKSPACE, dict(CUT, bytes_=100)), (WORKSPACE, dict(CUT, space=at(9) + 8)),
+    (INVALID, dict(CUT, out=arr(9, 16))), (INVALID, dict(CUT, space=at(0))), (INVALID, dict(CUT, space=at(5))),
 ])
 def test_int8_refusals(gated, want, kw):
     assert linear(gated, **kw) == want
@@ -147,7 +151,7 @@ def test_workspaces():
         size = getattr(T, f"taco_{n}_workspace_bytes")
         for refused in ((-1, 8, 8), (8, 0, 8), (8, 8, 0), (8, 8, 131072)):
             assert size(*refused) == 0
-        assert size(1, 4096, 4096) == 0 and size(2000, 20, 20) > 0
+        assert size(1, 4096, 4096) == 0 and size(100, 16, 4112) > 0
 
 
 def fake(shape, where, dtype=torch.bfloat16):
