@@ -462,6 +462,16 @@ static Shape shape_of(const Groups& g, int64_t wide) {
   return rows >= 256 && g.rows * wide >= int64_t(192) << 16 ? kLarge : kSmall;
 }
 
+// The same for dx of N columns. A group of a few more rows than a tall tile's
+// half leaves two low tiles beside its full ones, and of the largest sizes these
+// would be more than a launch has threads (1024 groups of 33 rows, 1016800 columns:
+// 5.2e9); small tiles are few enough at every size.
+static Shape dx_shape(const Groups& g, int64_t N) {
+  const Shape shape = shape_of(g, N);
+  const int64_t ntn = (N + TilesTall::BN - 1) / TilesTall::BN;
+  return shape == kTall && !fits_launch(most_row_tiles<TilesTall>(g) * ntn, TilesTall::kThreads) ? kSmall : shape;
+}
+
 // The same for a forward product of `ntn` columns of small tiles. More than one
 // small tile to a CU: low tiles would read the weights of groups that have more
 // rows than they hold in two rounds (8 groups of 2 x 2816 x 4096, 32, 48 and 64
@@ -540,7 +550,7 @@ static ExpertsPlan experts_plan(const Groups& g, int64_t N, int64_t K, bool gate
 static ExpertsPlan dx_plan(const Groups& g, int64_t N, int64_t wide, bool beside) {
   const double steps = (double)(g.rows / g.count) / 64.0;
   const double other = (double)(((wide + 127) / 128) * ((N + 127) / 128) * g.count) * (5.0 + 0.6 * steps);
-  return plan_of(g, shape_of(g, N), N, wide, false, false, beside ? other : 0.0);
+  return plan_of(g, dx_shape(g, N), N, wide, false, false, beside ? other : 0.0);
 }
 static void set_experts_plan(GemmArgs* a, const ExpertsPlan& p, void* partials) {
   a->parts = p.parts;
@@ -647,7 +657,7 @@ hipError_t launch_experts_back(const GemmArgs* dx, const GemmArgs* dw, const flo
                                const Groups& g, int64_t b_rows, void* partials, hipStream_t s) {
   const DbiasArgs db = {sums, (int)N, dbias, (unsigned)experts_back_ranges(g), range_log(g)};
   const bool large_dw = dw && dw_large(*dw, g);
-  const Shape shape = dx ? shape_of(g, dx->N) : kFlat;
+  const Shape shape = dx ? dx_shape(g, dx->N) : kFlat;
   const bool short_dw = dw && !large_dw && dw_short(*dw, g);
   const ExpertsPlan p = dx ? dx_plan(g, dx->N, dx->K, true) : ExpertsPlan();
   const unsigned count_dx = (unsigned)p.tiles * p.parts;

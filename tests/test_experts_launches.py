@@ -1,0 +1,77 @@
+"""The launches that calls of the products by group make, without a GPU: the
+entry points and plans as they are, with a recorder in place of the launch (see
+experts_launches.cpp). At every size that the entry points accept, a launch stays
+below 2^32 threads along each axis and within a CU's LDS."""
+
+import os
+import subprocess
+
+import pytest
+
+from tests.conftest import ROOT
+from tests.test_layers_large import HIPCC
+
+CALLS = ("linear", "gated", "linear-dx", "linear-dw", "linear-both", "linear-db", "linear-all", "gated-dx", "gated-dw",
+         "gated-both")
+MOST = 1 << 35          # elements of a tensor
+DIM = 1 << 20           # of N, 2 F and K
+
+
+@pytest.fixture(scope="session")
+def launches(tmp_path_factory):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not installed")
+    import importlib.util
+    spec = importlib.util.spec_from_file_location(
+        "taco_build", os.path.join(ROOT, "quantized_compression_tensor_amd", "build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    exe = str(tmp_path_factory.mktemp("launches") / "experts_launches")
+    flags = [f for f in build.FLAGS if f != "-O3"]
+    b = subprocess.run([HIPCC, *flags, "-O1", "-x", "hip", f"-I{build.CSRC}",
+                        os.path.join(ROOT, "tests", "experts_launches.cpp"), "-o", exe],
+                       capture_output=True, text=True, timeout=900)
+    assert b.returncode == 0, b.stderr[-3000:]
+
+    def ask(lines):
+        """Of each (call, groups, M, N, K, offset): the status, and (kernel, grid x, grid y, threads, LDS) of its launches."""
+        text = "".join(" ".join(map(str, line)) + "\n" for line in lines)
+        r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0
+        out = [line.split("\t") for line in r.stdout.splitlines()]
+        assert len(out) == len(lines)
+        return [(int(o[0]), [(p.split("|")[0], *map(int, p.split("|")[1:])) for p in o[1:]]) for o in out]
+    return ask
+
+
+def sizes():
+    """The largest N for each number of groups and rows to a group, and the largest K for that N; and the other way round."""
+    for groups in (1, 7, 33, 64, 65, 512, 777, 1000, 1024):
+        for per in (1, 4, 5, 31, 32, 33, 34, 40, 63, 64, 65, 66, 127, 128, 129, 255, 256, 257, 300, 4096, 1 << 20):
+            for rows in {per * groups, per * groups + groups - 1}:
+                if rows > 1 << 30:
+                    continue
+                for most in {min(DIM, MOST // rows), min(DIM, MOST // rows) // 2 + 1}:
+                    other = min(DIM, MOST // (groups * most), MOST // rows)
+                    for less in {other, min(other, 64), 1}:
+                        if less > 0:
+                            yield groups, rows, most, less
+                            yield groups, rows, less, most
+
+
+def test_launches_at_the_largest_sizes(launches):
+    lines = [(call, groups, rows, max(1, n // (2 if call.startswith("gated") else 1)), k, offset)
+             for groups, rows, n, k in sizes() for call in CALLS for offset in (0, 1)]
+    # dx of 33 to 64 rows to a group, in tall tiles: more threads than a launch has
+    lines += [(call, 1024, rows, 32, k, 0) for rows, k in ((33792, 1016800), (40960, 838860))
+              for call in ("linear-dx", "linear-all")]
+    accepted = 0
+    for line, (status, all_) in zip(lines, launches(lines)):
+        # (the largest tensors with their rows further apart than their columns are too large)
+        assert status == 0 or line[-1] > 0, line
+        accepted += status == 0
+        assert all_ or status, line
+        for kernel, x, y, threads, lds in all_:
+            if kernel.startswith("k_"):
+                assert 0 < x and x * threads < 1 << 32 and 0 < y < 1 << 16 and lds <= 160 * 1024, (line, kernel, x, y)
+    assert accepted > len(lines) // 2
