@@ -420,10 +420,13 @@ int taco_gated_linear_backward(taco_array dout, taco_array x, taco_array w, int3
 size_t taco_gated_linear_backward_workspace_bytes(int64_t M, int64_t F, int64_t K);
 
 /* ---- projections in 8-bit integers -----------------------------------------
- * Rows to symmetric codes of 8 bits with one scale each, as INT8_SYM has them for
- * its blocks: with A = max |x| of the row,
+ * Rows to symmetric codes of 8 bits with one scale each: with A = max |x| of the
+ * row,
  *   scale = A / 127,  q = x * ((1 / A) * 127) to the nearest, ties to even
- * in float32, each step rounded once (codes lie in [-127, 127]). A below
+ * in float32, each step rounded once (codes lie in [-127, 127]). INT8_SYM has the
+ * same scale for a block, but multiplies by 127 / A rounded once: where
+ * x * 127 / A is within float32's roundings of a half, a code may be one off the
+ * code that INT8_SYM has (normal bf16 rows of 64: 4 in 10000). A below
  * 2^-100: codes 0 and scale 0. A row with an infinity or NaN: codes 0 and that
  * as its scale, so products with it are NaN. Serves tokens and, row by row of a
  * linear layer's weight, output channels.

@@ -167,9 +167,11 @@ TACO_DEV unsigned lanes_max(unsigned v) {
 }
 
 // A row's scale A / 127 and what its elements are multiplied by, (1 / A) 127 in
-// two roundings, as a program that has the reciprocals makes it; each is at most
-// 2^-23 off. Rows below kTiny are zeros; rows with an infinity or NaN have that
-// as their scale, and codes of zero.
+// two roundings, as a program that has the reciprocals makes it (the codec
+// INT8_SYM has 127 / A in one: codes next to a half may be one apart). The scale is
+// at most 2^-24 of its value off, the multiplier 2^-23 up to A = 2^126 and 2^-21.6
+// above, where 1 / A is subnormal (2^-22, and one rounding). Rows below kTiny are
+// zeros; rows with an infinity or NaN have that as their scale, and codes of zero.
 struct RowScale {
   float scale, inv;
   TACO_DEV explicit RowScale(unsigned bits) {
@@ -178,7 +180,7 @@ struct RowScale {
     scale = zero ? 0.0f : finite ? largest / 127.0f : largest;
     inv = finite && !zero ? 1.0f / largest * 127.0f : 0.0f;
   }
-  // |x inv| is below 127.5, so the codes need no clamp
+  // |x inv| is at most 127 (1 + 2^-21), below 127.5, so the codes need no clamp
   TACO_DEV int code(float x) const { return inv == 0.0f ? 0 : rne_int(x * inv); }
 };
 TACO_DEV unsigned four_codes(const float* f, const RowScale& s) {
