@@ -65,20 +65,27 @@ class ExpertsSublayer:
         self.dgamma, self.dbeta = new(hidden, dtype=F32), new(hidden, dtype=F32)
         self.shard = [T.empty_compressed(self.codec, tokens, hidden, device) for _ in range(ranks)]
         self.gathered = T.empty_compressed(self.codec, tokens, hidden, device)
-        sizes = [T.taco_grouped_gated_linear_workspace_bytes(experts, rows, self.f, hidden),
-                 T.taco_grouped_linear_workspace_bytes(experts, rows, hidden, self.f),
-                 T.taco_grouped_linear_backward_workspace_bytes(experts, rows, hidden, self.f),
-                 T.taco_grouped_gated_linear_backward_workspace_bytes(experts, rows, self.f, hidden),
-                 T.taco_layer_norm_backward_workspace_bytes(tokens, hidden)]
         if self.shared:
             s = self.shared
             self.s_in = [codes(normal(2 * s, hidden, scale=hidden ** -0.5)) for _ in range(ranks)]
             self.s_out = [codes(normal(hidden, s, scale=shared ** -0.5)) for _ in range(ranks)]
             self.nq, self.ns = new(tokens, hidden, dtype=torch.int8), new(tokens, dtype=F32)
             self.sh, self.hq, self.hs = new(tokens, s), new(tokens, s, dtype=torch.int8), new(tokens, dtype=F32)
+        # (a step of fewer tokens can need more: where tiles are few, their sums are cut into parts)
+        self.ws = new(max(self.workspace_bytes(t) for t in range(1, tokens + 1)), dtype=torch.uint8)
+
+    def workspace_bytes(self, tokens):
+        """The most that a call of a step of that many tokens needs."""
+        rows, hidden, experts, f, s = tokens * self.top, self.hidden, self.experts, self.f, self.shared
+        sizes = [T.taco_grouped_gated_linear_workspace_bytes(experts, rows, f, hidden),
+                 T.taco_grouped_linear_workspace_bytes(experts, rows, hidden, f),
+                 T.taco_grouped_linear_backward_workspace_bytes(experts, rows, hidden, f),
+                 T.taco_grouped_gated_linear_backward_workspace_bytes(experts, rows, f, hidden),
+                 T.taco_layer_norm_backward_workspace_bytes(tokens, hidden)]
+        if s:
             sizes += [T.taco_gated_linear_int8_workspace_bytes(tokens, s, hidden),
                       T.taco_linear_int8_workspace_bytes(tokens, hidden, s)]
-        self.ws = new(max(sizes), dtype=torch.uint8)
+        return max(sizes)
 
     def route(self, x):
         """The norm, and the tokens' rows sorted by expert: their token, their weight and each expert's first row."""

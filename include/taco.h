@@ -321,7 +321,10 @@ int taco_decompress_gemm(taco_codec c, const void* a, int64_t M, int64_t K, cons
  * 2^35 elements, a missing array or an output that overlaps an input or another
  * output; TACO_ERR_ALIGN; TACO_ERR_WORKSPACE for a workspace that is missing, smaller
  * than the call needs or not 16-byte aligned. The function's *_workspace_bytes
- * is enough for arrays of any alignment and all outputs. Workspaces are
+ * is enough for arrays of any alignment and all outputs, of the sizes asked for.
+ * It can be larger for fewer rows (a projection of few tiles has its sums cut
+ * into parts), so a workspace for calls of up to M rows is as large as the
+ * largest of those sizes. Workspaces are
  * scratch: nothing is kept in them between calls, they need no clearing, and
  * calls that may run at the same time need one each. Results do not depend on
  * timing: the same call gives the same bits. Inputs may hold infinities and
