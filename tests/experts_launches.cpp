@@ -7,19 +7,25 @@
 // "kernel|grid x|grid y|threads of a workgroup|bytes of LDS", on one line. The entry points
 // and their plans are the library's own; the arrays are addresses that nothing
 // reads, and a workspace is as large as its *_workspace_bytes says.
+#include <cxxabi.h>
 #include <hip/hip_runtime.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <string>
+#include <typeinfo>
 
 static std::string launches;
 template <auto K>
+struct Name {};
+template <auto K>
 static void record(dim3 grid, dim3 block, size_t lds) {
-  std::string name = __PRETTY_FUNCTION__;
-  name = name.substr(name.find("K = ") + 4);
+  char* text = abi::__cxa_demangle(typeid(Name<K>).name(), nullptr, nullptr, nullptr);
+  std::string name = text;
+  free(text);
   name = name.substr(name.find("k_"));
-  name.resize(name.size() - 1);
+  name = name.substr(0, name.find('('));   // without its arguments
   char sizes[96];
   snprintf(sizes, sizeof(sizes), "|%u|%u|%u|%zu", grid.x, grid.y, block.x, lds);
   launches += "\t" + name + sizes;

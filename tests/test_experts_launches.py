@@ -75,3 +75,38 @@ def test_launches_at_the_largest_sizes(launches):
             if kernel.startswith("k_"):
                 assert 0 < x and x * threads < 1 << 32 and 0 < y < 1 << 16 and lds <= 160 * 1024, (line, kernel, x, y)
     assert accepted > len(lines) // 2
+
+
+def test_every_kernel_is_run_by_a_test(launches):
+    """The kernels (with their tiles) that calls of any sizes take are those that
+    the cases of test_experts.py and test_experts_gradients.py take."""
+    import random
+
+    from tests.test_experts import CASES, REAL
+    from tests.test_experts_gradients import LARGE, ONE_BY_ONE, half
+
+    def line(call, c):
+        return call, c.G, c.M, c.N, c.K, int(bool(c.pad or c.offset))
+
+    def kernels(lines):
+        return {k for _, all_ in launches(lines) for k, *_ in all_}
+
+    cases = [line(call, c) for c in CASES + REAL if c.M for call in ("linear", "gated", "linear-all", "gated-both")]
+    cases += [line(call, c) for c in ONE_BY_ONE for call in ("linear-dx", "linear-dw", "linear-db", "linear-both")]
+    cases += [line(call, half(c)) for c in ONE_BY_ONE for call in ("gated-dx", "gated-dw", "gated-both")]
+    cases += [line("linear-all", c) for c in LARGE]
+    rng, lines = random.Random(3), []
+    for _ in range(100000):
+        groups, rows, n, k = rng.choice([1, 2, 3, 8, 16, 40, 64, 65, 300]), *(int(2 ** rng.uniform(0, e)) for e in (18, 14, 14))
+        offset = rng.randint(0, 1)
+        if not offset:
+            n, k = -(-n // 8) * 8, -(-k // 8) * 8
+        lines.append((rng.choice(CALLS), groups, rows, n, k, offset))
+    assert kernels(lines) <= kernels(cases), kernels(lines) - kernels(cases)
+    large = "taco::Tiles<256, 256, 2, 4>"
+    both = f"k_experts_back<{large}, {large}, false, false>"
+    took = [{k for k, *_ in all_} for _, all_ in launches([line("linear-all", c) for c in LARGE])]
+    assert [both in t for t in took] == [True] * 5 + [False] * 4
+    for t in took[5:7] + took[8:]:      # of dw alone
+        assert any(k.startswith(f"k_experts_dw<{large}") for k in t)
+    assert f"k_experts<{large}, true, false, false>" in took[7]
