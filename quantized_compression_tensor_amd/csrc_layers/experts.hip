@@ -354,15 +354,15 @@ __global__ __launch_bounds__(kFewWaves * kWave) void k_experts_few(GemmArgs a, G
 
 // ------------------------------------------- backward of activations, dbias --
 
-// dz, and the sums over ranges of 2^log rows of one group each.
-template <bool GATED>
+// dz, and the sums over ranges of 2^log rows of one group each (a gated layer has
+// no bias: its dz comes from k_act_back).
 __global__ __launch_bounds__(256) void k_experts_act_back(ActBackArgs a, Groups gr, int log, unsigned slabs, unsigned bound) {
   const GroupTiles<kAllTiles> gt(gr, log);
   const unsigned range = blockIdx.x / slabs;
   Group g;
   if (range >= bound || !group_of_tile(gt, range, &g)) return;
   const int64_t first = g.lo + ((int64_t)(range - g.before) << log), end = first + (int64_t(1) << log);
-  act_back<GATED>(a, first, end < g.hi ? end : g.hi, range, blockIdx.x % slabs);
+  act_back<false>(a, first, end < g.hi ? end : g.hi, range, blockIdx.x % slabs);
 }
 
 // Group g's sums of those, in order; zeros for a group without rows. `block`
@@ -568,11 +568,13 @@ size_t experts_back_bytes(const Groups& g, int64_t N, int64_t wide) {
 
 template <class TL>
 static void launch_experts_join(const GemmArgs& a, const Groups& g, hipStream_t s) {
-  if (a.parts <= 1) return;
-  const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
-  const dim3 grid(a.rest, (unsigned)((TL::BM + rows - 1) / rows));
-  if (a.gated) hipLaunchKernelGGL((k_experts_join<TL, true>), grid, dim3(256), 0, s, a, g);
-  else hipLaunchKernelGGL((k_experts_join<TL, false>), grid, dim3(256), 0, s, a, g);
+  if constexpr (TL::BM < TilesLarge::BM) {   // (large tiles take all of K)
+    if (a.parts <= 1) return;
+    const int octs = (a.gated ? TL::BN / 2 : TL::BN) / 8, rows = 256 / octs;
+    const dim3 grid(a.rest, (unsigned)((TL::BM + rows - 1) / rows));
+    if (a.gated) hipLaunchKernelGGL((k_experts_join<TL, true>), grid, dim3(256), 0, s, a, g);
+    else hipLaunchKernelGGL((k_experts_join<TL, false>), grid, dim3(256), 0, s, a, g);
+  }
 }
 
 hipError_t launch_experts(const GemmArgs& args, const Groups& g, int64_t b_rows, void* partials, hipStream_t s) {
@@ -649,7 +651,7 @@ int64_t experts_back_ranges(const Groups& g) { return most_tiles(g, range_log(g)
 
 hipError_t launch_experts_act_back(const ActBackArgs& a, const Groups& g, hipStream_t s) {
   const unsigned bound = (unsigned)experts_back_ranges(g), slabs = (unsigned)((a.N + 511) / 512);
-  if (bound > 0) hipLaunchKernelGGL((k_experts_act_back<false>), dim3(bound * slabs), dim3(256), 0, s, a, g, range_log(g), slabs, bound);
+  if (bound > 0) hipLaunchKernelGGL(k_experts_act_back, dim3(bound * slabs), dim3(256), 0, s, a, g, range_log(g), slabs, bound);
   return hipGetLastError();
 }
 
