@@ -42,8 +42,10 @@ static void launch_tiles_int8(const GemmArgs& a, hipStream_t s) {
 // Products whose operands are not aligned take them from where they lie
 // (DIRECT), in tiles of 32 or 64 rows, or copies of them in the other tiles,
 // whichever a model of their times says is least. In us: a step of the direct
-// tiles, of which a CU holds one; parts of K, as in linear.hip's plan; a copy at
-// 4 TB/s and its launch. Tiles of 32 and of 64 rows, 3 bytes off: 200 rows by 4096
+// tiles, in rounds of 256; parts of K, as in linear.hip's plan; a copy at 4 TB/s
+// and its launch. (A CU holds four of the tiles of 32 rows, 40 KB of LDS and 110
+// registers each, and three of 64, so more than 256 take less than their rounds
+// say: of those, copies are taken a little early.) Tiles of 32 and of 64 rows, 3 bytes off: 200 rows by 4096
 // x 4096 20.6 and 27.2, 301 by 1001 x 1285 12.1 and 14.7; but 100 by 4096 x 4096 21.9
 // and 17.9 (copied 22.1). 8000 by 129 x 777 15.1, copied 19.4; 1000 by 6000 x 511
 // 26.5 and 20.4.

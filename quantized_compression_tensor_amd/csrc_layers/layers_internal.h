@@ -95,7 +95,8 @@ struct GemmArgs {
   int64_t K;
   bool gated;
   Epilogue e;
-  // set by launch_gemm: the first `whole` tiles take all of K; K is cut into
+  // set by a product's launch (launch_gemm, launch_gemm_pair, launch_gemm_int8,
+  // launch_experts and launch_experts_back): the first `whole` tiles take all of K; K is cut into
   // `parts` parts of `part` (a multiple of 64) for the `rest` others, whose
   // sums go to partials [parts][rest] tiles in float32
   unsigned whole, rest, parts;
@@ -141,7 +142,8 @@ hipError_t launch_gemm_pair(GemmArgs dx, GemmArgs dw, const ColumnSumArgs& sum, 
 hipError_t launch_act_back(const ActBackArgs& a, const PackArgs& p, hipStream_t s);   // and launch_pack's work
 void launch_column_sum(const ColumnSumArgs& a, hipStream_t s);
 
-// Rows to codes of 8 bits, q[r, c] = x[r, c] / scale[r] rounded.
+// Rows to codes of 8 bits, q[r, c] = x[r, c] ((1 / A) 127) rounded, and
+// scale[r] = A / 127, with A the largest magnitude of row r.
 struct QuantizeArgs {
   Mat x, q;
   int64_t rows, cols;

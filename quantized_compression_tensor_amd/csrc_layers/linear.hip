@@ -1006,13 +1006,13 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
 
 // --------------------------------------------------------------- few rows --
 
-// Up to 32 rows of x: the weight's bytes bound it, so every weight is read
-// once, straight into the registers of a 16 x 16 x 32 product whose other
+// Up to 32 rows of x (64 of codes): the weight's bytes bound it, so every weight
+// is read once, straight into the registers of a 16 x 16 x 32 product whose other
 // operand is x (rows past the last one repeat it; their sums are not stored).
 // A workgroup takes up to 16 weight rows (gated: eight of each projection; as
 // many as give every CU the same number of workgroups), its sixteen waves units
-// of 64 k in turn, so that a row's bytes are read 2 KiB at a time, two units of
-// a wave together. The waves' sums are joined in LDS. Rows may start anywhere.
+// of 64 k (128 codes) in turn, so that a row's bytes are read 2 KiB at a time, two
+// units of a wave together (more than 32 rows: one, whose x fills the registers). The waves' sums are joined in LDS. Rows may start anywhere.
 // One row, 8192 x 8192 weights: 27.6 us, 4.9 TB/s (eight waves with eight units
 // each 31.8 us); 4096 x 4096: 7.6 us. With 24 rows the reads of x, which every
 // workgroup makes, are more than those of the weights: 24 x 5120 into 2 x 1728
