@@ -9,7 +9,7 @@
 // token's whole product.
 // Few rows to a group: bound by the weights' bytes (one token of eight experts out
 // of 64, gated 2 x 1024 x 2048, 15.2 us, 67 MB at 4.4 TB/s); many: by the matrix cores
-// (8192 rows over 8 groups of 2 x 4096 x 4096, both projections kept, 510 to 523 us,
+// (8192 rows over 8 groups of 2 x 4096 x 4096, both projections kept, 510 to 535 us,
 // 1050 TFLOP/s of the rows' own products; profiled 518 us, busy 0.60 of the time at
 // 1.89 GHz. The rows left in tiles cost 0.05 of the work, a tile's first loads and
 // its stores, beside which nothing runs, 0.1).
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(256) void k_experts_dbias(DbiasArgs a, Groups gr) {
 // All gradients in one launch: dx's `count_dx` workgroups, dw's `count_dw`, and
 // the biases'. dx's sums are the longer ones as a rule, so dw's tiles fill
 // what dx leaves of the device at its end (8192 rows over 8 groups of 2 x 4096 x
-// 4096 1073 to 1102 us with the activation's 64; as two launches 1126; large and small
+// 4096 1073 to 1133 us with the activation's 64; as two launches 1126; large and small
 // groups' tiles of dw in turn instead of the largest first 1273). FEW: few rows to a group, dw's sums
 // are short (SINGLE) and dx takes the way with less LDS (DIRECT), so that three
 // workgroups share a CU: 2000 rows over 32 groups of 520 x 1000 42.3 us with two,

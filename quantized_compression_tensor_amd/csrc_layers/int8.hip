@@ -10,10 +10,10 @@
 // same 16 bytes of a lane, so a product of codes is one of 16-bit elements with
 // half the K to everything but the matrix instruction and the epilogue: tiles,
 // stages of LDS, waits and plans are those of linear.hip.
-// Measured in streams of calls: 8192^3 with bias and residual 431 to 443 us (2500
+// Measured in streams of calls: 8192^3 with bias and residual 431 to 456 us (2500
 // TOP/s; the library's product of codes, without an epilogue, 515), bound by the
 // matrix cores at the clock that power leaves (profiled 449 us, busy 0.67 of the
-// time at 1.89 GHz); gated 4096 x 5120 x 5120 190 to 194 (2.2 PTOP/s, busy 0.64 at 2.1
+// time at 1.89 GHz); gated 4096 x 5120 x 5120 190 to 198 (2.2 PTOP/s, busy 0.64 at 2.1
 // GHz). One row, 4096 x 4096: 8.0 us, 6.6 of them on the device; 24 rows, gated 2 x
 // 1728 x 5120: 8.7. Large tiles that stay on their CU and load the next one's first
 // steps during an epilogue were slower (8192^3 457 to 477 us).
