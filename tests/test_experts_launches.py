@@ -110,3 +110,42 @@ def test_every_kernel_is_run_by_a_test(launches):
     for t in took[5:7] + took[8:]:      # of dw alone
         assert any(k.startswith(f"k_experts_dw<{large}") for k in t)
     assert f"k_experts<{large}, true, false, false>" in took[7]
+
+
+def test_tiles_are_enough_for_any_rows(launches):
+    """The workgroups of a launch are enough for every distribution of the rows
+    over the groups: full tiles, and for the rows left tiles half as high (32 rows:
+    as high). Among them the worst: as many groups as there can be with one row
+    more than a half, or one."""
+    import random
+    import re
+    rng, lines = random.Random(8), []
+    for _ in range(400):
+        groups, per = rng.choice([1, 2, 3, 8, 33, 64, 100, 300]), rng.choice([5, 20, 33, 50, 64, 70, 200, 256, 300, 700])
+        rows = per * groups + rng.randrange(groups)
+        n, k = rng.choice([120, 520, 2056, 8200]), rng.choice([72, 264, 2056, 6000])
+        lines.append((rng.choice(["linear", "gated", "linear-dx", "gated-dx"]), groups, rows, n, k, rng.randint(0, 1)))
+    seen = set()
+    for (call, groups, rows, n, k, _), (status, all_) in zip(lines, launches(lines)):
+        assert status == 0
+        tiles = {kernel.split("<")[0]: (kernel, x) for kernel, x, *_ in all_}
+        if "k_experts" not in tiles:      # few rows: a workgroup takes all of a group's
+            continue
+        kernel, workgroups = tiles["k_experts"]
+        have = tiles["k_experts_join"][1] if "k_experts_join" in tiles else workgroups      # (K cut: parts of each)
+        height, width = map(int, re.search(r"Tiles<(\d+), (\d+)", kernel).groups())
+        columns = -(-k // width) if call.endswith("-dx") else -(-n // (width // 2 if call == "gated" else width))
+        low = max(32, height // 2)
+        seen.add((height, call.endswith("-dx")))
+        ways = [[rows // groups + (g < rows % groups) for g in range(groups)], [rows] + [0] * (groups - 1)]
+        for least in (1, low + 1, height + 1, height + low + 1):
+            used = min(groups, rows // least)
+            ways.append([least] * used + [rows - least * used] if used < groups else [least] * (used - 1) + [rows - least * (used - 1)])
+        for _ in range(20):
+            cuts = sorted(rng.choice([0, rows, rng.randint(0, rows)]) for _ in range(groups - 1))
+            ways.append([b - a for a, b in zip([0] + cuts, cuts + [rows])])
+        for way in ways:
+            assert sum(way) == rows and len([s for s in way if s]) <= groups
+            need = sum(s // height + -(-(s % height) // low) for s in way) * columns
+            assert need <= have, (call, groups, rows, n, k, kernel, way)
+    assert seen == {(h, dx) for h in (32, 64, 128, 256) for dx in (False, True)}
