@@ -96,9 +96,9 @@ struct GemmArgs {
   bool gated;
   Epilogue e;
   // set by a product's launch (launch_gemm, launch_gemm_pair, launch_gemm_int8,
-  // launch_experts and launch_experts_back): the first `whole` tiles take all of K; K is cut into
-  // `parts` parts of `part` (a multiple of 64) for the `rest` others, whose
-  // sums go to partials [parts][rest] tiles in float32
+  // launch_experts, launch_experts_back): the first `whole` tiles take all of K;
+  // K is cut into `parts` parts of `part` (a multiple of 64) for the `rest`
+  // others, whose sums go to partials [parts][rest] tiles in float32
   unsigned whole, rest, parts;
   int64_t part;
   float* partials;
